@@ -2,7 +2,8 @@
  * kv_codec.h -- C ABI of the KV-cache codec in the same library (libw4a16.so):
  * symmetric INT8 / INT4 quantization of attention keys per channel and of
  * values per token, their dequantization, and the flush of FP16 window blocks
- * into a pool of quantized blocks.
+ * into a pool of quantized blocks; and of the paged INT8 cache (kv_paged_*):
+ * rotating and appending new tokens, and attention over what it holds.
  *
  * Sources (cited by page title and section):
  *   [Guide] "27届大模型面试准备十九 模型量化全攻略 -- INT8/INT4、GPTQ、AWQ、
@@ -84,6 +85,110 @@ int kv_flush_blocks(const uint16_t *k, const uint16_t *v, int64_t blocks, int32_
                     int32_t d, int32_t bits, const int32_t *dst, int64_t pool_blocks,
                     int8_t *k_pool, float *k_scale, int8_t *v_pool, float *v_scale,
                     void *stream);
+
+/*
+ * The paged INT8 cache
+ * --------------------
+ * One layer's keys and values of many sequences.  A page holds `page`
+ * consecutive tokens of one sequence for one kv head, as int8 codes with one
+ * fp32 scale for K and one for V (scale and codes by the map above, taken over
+ * all page * d values: scale = max|x| / 127 floored at 1e-8, codes =
+ * clamp(rint(x / scale), -128, 127), each step one binary32 operation).  A
+ * page's scale needs all of its tokens, so the newest tokens stay in fp16: a
+ * slot per sequence holds its last two pages (the ring; page p of the sequence
+ * in half p % 2), a page that becomes full is quantized into the pool as well,
+ * and readers take the unfinished page from the ring.  Since the ring keeps
+ * two pages, a sequence can be shortened (drafted tokens taken back) by calling
+ * again with a smaller ctx_lens, as far back as the first token of the page
+ * before that of its last token.
+ *
+ * Both pools have the order in which the attention kernels read them: inside
+ * a page of one head, K is [page / 64][4][d / 16][16][16] -- token
+ * 64 i + 16 (m / 4) + 4 a + m % 4, channel 16 c + e at [i][a][c][m][e] -- and V
+ * is [page / 16][d][16], token 16 i + j at [i][channel][j].  Ring pages have the
+ * same order in fp16.
+ *
+ *  - page: 64, 128 or 256.  d: 64, 96, 128 or 256.  n_kv in [1, 1024], n_q a
+ *    multiple of n_kv, at most 1024; query head i reads kv head
+ *    i / (n_q / n_kv).
+ *  - Alignment: k, v, k_tail, v_tail, q, k, v of new tokens and out 16 bytes,
+ *    the rest 4 (the rotation table 16).
+ */
+typedef struct kv_paged_cache {
+    int8_t *k, *v;              /* [pages][n_kv][page * d], in the order above */
+    float *k_scale, *v_scale;   /* [pages][n_kv] */
+    uint16_t *k_tail, *v_tail;  /* fp16 [slots][2][n_kv][page * d] */
+    int64_t pages, slots;
+    int32_t n_kv, d, page;
+} kv_paged_cache;
+
+/*
+ * The sequences of one call: rows cu_q[b] .. cu_q[b + 1] - 1 of the new tokens
+ * (or queries) belong to sequence b, which holds ctx_lens[b] tokens before
+ * them; its page p is pool page block_table[b][p] and its ring is slots[b].
+ * Rows before cu_q[0] and from cu_q[batch] on (padding) belong to none.  All
+ * four arrays are int32 device arrays, read when the kernels run.  A sequence
+ * with ctx_lens[b] < 0, slots[b] outside [0, cache.slots) or more than
+ * table_cols full pages is skipped as if it had no rows.  cu_q must not
+ * decrease (a decreasing one gives unspecified, memory-safe results); two
+ * sequences of one call must not share a slot, nor a page that the call fills.
+ */
+typedef struct kv_paged_batch {
+    const int32_t *cu_q;         /* [batch + 1] */
+    const int32_t *ctx_lens;     /* [batch] */
+    const int32_t *block_table;  /* [batch][table_cols] */
+    const int32_t *slots;        /* [batch] */
+    int64_t tokens;              /* rows of the call */
+    int32_t batch, table_cols;
+} kv_paged_batch;
+
+/*
+ * Appends k and v (fp16 [tokens][n_kv][d], row strides in elements) behind
+ * each sequence's ctx_lens tokens.  With `rope`, k and q (fp16
+ * [tokens][n_q][d], optional) are rotated first: rope is fp32
+ * [rope_rows][rope_dim / 2][2], cosine and sine of pair j at a position;
+ * row r has position positions[r] (int32 device array, required with rope).
+ * Pair j is channels (j, j + rope_dim / 2), or (2 j, 2 j + 1) if `interleaved`;
+ * channels from rope_dim on are copied.  a' = a cos - b sin, b' = b cos + a sin
+ * in binary64, rounded once to fp16.  A position outside [0, rope_rows) gives
+ * NaN.  q_out is fp16 [tokens][n_q][d], contiguous; rows of no sequence are
+ * rotated as well.  Pages whose block_table entry is outside [0, pages) are
+ * not stored.  Strides: multiples of 8 (at least n_kv * d, n_q * d).
+ * rope_dim: a multiple of 32, at most d.  q NULL: n_q is not read.
+ */
+int kv_paged_append(const kv_paged_cache *cache, const kv_paged_batch *batch, const uint16_t *k, int64_t k_stride,
+                    const uint16_t *v, int64_t v_stride, const uint16_t *q, int64_t q_stride, int32_t n_q,
+                    const float *rope, int64_t rope_rows, int32_t rope_dim, int32_t interleaved,
+                    const int32_t *positions, uint16_t *q_out, void *stream);
+
+/*
+ * Pages ids[0 .. n) of the pool, dequantized in the order of tokens: k_out,
+ * v_out fp16 [n][n_kv][page][d] = fp16(code * scale).  Entries of ids outside
+ * [0, pages) are skipped (their outputs are not written).
+ */
+int kv_paged_read(const kv_paged_cache *cache, const int32_t *ids, int64_t n, uint16_t *k_out, uint16_t *v_out,
+                  void *stream);
+
+/* Workspace bytes of kv_paged_attention; no HIP call is made. */
+int64_t kv_paged_attention_workspace_size(int64_t tokens, int32_t batch, int32_t n_q, int32_t n_kv, int32_t d);
+
+/*
+ * Attention of q (fp16 [tokens][n_q][d], row stride in elements) over the
+ * cache, whose last tokens are the batch's own (append first): row i of a
+ * sequence stands at index ctx_lens[b] + i and sees the tokens j <= that
+ * index, with window > 0 only those with index - j < window and the first
+ * `sinks` tokens.  out fp16 [tokens][n_q][d], contiguous:
+ * softmax_j(scale * q . k_j) v, with sums and statistics in binary32, rounded
+ * once.  Pages whose block_table entry is outside [0, pages) are not visible
+ * (pages that no row sees are not looked up at all); a row that sees nothing
+ * gives zeros.  Rows of no sequence are left as they were.  `workspace`: device
+ * memory of at least kv_paged_attention_workspace_size bytes, 16-byte aligned,
+ * overwritten; calls sharing a workspace must not overlap.  Results are
+ * deterministic for given inputs and sizes.
+ */
+int kv_paged_attention(const kv_paged_cache *cache, const kv_paged_batch *batch, const uint16_t *q, int64_t q_stride,
+                       int32_t n_q, float scale, int32_t window, int32_t sinks, void *workspace,
+                       int64_t workspace_bytes, uint16_t *out, void *stream);
 
 #ifdef __cplusplus
 }

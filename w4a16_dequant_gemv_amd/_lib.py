@@ -9,12 +9,28 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("W4A16_LIB") or os.path.join(PKG, "libw4a16.so")
 
 Q4_OK, Q4_ERR_NULL, Q4_ERR_SHAPE, Q4_ERR_GROUP, Q4_ERR_ALIGN, Q4_ERR_HIP, Q4_ERR_CAPACITY = range(7)
-ABI_VERSION = 4
+ABI_VERSION = 5
 
 # Every symbol the public header declares, with its ctypes signature.
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+
+
+class PagedCache(ctypes.Structure):
+    """kv_paged_cache of kv_codec.h."""
+    _fields_ = ([(n, _p) for n in ("k", "v", "k_scale", "v_scale", "k_tail", "v_tail")]
+                + [("pages", _i64), ("slots", _i64), ("n_kv", _i32), ("d", _i32), ("page", _i32)])
+
+
+class PagedBatch(ctypes.Structure):
+    """kv_paged_batch of kv_codec.h."""
+    _fields_ = ([(n, _p) for n in ("cu_q", "ctx_lens", "block_table", "slots")]
+                + [("tokens", _i64), ("batch", _i32), ("table_cols", _i32)])
+
+
+_cache = ctypes.POINTER(PagedCache)
+_batch = ctypes.POINTER(PagedBatch)
 SIGNATURES = {
     "q4_abi_version": (ctypes.c_int, []),
     "q4_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -33,6 +49,11 @@ SIGNATURES = {
     "kv_dequant_tokens": (ctypes.c_int, [_p, _p, _i64, _i32, _p, _p]),
     "kv_dequant_channels": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _p, _p]),
     "kv_flush_blocks": (ctypes.c_int, [_p, _p, _i64, _i32, _i32, _i32, _p, _i64, _p, _p, _p, _p, _p]),
+    "kv_paged_append": (ctypes.c_int, [_cache, _batch, _p, _i64, _p, _i64, _p, _i64, _i32, _p, _i64, _i32, _i32, _p, _p,
+                                       _p]),
+    "kv_paged_read": (ctypes.c_int, [_cache, _p, _i64, _p, _p, _p]),
+    "kv_paged_attention_workspace_size": (_i64, [_i64, _i32, _i32, _i32, _i32]),
+    "kv_paged_attention": (ctypes.c_int, [_cache, _batch, _p, _i64, _i32, ctypes.c_float, _i32, _i32, _p, _i64, _p, _p]),
     "sq_absmax_update_f16": (ctypes.c_int, [_p, _i64, _i32, _p, _p]),
     "sq_absmax_update_f32": (ctypes.c_int, [_p, _i64, _i32, _p, _p]),
     "sq_smooth_factors": (ctypes.c_int, [_p, _p, _i32, ctypes.c_float, _p, _p]),

@@ -21,34 +21,12 @@
 // through LDS, and the codes are written from the registers, so the block is
 // read from HBM once.  The flush does both for one window block per
 // workgroup and writes to the pool slot the block table names.
-#include "q4_device.h"
+#include "kv_device.h"
 #include "q4_launch.h"
 
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float kv_scale(float amax, float qmax)
-{
-    float s = amax / qmax;
-    return s < 1e-8f ? 1e-8f : s;
-}
-
-// round(v / s) clamped to [-qmax - 1, qmax], as the byte of an int8.  The
-// product with r, the hardware reciprocal of s (within 1 ulp), is within
-// 2^-21.5 * |v / s| of the correctly rounded quotient; for |v / s| < 2^7 that
-// is below 2^-14, so both round to the same integer unless the product lies
-// within 2^-14 of a half-integer.  There, and for larger quotients, the
-// correctly rounded division decides: the code is the one round(v / s)
-// gives, bit for bit.
-__device__ __forceinline__ uint32_t kv_code(float v, float s, float r, float qmax)
-{
-    const float a = v * r;
-    float c = __builtin_rintf(a);
-    if (fabsf(a - c) > 0.5f - 0x1p-14f || fabsf(a) >= 128.0f) c = __builtin_rintf(v / s);
-    c = fminf(fmaxf(c, -qmax - 1.0f), qmax);
-    return (uint32_t)(int32_t)c & 0xFFu;
-}
 
 __device__ __forceinline__ void widen8(const u32x4 &raw, float v[8])
 {

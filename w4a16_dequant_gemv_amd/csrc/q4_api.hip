@@ -95,6 +95,48 @@ int check_kv_rows(int64_t rows, int32_t d)
     return Q4_OK;
 }
 
+// The paged cache.  Sequences end before 2^30 tokens, so places in them fit 32
+// bits; pools are addressed with 64.
+constexpr int64_t kMaxPool = int64_t(1) << 38;
+
+int check_heads(int64_t n_q, int64_t n_kv)
+{
+    return n_kv >= 1 && n_kv <= 1024 && n_q >= n_kv && n_q <= 1024 && n_q % n_kv == 0 ? Q4_OK : Q4_ERR_SHAPE;
+}
+
+int check_paged_d(int32_t d) { return d == 64 || d == 96 || d == 128 || d == 256 ? Q4_OK : Q4_ERR_SHAPE; }
+
+int check_paged_cache(const kv_paged_cache *c)
+{
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->k_tail || !c->v_tail) return Q4_ERR_NULL;
+    if (check_heads(c->n_kv, c->n_kv) || check_paged_d(c->d)) return Q4_ERR_SHAPE;
+    if (c->page != 64 && c->page != 128 && c->page != 256) return Q4_ERR_SHAPE;
+    const int64_t head = (int64_t)c->page * c->d, most = kMaxPool / (head * c->n_kv);
+    if (c->pages < 1 || c->pages > most || c->slots < 1 || c->slots > most / 2) return Q4_ERR_SHAPE;
+    if (c->pages > INT32_MAX || c->slots > INT32_MAX) return Q4_ERR_SHAPE;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_tail, 16) || !aligned(c->v_tail, 16) ||
+        !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return Q4_ERR_ALIGN;
+    return Q4_OK;
+}
+
+int check_paged_batch(const kv_paged_batch *b, int32_t page)
+{
+    if (!b || !b->cu_q || !b->ctx_lens || !b->block_table || !b->slots) return Q4_ERR_NULL;
+    if (check_rows(b->tokens) || b->batch < 1 || b->batch > 65536) return Q4_ERR_SHAPE;
+    if (b->table_cols < 1 || b->table_cols > (1 << 30) / page) return Q4_ERR_SHAPE;
+    if (!aligned(b->cu_q, 4) || !aligned(b->ctx_lens, 4) || !aligned(b->block_table, 4) || !aligned(b->slots, 4))
+        return Q4_ERR_ALIGN;
+    return Q4_OK;
+}
+
+// fp16 rows of `width` elements, `stride` apart.
+int check_paged_rows(const uint16_t *x, int64_t stride, int64_t width, int64_t tokens)
+{
+    if (stride < width || stride % 8 != 0 || stride > kMaxElems / tokens) return Q4_ERR_SHAPE;
+    return aligned(x, 16) ? Q4_OK : Q4_ERR_ALIGN;
+}
+
 }  // namespace
 
 extern "C" {
@@ -293,6 +335,66 @@ int kv_flush_blocks(const uint16_t *k, const uint16_t *v, int64_t blocks, int32_
         return Q4_ERR_ALIGN;
     return finish(kv_launch_flush(k, v, blocks, t, d, bits, dst, pool_blocks, k_pool, k_scale, v_pool,
                                   v_scale, (hipStream_t)stream));
+}
+
+int kv_paged_append(const kv_paged_cache *cache, const kv_paged_batch *batch, const uint16_t *k, int64_t k_stride,
+                    const uint16_t *v, int64_t v_stride, const uint16_t *q, int64_t q_stride, int32_t n_q,
+                    const float *rope, int64_t rope_rows, int32_t rope_dim, int32_t interleaved,
+                    const int32_t *positions, uint16_t *q_out, void *stream)
+{
+    if (int rc = check_paged_cache(cache)) return rc;
+    if (int rc = check_paged_batch(batch, cache->page)) return rc;
+    if (!k || !v || (rope && !positions) || (q && !q_out)) return Q4_ERR_NULL;
+    const int64_t T = batch->tokens;
+    const int64_t width = (int64_t)cache->n_kv * cache->d;
+    if (int rc = check_paged_rows(k, k_stride, width, T)) return rc;
+    if (int rc = check_paged_rows(v, v_stride, width, T)) return rc;
+    if (q) {
+        if (check_heads(n_q, cache->n_kv)) return Q4_ERR_SHAPE;
+        if (int rc = check_paged_rows(q, q_stride, (int64_t)n_q * cache->d, T)) return rc;
+        if (!aligned(q_out, 16)) return Q4_ERR_ALIGN;
+    }
+    if (rope) {
+        if (rope_dim < 32 || rope_dim > cache->d || rope_dim % 32 != 0 || rope_rows < 1 || rope_rows > kMaxElems / rope_dim)
+            return Q4_ERR_SHAPE;
+        if (!aligned(rope, 16) || !aligned(positions, 4)) return Q4_ERR_ALIGN;
+    }
+    return finish(kv_launch_append(*cache, *batch, k, k_stride, v, v_stride, q, q_stride, n_q, rope, rope_rows,
+                                   rope_dim, interleaved != 0, positions, q_out, (hipStream_t)stream));
+}
+
+int kv_paged_read(const kv_paged_cache *cache, const int32_t *ids, int64_t n, uint16_t *k_out, uint16_t *v_out,
+                  void *stream)
+{
+    if (int rc = check_paged_cache(cache)) return rc;
+    if (!ids || !k_out || !v_out) return Q4_ERR_NULL;
+    if (n < 1 || n > kMaxRows / cache->n_kv || n * cache->n_kv * cache->page * cache->d > kMaxElems) return Q4_ERR_SHAPE;
+    if (!aligned(ids, 4) || !aligned(k_out, 16) || !aligned(v_out, 16)) return Q4_ERR_ALIGN;
+    return finish(kv_launch_read(*cache, ids, n, k_out, v_out, (hipStream_t)stream));
+}
+
+int64_t kv_paged_attention_workspace_size(int64_t tokens, int32_t batch, int32_t n_q, int32_t n_kv, int32_t d)
+{
+    if (check_rows(tokens) || batch < 1 || batch > 65536 || check_heads(n_q, n_kv) || check_paged_d(d)) return 0;
+    return kv_attention_workspace(tokens, batch, n_q, n_kv, d);
+}
+
+int kv_paged_attention(const kv_paged_cache *cache, const kv_paged_batch *batch, const uint16_t *q, int64_t q_stride,
+                       int32_t n_q, float scale, int32_t window, int32_t sinks, void *workspace,
+                       int64_t workspace_bytes, uint16_t *out, void *stream)
+{
+    if (int rc = check_paged_cache(cache)) return rc;
+    if (int rc = check_paged_batch(batch, cache->page)) return rc;
+    if (!q || !workspace || !out) return Q4_ERR_NULL;
+    if (check_heads(n_q, cache->n_kv) || !(scale > 0.0f && scale <= 1e6f)) return Q4_ERR_SHAPE;
+    if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return Q4_ERR_SHAPE;
+    if (batch->tokens * n_q * cache->d > kMaxElems) return Q4_ERR_SHAPE;
+    if (int rc = check_paged_rows(q, q_stride, (int64_t)n_q * cache->d, batch->tokens)) return rc;
+    if (!aligned(workspace, 16) || !aligned(out, 16)) return Q4_ERR_ALIGN;
+    if (workspace_bytes < kv_attention_workspace(batch->tokens, batch->batch, n_q, cache->n_kv, cache->d))
+        return Q4_ERR_SHAPE;
+    return finish(kv_launch_attention(*cache, *batch, q, q_stride, n_q, scale, window, sinks, workspace, out,
+                                      (hipStream_t)stream));
 }
 
 int sq_absmax_update_f16(const uint16_t *x, int64_t rows, int32_t cols, float *amax, void *stream)

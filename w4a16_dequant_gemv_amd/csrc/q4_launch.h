@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kv_codec.h"
+
 // bits is 4 or 8; group_size is 32..256 or n_in (per-channel).
 hipError_t q4_launch_quantize_pack(const float *w, int64_t n_out, int64_t n_in, int group_size,
                                    int bits, bool symmetric, uint32_t *qweight, uint16_t *scales,
@@ -40,6 +42,18 @@ hipError_t kv_launch_dequant_tokens(const int8_t *q, const float *scale, int64_t
                                     hipStream_t stream);
 hipError_t kv_launch_dequant_channels(const int8_t *q, const float *scale, int64_t blocks, int t, int d,
                                       uint16_t *out, hipStream_t stream);
+
+// The paged INT8 cache (kv_append.hip, kv_attention.hip).
+hipError_t kv_launch_append(const kv_paged_cache &cache, const kv_paged_batch &batch, const uint16_t *k,
+                            int64_t k_stride, const uint16_t *v, int64_t v_stride, const uint16_t *q, int64_t q_stride,
+                            int n_q, const float *rope, int64_t rope_rows, int rope_dim, bool interleaved,
+                            const int32_t *positions, uint16_t *q_out, hipStream_t stream);
+hipError_t kv_launch_read(const kv_paged_cache &cache, const int32_t *ids, int64_t n, uint16_t *k_out, uint16_t *v_out,
+                          hipStream_t stream);
+int64_t kv_attention_workspace(int64_t tokens, int batch, int n_q, int n_kv, int d);
+hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch &batch, const uint16_t *q,
+                               int64_t q_stride, int n_q, float scale, int window, int sinks, void *workspace,
+                               uint16_t *out, hipStream_t stream);
 
 // W8A8 with SmoothQuant (w8a8.hip); cols % 8 == 0, k % 32 == 0, k <= 32768.
 hipError_t w8a8_launch_col_absmax(const void *src, bool f32, int64_t rows, int cols, float *out,

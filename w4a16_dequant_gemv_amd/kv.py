@@ -1,12 +1,17 @@
 """torch-facing wrappers over the KV-cache codec of libw4a16.so
 (`include/kv_codec.h`): V quantized per token, K per channel over blocks of
-tokens, symmetric INT8 or INT4 codes in int8, fp32 scales.
+tokens, symmetric INT8 or INT4 codes in int8, fp32 scales; and the paged INT8
+cache (PagedKVCache): appending new tokens with rotation, and attention over it.
 
 Only argument marshalling happens here: tensors must already live on the GPU
 and the library does all of the arithmetic on torch's current stream.
 """
+import contextlib
+from ctypes import byref
+
 import torch
 
+from . import _lib
 from ._lib import W4A16Error, check, lib
 from .api import _need, _same_device, _stream
 
@@ -115,3 +120,202 @@ class KVBlockPool:
                                         dst.data_ptr(), self.pool_blocks, self.k.data_ptr(),
                                         self.k_scale.data_ptr(), self.v.data_ptr(), self.v_scale.data_ptr(),
                                         _stream(self.k)), "kv_flush_blocks")
+
+
+def rope_table(rows, dim, base=10000.0, device="cuda"):
+    """Cosine and sine of position p times base^(-2 j / dim), fp32 [rows, dim/2, 2]
+    (angles in binary64: positions lose whole turns in binary32)."""
+    f = float(base) ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    a = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * f
+    return torch.stack((a.cos(), a.sin()), -1).float()
+
+
+def _on(device):
+    """torch.cuda.device(device), or nothing where that is the current one."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _heads(t, heads, d, name, device):
+    """The row stride of fp16 t [T, heads, d] whose rows are whole (a view into
+    a fused projection's output is)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise W4A16Error(f"{name} must be a GPU tensor (there is no CPU implementation)")
+    if t.dtype != torch.float16 or t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise W4A16Error(f"{name} must be float16 [tokens, {'heads' if heads is None else heads}, {d}], got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise W4A16Error("all tensors must be on the same GPU")
+    row, head, one = t.stride()
+    if one != 1 or (head != d and t.shape[1] > 1):
+        raise W4A16Error(f"{name}: a token's heads must lie side by side")
+    return row if t.shape[0] > 1 else t.shape[1] * d
+
+
+class PagedBatch:
+    """The sequences of one call (kv_paged_batch in kv_codec.h), int32 GPU
+    tensors: rows cu_q[b] .. cu_q[b+1]-1 of the call belong to sequence b, which
+    holds ctx_lens[b] tokens before them; its page p is pool page
+    block_table[b, p], its ring of fp16 pages is slots[b].  The tensors are read
+    when the kernels run, so one PagedBatch can be kept (and captured) while
+    their contents change from step to step."""
+
+    def __init__(self, cu_q, ctx_lens, block_table, slots):
+        if not isinstance(ctx_lens, torch.Tensor) or not isinstance(block_table, torch.Tensor):
+            raise W4A16Error("ctx_lens and block_table must be GPU tensors")
+        if ctx_lens.dim() != 1 or block_table.dim() != 2 or ctx_lens.numel() == 0 or block_table.shape[1] == 0:
+            raise W4A16Error("ctx_lens must be [batch], block_table [batch, pages per sequence], neither empty")
+        B = ctx_lens.shape[0]
+        for t, shape, name in ((cu_q, (B + 1,), "cu_q"), (ctx_lens, (B,), "ctx_lens"),
+                               (block_table, (B, block_table.shape[1]), "block_table"), (slots, (B,), "slots")):
+            _need(t, torch.int32, shape, name)
+        _same_device(cu_q, ctx_lens, block_table, slots)
+        self.cu_q, self.ctx_lens, self.block_table, self.slots = cu_q, ctx_lens, block_table, slots
+
+    def _struct(self, tokens, device):
+        if self.cu_q.device != device:
+            raise W4A16Error("all tensors must be on the same GPU")
+        return _lib.PagedBatch(self.cu_q.data_ptr(), self.ctx_lens.data_ptr(), self.block_table.data_ptr(),
+                               self.slots.data_ptr(), tokens, self.ctx_lens.shape[0], self.block_table.shape[1])
+
+
+class PagedKVCache:
+    """One layer's paged INT8 cache (kv_paged_* in kv_codec.h): pages of `page`
+    tokens with one scale per (page, kv head) for K and one for V, and a ring of
+    each sequence's last two pages in fp16, from which the unfinished page is
+    read.  Pages and rings are in the order of kv_codec.h; `read` gives pages in
+    the order of tokens.  Block tables, lengths and slots are the caller's
+    (PagedBatch), shared by a model's layers."""
+
+    def __init__(self, pool_pages, n_kv, d, slots, device, page=128):
+        if page not in (64, 128, 256) or d not in (64, 96, 128, 256):
+            raise W4A16Error(f"page must be 64, 128 or 256 and d 64, 96, 128 or 256, got {page} and {d}")
+        if pool_pages < 1 or slots < 1 or not 1 <= n_kv <= 1024:
+            raise W4A16Error("pool_pages and slots must be positive, n_kv in [1, 1024]")
+        self.n_kv, self.d, self.page = n_kv, d, page
+        kshape, vshape = self._shapes()
+        self.k = torch.zeros((pool_pages, *kshape), dtype=torch.int8, device=device)
+        self.v = torch.zeros((pool_pages, *vshape), dtype=torch.int8, device=device)
+        self.k_scale = torch.zeros((pool_pages, n_kv), dtype=torch.float32, device=device)
+        self.v_scale = torch.zeros((pool_pages, n_kv), dtype=torch.float32, device=device)
+        self.k_tail = torch.zeros((slots, 2, *kshape), dtype=torch.float16, device=device)
+        self.v_tail = torch.zeros((slots, 2, *vshape), dtype=torch.float16, device=device)
+
+    def _shapes(self):
+        h, d, t = self.n_kv, self.d, self.page
+        return (h, t // 64, 4, d // 16, 16, 16), (h, t // 16, d, 16)
+
+    @property
+    def pool_pages(self):
+        return self.k.shape[0]
+
+    @property
+    def slots(self):
+        return self.k_tail.shape[0]
+
+    def _checked(self):
+        """The six tensors, checked, as the library's struct."""
+        kshape, vshape = self._shapes()
+        P, S = self.pool_pages, self.slots
+        _need(self.k, torch.int8, (P, *kshape), "k")
+        _need(self.v, torch.int8, (P, *vshape), "v")
+        _need(self.k_scale, torch.float32, (P, self.n_kv), "k_scale")
+        _need(self.v_scale, torch.float32, (P, self.n_kv), "v_scale")
+        _need(self.k_tail, torch.float16, (S, 2, *kshape), "k_tail")
+        _need(self.v_tail, torch.float16, (S, 2, *vshape), "v_tail")
+        _same_device(self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
+        return _lib.PagedCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                               self.k_tail.data_ptr(), self.v_tail.data_ptr(), P, S, self.n_kv, self.d, self.page)
+
+    def append(self, k, v, batch, q=None, rope=None, positions=None, interleaved=False, q_out=None):
+        """Put fp16 k, v [T, n_kv, d] behind each sequence's ctx_lens tokens; with
+        `rope` (fp32 [rows, dim/2, 2], see rope_table) and int32 positions [T], k
+        is rotated first, and q [T, n_q, d] into the result [T, n_q, d] (None
+        without q).  ctx_lens is not changed: advance it once every layer has
+        appended and attended."""
+        c, dev = self._checked(), self.k.device
+        ks, vs = _heads(k, self.n_kv, self.d, "k", dev), _heads(v, self.n_kv, self.d, "v", dev)
+        T = k.shape[0]
+        if v.shape[0] != T:
+            raise W4A16Error("k and v must have the same tokens")
+        qs = n_q = 0
+        if rope is None:
+            if q is not None or positions is not None:
+                raise W4A16Error("q and positions are only used with rope")
+        else:
+            if not isinstance(rope, torch.Tensor) or rope.dim() != 3:
+                raise W4A16Error("rope must be fp32 [rows, dim/2, 2] on the GPU")
+            _need(rope, torch.float32, (rope.shape[0], rope.shape[1], 2), "rope")
+            if rope.shape[0] < 1 or rope.shape[1] < 16 or rope.shape[1] % 16 or rope.shape[1] * 2 > self.d:
+                raise W4A16Error(f"rope must rotate a multiple of 32 channels, at most d={self.d}")
+            _need(positions, torch.int32, (T,), "positions")
+            _same_device(self.k, rope, positions)
+            if q is not None:
+                qs, n_q = _heads(q, None, self.d, "q", dev), q.shape[1]
+                if q.shape[0] != T:
+                    raise W4A16Error("q and k must have the same tokens")
+                q_out = torch.empty((T, n_q, self.d), dtype=torch.float16, device=dev) if q_out is None else q_out
+                _need(q_out, torch.float16, (T, n_q, self.d), "q_out")
+                _same_device(self.k, q_out)
+        if T == 0:
+            return q_out
+        with _on(dev):
+            check(lib().kv_paged_append(
+                byref(c), byref(batch._struct(T, dev)), k.data_ptr(), ks, v.data_ptr(), vs,
+                None if q is None else q.data_ptr(), qs, n_q, None if rope is None else rope.data_ptr(),
+                0 if rope is None else rope.shape[0], 0 if rope is None else rope.shape[1] * 2, int(bool(interleaved)),
+                None if rope is None else positions.data_ptr(), None if q is None else q_out.data_ptr(),
+                _stream(self.k)), "kv_paged_append")
+        return None if q is None else q_out
+
+    def read(self, ids, k_out=None, v_out=None):
+        """Pool pages ids (int32 [n]) as fp16 (K, V), each [n, n_kv, page, d] in the
+        order of tokens; ids outside the pool are skipped."""
+        c, dev = self._checked(), self.k.device
+        if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+            raise W4A16Error("ids must be int32 [n] on the GPU")
+        n = ids.shape[0]
+        _need(ids, torch.int32, (n,), "ids")
+        shape = (n, self.n_kv, self.page, self.d)
+        k_out = torch.empty(shape, dtype=torch.float16, device=dev) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=torch.float16, device=dev) if v_out is None else v_out
+        _need(k_out, torch.float16, shape, "k_out")
+        _need(v_out, torch.float16, shape, "v_out")
+        _same_device(self.k, ids, k_out, v_out)
+        if n:
+            with _on(dev):
+                check(lib().kv_paged_read(byref(c), ids.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+                                          _stream(self.k)), "kv_paged_read")
+        return k_out, v_out
+
+    def attend(self, q, batch, scale=None, window=0, sinks=0, out=None, workspace=None):
+        """softmax(scale * q k^T) v of fp16 q [T, n_q, d] over the cache, into fp16
+        [T, n_q, d]; the batch's own tokens have been appended before.  Row i of
+        a sequence sees the tokens up to its own, with window > 0 the last
+        `window` of them and the sequence's first `sinks`.  scale defaults to
+        d^-1/2.  Rows of no sequence are left as they were."""
+        c, dev = self._checked(), self.k.device
+        qs = _heads(q, None, self.d, "q", dev)
+        T, n_q = q.shape[:2]
+        if n_q == 0 or n_q % self.n_kv or n_q > 1024:
+            raise W4A16Error(f"q must have a multiple of {self.n_kv} heads, at most 1024, got {n_q}")
+        if window < 0 or sinks < 0 or (sinks and not window) or max(window, sinks) >= 1 << 31:
+            raise W4A16Error("window and sinks must not be negative, and sinks need a window")
+        scale = self.d ** -0.5 if scale is None else float(scale)
+        if not 0.0 < scale <= 1e6:
+            raise W4A16Error(f"scale must be in (0, 1e6], got {scale}")
+        out = torch.empty((T, n_q, self.d), dtype=torch.float16, device=dev) if out is None else out
+        _need(out, torch.float16, (T, n_q, self.d), "out")
+        _same_device(self.k, out)
+        if T == 0:
+            return out
+        b = batch._struct(T, dev)
+        need = lib().kv_paged_attention_workspace_size(T, b.batch, n_q, self.n_kv, self.d)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+            raise W4A16Error("workspace must be a contiguous tensor on the cache's GPU")
+        with _on(dev):
+            check(lib().kv_paged_attention(byref(c), byref(b), q.data_ptr(), qs, n_q, scale, window, sinks,
+                                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                           out.data_ptr(), _stream(self.k)), "kv_paged_attention")
+        return out
