@@ -80,23 +80,28 @@ struct Args {
     uint16_t *out;
 };
 
-// The tiles that some row of a sequence sees: the first `head` ones and those
-// from `first` to the end (`count` in all).
+// The tiles that some of a sequence's rows at places lo .. hi sees: the first
+// `head` ones and those from `first` on (`count` in all).
 struct Tiles {
     int head, first, count;
     __device__ int at(int i) const { return i < head ? i : i - head + first; }
 };
 
-__device__ __forceinline__ Tiles visible_tiles(const Args &a, const KvSeq &s)
+__device__ __forceinline__ Tiles visible_tiles(const Args &a, int lo, int hi)
 {
-    Tiles t = {0, 0, (s.total() + kTile - 1) / kTile};
+    Tiles t = {0, 0, hi / kTile + 1};
     if (a.window > 0) {
-        const int lo = max(s.ctx - a.window + 1, 0);               // the first row's first token
-        t.first = lo / kTile;
-        t.head = min((min(a.sinks, lo) + kTile - 1) / kTile, t.first);
+        const int first = max(lo - a.window + 1, 0);               // the first token that the window shows
+        t.first = first / kTile;
+        t.head = min((min(a.sinks, first) + kTile - 1) / kTile, t.first);
         t.count -= t.first - t.head;
     }
     return t;
+}
+
+__device__ __forceinline__ Tiles visible_tiles(const Args &a, const KvSeq &s)
+{
+    return visible_tiles(a, s.ctx, s.total() - 1);
 }
 
 // A run of row blocks' tiles as numbered units: sequence after sequence, its row
@@ -136,49 +141,83 @@ struct Wave {
     int at[QT];                  // the row's index in its sequence
 };
 
-// Scores to weights: masks, running maximum, P in two fp16 parts.  c1 = scale
-// log2(e) ks, w = log2(vs), inv = 1 / vs.
-template <int D, int QT>
-__device__ __forceinline__ void weights(Wave<D, QT> &s, int t, f32x4 x[4], const Args &a, bool masked, int tile0,
-                                        float c1, float w, float inv, f16x8 hi[2], f16x8 lo[2])
+// Scores x[a][i] of one query (row index `at`) to weights: masks, the running
+// maximum, P in fp16 and, with SPLIT, the rest of P beside it.  c1 = scale
+// log2(e) ks > 0, w = log2(vs), inv = 1 / vs.  Returns the factor that what was
+// summed before has to be multiplied with.
+template <bool SPLIT>
+__device__ __forceinline__ float weights(f32x4 x[4], const Args &a, int at, bool masked, int tile0, float c1, float w,
+                                         float inv, float &m_run, float &l_run, f16x8 hi[2], f16x8 lo[2])
 {
-    constexpr int DT = D / 16;
     const int g = (threadIdx.x & 63) >> 4;
-    float top = kNone;
+    if (masked) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int tok = tile0 + 16 * g + 4 * i + j;
+                const bool see = tok <= at && (a.window == 0 || at - tok < a.window || tok < a.sinks);
+                x[i][j] = see ? x[i][j] : -INFINITY;
+            }
+    }
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float e = x[i][j] * c1 + w;
-            if (masked) {
-                const int tok = tile0 + 16 * g + 4 * i + j;
-                const bool see = tok <= s.at[t] && (a.window == 0 || s.at[t] - tok < a.window || tok < a.sinks);
-                e = see ? e : -INFINITY;
-            }
-            x[i][j] = e;
-            top = fmaxf(top, e);
-        }
-    const float m = fmaxf(s.m[t], column_max(top));
-    const float keep = __builtin_amdgcn_exp2f(s.m[t] - m);
-    s.m[t] = m;
-    const float sub = m - kLift;
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, x[i][j]);
+    const float m = fmaxf(m_run, column_max(top) * c1 + w);
+    const float keep = __builtin_amdgcn_exp2f(m_run - m);
+    m_run = m;
+    const float add = w - m + kLift;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float p = __builtin_amdgcn_exp2f(x[i][j] - sub);
-            sum += p;
-            const _Float16 h = (_Float16)p;
-            hi[i >> 1][(i & 1) * 4 + j] = h;
-            lo[i >> 1][(i & 1) * 4 + j] = (_Float16)(p - (float)h);
+        for (int j = 0; j < 4; j += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(x[i][j] * c1 + add);
+            const float p1 = __builtin_amdgcn_exp2f(x[i][j + 1] * c1 + add);
+            sum += p0 + p1;
+            const f16x2 h = {(_Float16)p0, (_Float16)p1};
+            const int at8 = (i & 1) * 4 + j;
+            hi[i >> 1][at8] = h[0];
+            hi[i >> 1][at8 + 1] = h[1];
+            if (SPLIT) {
+                lo[i >> 1][at8] = (_Float16)(p0 - (float)h[0]);
+                lo[i >> 1][at8 + 1] = (_Float16)(p1 - (float)h[1]);
+            }
         }
-    s.l[t] = s.l[t] * keep + sum * inv;
+    l_run = l_run * keep + sum * inv;
+    return keep;
+}
+
+template <int D, int QT>
+__device__ __forceinline__ void weigh(Wave<D, QT> &s, int t, f32x4 x[4], const Args &a, bool masked, int tile0, float c1,
+                                      float w, float inv, f16x8 hi[2], f16x8 lo[2])
+{
+    const float keep = weights<true>(x, a, s.at[t], masked, tile0, c1, w, inv, s.m[t], s.l[t], hi, lo);
     if (__ballot(keep != 1.0f)) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) s.o[t][d] *= keep;
+        for (int d = 0; d < D / 16; ++d) s.o[t][d] *= keep;
     }
 }
+
+__device__ __forceinline__ float lane_value(float v, int i)
+{
+    return bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(v), i));
+}
+
+// What a tile's page contributes to the scores: c1 is kept positive so that a
+// masked score stays -inf, and a page that is not there has weight 2^-inf.
+struct PageScales {
+    float c1, w, inv;
+    __device__ PageScales() : c1(1.0f), w(-INFINITY), inv(0.0f) {}
+    __device__ void set(float scale, float ks, float vs)
+    {
+        c1 = fmaxf(scale * ks, 1e-30f);
+        w = __builtin_amdgcn_logf(vs);
+        inv = 1.0f / vs;
+    }
+};
 
 // Tiles t0, t0 + 4, ... < t1 of one row block, into the wave's state.
 template <int D, int QT>
@@ -198,7 +237,7 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
     for (int base = 0; base < n; base += 64) {
         // lane i: the tile base + i of the wave
         int tok0 = 0, id = 0;
-        float c1 = 0.0f, w = -INFINITY, inv = 0.0f;
+        PageScales ps;
         const int many = min(n - base, 64);
         if (lane < many) {
             tok0 = tiles.at(t0 + (base + lane) * kWaves) * kTile;
@@ -206,10 +245,7 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
                 const int e = a.batch.block_table[(int64_t)b * a.batch.table_cols + (tok0 >> a.page_shift)];
                 if (e >= 0 && e < a.cache.pages) {
                     id = e;
-                    const float vs = a.cache.v_scale[(int64_t)e * n_kv + h];
-                    c1 = a.scale * a.cache.k_scale[(int64_t)e * n_kv + h];
-                    w = __builtin_amdgcn_logf(vs);
-                    inv = 1.0f / vs;
+                    ps.set(a.scale, a.cache.k_scale[(int64_t)e * n_kv + h], a.cache.v_scale[(int64_t)e * n_kv + h]);
                 }
             }
         }
@@ -245,9 +281,9 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
         }
         for (int i = 0; i < in_pages; ++i) {
             const int tile0 = __builtin_amdgcn_readlane(tok0, i);
-            const float c = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(c1), i));
-            const float lw = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(w), i));
-            const float iv = bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(inv), i));
+            const float c = lane_value(ps.c1, i);
+            const float lw = lane_value(ps.w, i);
+            const float iv = lane_value(ps.inv, i);
             f32x4 x[QT][4];
 #pragma unroll
             for (int t = 0; t < QT; ++t)
@@ -269,7 +305,7 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
             const bool masked = is_masked(tile0);
             f16x8 ph[QT][2], pl[QT][2];
 #pragma unroll
-            for (int t = 0; t < QT; ++t) weights<D, QT>(s, t, x[t], a, masked, tile0, c, lw, iv, ph[t], pl[t]);
+            for (int t = 0; t < QT; ++t) weigh<D, QT>(s, t, x[t], a, masked, tile0, c, lw, iv, ph[t], pl[t]);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
                 f16x8 lo, hi;
@@ -312,7 +348,7 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
             }
             f16x8 ph[QT][2], pl[QT][2];
 #pragma unroll
-            for (int t = 0; t < QT; ++t) weights<D, QT>(s, t, x[t], a, true, tile0, a.scale, 0.0f, 1.0f, ph[t], pl[t]);
+            for (int t = 0; t < QT; ++t) weigh<D, QT>(s, t, x[t], a, true, tile0, a.scale, 0.0f, 1.0f, ph[t], pl[t]);
             // places behind the last token hold anything: zero them, 0 * NaN is not 0
             const int left = seq.total() - tile0 - 16 * g;
             u32x4 keep[2];
@@ -539,19 +575,269 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(Args a)
     }
 }
 
-// Blocks of 16 rows that a wave holds: as many as an average sequence fills,
-// within the registers (D = 256 leaves room for two).
-int row_blocks(int64_t tokens, int batch, int group, int d)
+// Many rows of a sequence: a workgroup of NW waves holds 32 NW rows (a wave two
+// blocks of 16) and walks the tiles they see; each tile is converted to fp16
+// once, into LDS, in the order of the operands (a wave reads 1 KiB in a row).
+// Two buffers: while one tile is multiplied, the next is written and the one
+// after it is on its way in registers.  With few row blocks the tiles are cut
+// into `splits` runs and joined by kv_join_rows_kernel.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kernel(Args a, int splits)
 {
-    const int64_t rows = (tokens + batch - 1) / batch * group;
-    return rows <= 16 ? 1 : rows <= 32 || d > 128 ? 2 : 4;
+    constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 32 * NW, THREADS = 64 * NW;
+    constexpr int UNITS = 4 * D, UN = (UNITS + THREADS - 1) / THREADS;     // 16-byte units of a tile's K (and V)
+    constexpr int KF = 8 * KS, VF = 2 * DT;                                // operands of 1 KiB
+    extern __shared__ f16x8 tile[];                        // [2][KF + VF][64]
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, m16 = lane & 15;
+    const int n_kv = a.cache.n_kv, page = 1 << a.page_shift, head = page * D;
+    const int h = blockIdx.x % n_kv, split = blockIdx.x / n_kv % splits;
+    int b;
+    int64_t rb64;
+    if (!kv_locate(a.batch.batch, (int64_t)(blockIdx.x / n_kv / splits), [&](int i) {
+            return (int64_t)((kv_seq(a.batch, i, a.cache.slots, a.page_shift).n * a.group + RB - 1) / RB);
+        }, b, rb64))
+        return;
+    const KvSeq seq = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
+    const int rows = seq.n * a.group, row0 = (int)rb64 * RB, full = seq.total() >> a.page_shift << a.page_shift;
+    const Tiles tiles = visible_tiles(a, seq.ctx + row0 / a.group, seq.ctx + (min(row0 + RB, rows) - 1) / a.group);
+    const int t0 = (int)((int64_t)tiles.count * split / splits), t1 = (int)((int64_t)tiles.count * (split + 1) / splits);
+
+    // this wave's rows
+    const int first = row0 + wave * 32;
+    const bool live = first < rows;
+    const int at_min = seq.ctx + first / a.group, at_max = seq.ctx + (min(first + 32, rows) - 1) / a.group;
+    f16x8 q[2][2 * KS];
+    f32x4 o[2][DT];
+    float m[2], l[2];
+    int at[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int r = first + t * 16 + m16, tok = r / a.group;
+        at[t] = seq.ctx + tok;
+        m[t] = kNone;
+        l[t] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const uint16_t *row = a.q + (int64_t)(seq.q0 + tok) * a.q_stride + (h * a.group + r - tok * a.group) * D;
+#pragma unroll
+        for (int e = 0; e < 2 * KS; ++e) {
+            const int ch = (e >> 1) * 64 + g * 16 + (e & 1) * 8;
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (r < rows && ch < D) v = *reinterpret_cast<const u32x4 *>(row + ch);
+            q[t][e] = bitcast<f16x8>(v);
+        }
+    }
+    if (D % 64 != 0) {                                     // channels that a last K operand has beyond D
+        for (int i = tid; i < 2 * (KF + VF) * 64; i += THREADS) tile[i] = f16x8{};
+        __syncthreads();
+    }
+
+    for (int base = t0; base < t1; base += 64) {
+        const int many = min(t1 - base, 64);
+        int tok0 = 0, id = 0;
+        PageScales ps;
+        if (lane < many) {
+            tok0 = tiles.at(base + lane) * kTile;
+            if (tok0 >= full) {
+                ps.set(a.scale, 1.0f, 1.0f);
+            } else {
+                const int e = a.batch.block_table[(int64_t)b * a.batch.table_cols + (tok0 >> a.page_shift)];
+                if (e >= 0 && e < a.cache.pages) {
+                    id = e;
+                    ps.set(a.scale, a.cache.k_scale[(int64_t)e * n_kv + h], a.cache.v_scale[(int64_t)e * n_kv + h]);
+                }
+            }
+        }
+        const int in_pages = __popcll(__ballot(lane < many && tok0 < full));
+
+        u32x4 kr[UN], vr[UN];
+        auto load = [&](int i) {                           // a tile of a finished page, into registers
+            const int64_t at0 = ((int64_t)__builtin_amdgcn_readlane(id, i) * n_kv + h) * head +
+                                (__builtin_amdgcn_readlane(tok0, i) & (page - 1)) * D;
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                if (UNITS % THREADS != 0 && tid + u * THREADS >= UNITS) continue;
+                kr[u] = *reinterpret_cast<const u32x4 *>(a.cache.k + at0 + (tid + u * THREADS) * 16);
+                vr[u] = *reinterpret_cast<const u32x4 *>(a.cache.v + at0 + (tid + u * THREADS) * 16);
+            }
+        };
+        auto put = [&](int i) {                            // tile i into its buffer
+            f16x8 *to = tile + (i & 1) * (KF + VF) * 64;
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                const int unit = tid + u * THREADS;
+                if (UNITS % THREADS != 0 && unit >= UNITS) continue;
+                const int c = unit / 16 % DT, ka = unit / 16 / DT, kl = (c & 3) * 16 + (unit & 15);
+                const int ch = unit % D, vl = unit / D * 16 + (ch & 15);
+                f16x8 k0, k1, v0, v1;
+                if (i < in_pages) {
+                    codes_to_half(kr[u], k0, k1);
+                    codes_to_half(vr[u], v0, v1);
+                } else {
+                    const int tile0 = __builtin_amdgcn_readlane(tok0, i);
+                    const int64_t at0 = (((int64_t)seq.slot * 2 + (tile0 >> a.page_shift & 1)) * n_kv + h) * head +
+                                        (tile0 & (page - 1)) * D + unit * 16;
+                    const f16x8 *kp = reinterpret_cast<const f16x8 *>(a.cache.k_tail + at0);
+                    const u32x4 *vp = reinterpret_cast<const u32x4 *>(a.cache.v_tail + at0);
+                    k0 = kp[0];
+                    k1 = kp[1];
+                    // places behind the last token hold anything: zero them, 0 * NaN is not 0
+                    const int left = seq.total() - tile0 - 16 * (unit / D);
+                    u32x4 x = vp[0], y = vp[1];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] &= left >= 2 * e + 2 ? 0xFFFFFFFFu : left == 2 * e + 1 ? 0xFFFFu : 0u;
+                        y[e] &= left >= 2 * e + 10 ? 0xFFFFFFFFu : left == 2 * e + 9 ? 0xFFFFu : 0u;
+                    }
+                    v0 = bitcast<f16x8>(x);
+                    v1 = bitcast<f16x8>(y);
+                }
+                f16x8 *kt = to + ((ka * KS + (c >> 2)) * 2) * 64 + kl;
+                kt[0] = k0;
+                kt[64] = k1;
+                f16x8 *vt = to + (KF + ch / 16 * 2) * 64 + vl;
+                vt[0] = v0;
+                vt[64] = v1;
+            }
+        };
+
+        if (in_pages > 0) load(0);
+        __syncthreads();                                   // the last batch of tiles has been read
+        put(0);
+        if (in_pages > 1) load(1);
+        __syncthreads();
+        for (int i = 0; i < many; ++i) {
+            const int tile0 = __builtin_amdgcn_readlane(tok0, i);
+            const f16x8 *from = tile + (i & 1) * (KF + VF) * 64 + lane;
+            const bool see = live && tile0 <= at_max;
+            if (see) {
+                const float c1 = lane_value(ps.c1, i), w = lane_value(ps.w, i), inv = lane_value(ps.inv, i);
+                const bool masked = tile0 + kTile - 1 > at_min ||
+                                    (a.window > 0 && at_max - tile0 >= a.window && tile0 + kTile > a.sinks);
+                f32x4 x[2][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[0][j] = x[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 2 * KS; ++e) {
+                        const f16x8 k = from[(j * 2 * KS + e) * 64];
+                        x[0][j] = mfma(k, q[0][e], x[0][j]);
+                        x[1][j] = mfma(k, q[1][e], x[1][j]);
+                    }
+                }
+                f16x8 p[2][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float keep = weights<false>(x[t], a, at[t], masked, tile0, c1, w, inv, m[t], l[t], p[t], nullptr);
+                    if (__ballot(keep != 1.0f)) {
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) o[t][d] *= keep;
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const f16x8 v = from[(KF + d * 2 + e) * 64];
+                        o[0][d] = mfma(v, p[0][e], o[0][d]);
+                        o[1][d] = mfma(v, p[1][e], o[1][d]);
+                    }
+            }
+            if (i + 1 < many) put(i + 1);
+            if (i + 2 < in_pages) load(i + 2);
+            __syncthreads();
+        }
+    }
+
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int r = first + t * 16 + m16;
+        const float sum = column_sum(l[t]);
+        if (r >= rows) continue;
+        const int tok = r / a.group;
+        const int64_t at_out = (int64_t)(seq.q0 + tok) * a.n_q + h * a.group + r - tok * a.group;
+        if (splits == 1) {
+            const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const f16x2 x = {(_Float16)(o[t][d][0] * f), (_Float16)(o[t][d][1] * f)};
+                const f16x2 y = {(_Float16)(o[t][d][2] * f), (_Float16)(o[t][d][3] * f)};
+                *reinterpret_cast<u32x2 *>(a.out + at_out * D + d * 16 + g * 4) =
+                    u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
+            }
+        } else {
+            const int64_t slot = at_out * splits + split;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(a.part + slot * D + d * 16 + g * 4) = o[t][d];
+            if (g == 0) {
+                a.stats[slot * 2] = m[t];
+                a.stats[slot * 2 + 1] = sum;
+            }
+        }
+    }
 }
 
-// Two workgroups per CU: 512 on the 256 CUs, shared by the kv heads.
-int workers(int n_kv) { return n_kv < 512 ? (512 + n_kv - 1) / n_kv : 1; }
+// Joins the `splits` parts of every row of the batch's sequences.
+template <int D>
+__global__ __launch_bounds__(kThreads) void kv_join_rows_kernel(Args a, int splits)
+{
+    constexpr int PER = D / 4;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, row = i / PER;
+    const int ch = (int)(i - row * PER) * 4;
+    if (row >= a.batch.tokens * a.n_q) return;
+    const int tok = (int)(row / a.n_q);
+    // a row of no sequence, or of one that was skipped, is left as it was
+    int lo = 0, hi = a.batch.batch;                        // the last sequence that starts at or before the row
+    while (lo + 1 < hi) {
+        const int mid = (lo + hi) / 2;
+        if (a.batch.cu_q[mid] <= tok) lo = mid; else hi = mid;
+    }
+    const KvSeq s = kv_seq(a.batch, lo, a.cache.slots, a.page_shift);
+    if (tok < s.q0 || tok >= s.q0 + s.n) return;
+    float m = kNone;
+    for (int p = 0; p < splits; ++p) m = fmaxf(m, a.stats[(row * splits + p) * 2]);
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.0f;
+    for (int p = 0; p < splits; ++p) {
+        const float f = __builtin_amdgcn_exp2f(a.stats[(row * splits + p) * 2] - m);
+        l += a.stats[(row * splits + p) * 2 + 1] * f;
+        o += *reinterpret_cast<const f32x4 *>(a.part + (row * splits + p) * D + ch) * f;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const f16x2 x = {(_Float16)(o[0] * inv), (_Float16)(o[1] * inv)}, y = {(_Float16)(o[2] * inv), (_Float16)(o[3] * inv)};
+    *reinterpret_cast<u32x2 *>(a.out + row * D + ch) = u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
+}
+
+// How a call is run.  qt > 0: the split kernel with qt blocks of 16 rows, as many
+// as an average sequence fills.  qt == 0: the rows kernel with `waves` waves and
+// `splits` runs of tiles.
+struct Plan {
+    int qt, waves, splits, workers;
+    int64_t items, parts;        // row blocks of the rows kernel (an upper bound); rows of workspace
+};
+
+Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d)
+{
+    Plan p = {};
+    const int64_t group = n_q / n_kv, rows = (tokens + batch - 1) / batch * group;
+    if (rows <= (d <= 128 ? 32 : 16)) {
+        p.qt = rows <= 16 ? 1 : 2;
+        p.workers = n_kv < 512 ? (512 + n_kv - 1) / n_kv : 1;    // two workgroups per CU: 512 on the 256 CUs
+        p.parts = (int64_t)p.workers * n_kv * 2 * 16 * p.qt;
+        return p;
+    }
+    // 256 rows a workgroup while that gives every CU one, else 128
+    p.waves = rows >= 256 && tokens * group / 256 * n_kv >= 256 && d <= 128 ? 8 : 4;
+    const int64_t rb = 32 * p.waves;
+    p.items = tokens * group / rb + batch;
+    const int64_t groups = (tokens * group + rb - 1) / rb * n_kv;
+    p.splits = (int)(groups >= 256 ? 1 : (511 + groups) / groups < 16 ? (511 + groups) / groups : 16);
+    p.parts = p.splits > 1 ? tokens * n_q * p.splits : 0;
+    return p;
+}
 
 template <int D, int QT>
-hipError_t launch(const Args &a, hipStream_t stream)
+hipError_t launch_split(const Args &a, hipStream_t stream)
 {
     kv_attend_split_kernel<D, QT><<<(unsigned)(a.workers * a.cache.n_kv), kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
@@ -560,35 +846,54 @@ hipError_t launch(const Args &a, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <int D, int NW>
+hipError_t launch_rows(const Args &a, const Plan &p, hipStream_t stream)
+{
+    constexpr int LDS = 2 * (8 * ((D + 63) / 64) + D / 8) * 1024;
+    if (LDS > 65536) {
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv_attend_rows_kernel<D, NW>),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+        if (e != hipSuccess) return e;
+    }
+    kv_attend_rows_kernel<D, NW><<<(unsigned)(p.items * a.cache.n_kv * p.splits), 64 * NW, LDS, stream>>>(a, p.splits);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int64_t threads = a.batch.tokens * a.n_q * (D / 4);
+    kv_join_rows_kernel<D><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a, p.splits);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch(const Args &a, const Plan &p, hipStream_t stream)
+{
+    if (p.qt == 1) return launch_split<D, 1>(a, stream);
+    if constexpr (D <= 128) {
+        if (p.qt == 2) return launch_split<D, 2>(a, stream);
+        if (p.waves == 8) return launch_rows<D, 8>(a, p, stream);
+    }
+    return launch_rows<D, 4>(a, p, stream);
+}
+
 }  // namespace
 
 int64_t kv_attention_workspace(int64_t tokens, int batch, int n_q, int n_kv, int d)
 {
-    const int64_t rows = (int64_t)workers(n_kv) * n_kv * 2 * 16 * row_blocks(tokens, batch, n_q / n_kv, d);
-    return rows * (d + 2) * 4;
+    return plan_for(tokens, batch, n_q, n_kv, d).parts * (d + 2) * 4 + 16;
 }
 
 hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch &batch, const uint16_t *q,
                                int64_t q_stride, int n_q, float scale, int window, int sinks, void *workspace,
                                uint16_t *out, hipStream_t stream)
 {
-    Args a = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, window, sinks,
-              __builtin_ctz(cache.page), workers(cache.n_kv), nullptr, nullptr, out};
-    const int qt = row_blocks(batch.tokens, batch.batch, a.group, cache.d);
-    a.part = (float *)workspace;
-    a.stats = a.part + (int64_t)a.workers * cache.n_kv * 2 * 16 * qt * cache.d;
-    switch (cache.d * 8 + qt) {
-    case 64 * 8 + 1: return launch<64, 1>(a, stream);
-    case 64 * 8 + 2: return launch<64, 2>(a, stream);
-    case 64 * 8 + 4: return launch<64, 4>(a, stream);
-    case 96 * 8 + 1: return launch<96, 1>(a, stream);
-    case 96 * 8 + 2: return launch<96, 2>(a, stream);
-    case 96 * 8 + 4: return launch<96, 4>(a, stream);
-    case 128 * 8 + 1: return launch<128, 1>(a, stream);
-    case 128 * 8 + 2: return launch<128, 2>(a, stream);
-    case 128 * 8 + 4: return launch<128, 4>(a, stream);
-    case 256 * 8 + 1: return launch<256, 1>(a, stream);
-    case 256 * 8 + 2: return launch<256, 2>(a, stream);
+    const Plan p = plan_for(batch.tokens, batch.batch, n_q, cache.n_kv, cache.d);
+    float *part = (float *)workspace;
+    const Args a = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, window, sinks,
+                    __builtin_ctz(cache.page), p.workers, part + p.parts * cache.d, part, out};
+    switch (cache.d) {
+    case 64: return launch<64>(a, p, stream);
+    case 96: return launch<96>(a, p, stream);
+    case 128: return launch<128>(a, p, stream);
+    case 256: return launch<256>(a, p, stream);
     default: return hipErrorInvalidValue;
     }
 }
