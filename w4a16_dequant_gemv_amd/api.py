@@ -40,7 +40,7 @@ class QuantizedWeight:
 
 def _stream(t):
     """Handle of torch's current HIP stream on t's device."""
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _need(t, dtype, shape, name):

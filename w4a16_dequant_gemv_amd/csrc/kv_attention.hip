@@ -50,6 +50,14 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Four channels of o = O / l to fp16; a row that saw nothing gives zeros.
+__device__ __forceinline__ void store_out(uint16_t *to, f32x4 o, float l)
+{
+    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+    const f16x2 x = {(_Float16)(o[0] * f), (_Float16)(o[1] * f)}, y = {(_Float16)(o[2] * f), (_Float16)(o[3] * f)};
+    *reinterpret_cast<u32x2 *>(to) = u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
+}
+
 // Over the four lanes that hold one query's tokens.
 __device__ __forceinline__ float column_max(float v)
 {
@@ -75,8 +83,10 @@ struct Args {
     int n_q, group;              // query heads, and those per kv head
     float scale;                 // times log2(e)
     int window, sinks, page_shift;
-    int workers;                 // per kv head
-    float *stats, *part;         // of unfinished row blocks
+    int workers;                 // per kv head, of the split kernel
+    double inv_workers;
+    float *part, *stats;         // sums and (m, l) of unfinished row blocks
+    int32_t *notes;              // [workers][4]: what the joining kernel has to do
     uint16_t *out;
 };
 
@@ -104,32 +114,33 @@ __device__ __forceinline__ Tiles visible_tiles(const Args &a, const KvSeq &s)
     return visible_tiles(a, s.ctx, s.total() - 1);
 }
 
-// A run of row blocks' tiles as numbered units: sequence after sequence, its row
-// blocks of RB rows one after the other, each with the sequence's tiles.
+// The split kernel's work as numbered units: sequence after sequence, its row
+// blocks of RB rows one after the other, each with the sequence's tiles.  Lane i
+// of a wave holds sequence 64 chunk + i.
 template <int RB>
-__device__ __forceinline__ int64_t seq_units(const Args &a, int b)
-{
-    const KvSeq s = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
-    return s.n ? (int64_t)((s.n * a.group + RB - 1) / RB) * visible_tiles(a, s).count : 0;
-}
+struct Roster {
+    int chunk = -1;
+    KvSeq s;
+    int64_t units, end;          // the sequence's units, and their sum up to it within the chunk
 
-template <int RB>
-__device__ __forceinline__ int64_t all_units(const Args &a)
-{
-    const int lane = threadIdx.x & 63;
-    int64_t n = 0;
-    for (int b = lane; b < a.batch.batch; b += 64) n += seq_units<RB>(a, b);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o);
-    return n;
-}
-
-// How many workers of a kv head share `units` of work: no fewer than four tiles
-// (one for each wave) for a worker.
-__device__ __forceinline__ int64_t used_workers(const Args &a, int64_t units)
-{
-    return max(min((int64_t)a.workers, (units + kWaves - 1) / kWaves), (int64_t)1);
-}
+    __device__ void load(const Args &a, int c)
+    {
+        chunk = c;
+        const int b = c * 64 + (threadIdx.x & 63);
+        units = 0;
+        s = {0, 0, 0, 0};
+        if (b < a.batch.batch) {
+            s = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
+            if (s.n) units = (int64_t)((s.n * a.group + RB - 1) / RB) * visible_tiles(a, s).count;
+        }
+        end = kv_wave_scan(units);
+    }
+    __device__ KvSeq get(int i) const
+    {
+        return {__builtin_amdgcn_readlane(s.q0, i), __builtin_amdgcn_readlane(s.n, i),
+                __builtin_amdgcn_readlane(s.ctx, i), __builtin_amdgcn_readlane(s.slot, i)};
+    }
+};
 
 // One wave's state for QT blocks of 16 rows.
 template <int D, int QT>
@@ -236,19 +247,15 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
 
     for (int base = 0; base < n; base += 64) {
         // lane i: the tile base + i of the wave
-        int tok0 = 0, id = 0;
-        PageScales ps;
+        int tok0 = 0, id = -1;
         const int many = min(n - base, 64);
         if (lane < many) {
             tok0 = tiles.at(t0 + (base + lane) * kWaves) * kTile;
-            if (tok0 < full) {
-                const int e = a.batch.block_table[(int64_t)b * a.batch.table_cols + (tok0 >> a.page_shift)];
-                if (e >= 0 && e < a.cache.pages) {
-                    id = e;
-                    ps.set(a.scale, a.cache.k_scale[(int64_t)e * n_kv + h], a.cache.v_scale[(int64_t)e * n_kv + h]);
-                }
-            }
+            if (tok0 < full) id = a.batch.block_table[(int64_t)b * a.batch.table_cols + (tok0 >> a.page_shift)];
         }
+        const bool there = id >= 0 && id < a.cache.pages;
+        id = there ? id : 0;                                           // a page that is not there: read page 0, weigh it 0
+        const float ks = a.cache.k_scale[(int64_t)id * n_kv + h], vs = a.cache.v_scale[(int64_t)id * n_kv + h];
         const int in_pages = __popcll(__ballot(lane < many && tok0 < full));
 
         u32x4 kr[4][KS], vr[DT];
@@ -279,6 +286,8 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
             load_k(0);
             load_v(0);
         }
+        PageScales ps;                                                 // waits for its loads behind the first tile's
+        if (there) ps.set(a.scale, ks, vs);
         for (int i = 0; i < in_pages; ++i) {
             const int tile0 = __builtin_amdgcn_readlane(tok0, i);
             const float c = lane_value(ps.c1, i);
@@ -374,9 +383,11 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
 // One kv head's work is cut into equal runs of units, one for each worker (a
 // workgroup), whatever the sequences' lengths; a worker's four waves take its
 // tiles in turn and join at the end of each row block.  A row block that one
-// worker has whole is finished there; the others' parts go to the workspace.
-template <int D, int QT>
-__global__ __launch_bounds__(kThreads, QT == 1 && D <= 128 ? 2 : 1) void kv_attend_split_kernel(Args a)
+// worker has whole is finished there; the others' parts go to the workspace: the
+// run's first row block to place 0, its last to place 1.  The worker that has a
+// shared row block's first tile leaves a note for the kernel that joins them.
+template <int D, int QT, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
 {
     constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 16 * QT;
     constexpr int PAD = D + 4;                       // floats a row of the joining buffer: four banks on per row
@@ -384,20 +395,45 @@ __global__ __launch_bounds__(kThreads, QT == 1 && D <= 128 ? 2 : 1) void kv_atte
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, m16 = lane & 15;
     const int h = blockIdx.x % a.cache.n_kv, worker = blockIdx.x / a.cache.n_kv;
 
-    const int64_t units = all_units<RB>(a), used = used_workers(a, units);
-    if (worker >= used) return;
-    int64_t u = units * worker / used;
-    const int64_t end = units * (worker + 1) / used;
-    int b;
-    int64_t off;
-    if (u >= end || !kv_locate(a.batch.batch, u, [&](int i) { return seq_units<RB>(a, i); }, b, off)) return;
+    // how many units there are, and what a worker takes: no less than a tile for each wave
+    Roster<RB> roster;
+    int64_t units = 0;
+    for (int c = 0; c * 64 < a.batch.batch; ++c) {
+        roster.load(a, c);
+        units += kv_lane(roster.end, 63);
+    }
+    int64_t run = (int64_t)((double)units * a.inv_workers);
+    while (run * a.workers < units) ++run;
+    run = max(run, (int64_t)kWaves);
+    int64_t u = run * worker;
+    const int64_t end = min(u + run, units);
+    int note_row = 0, note_rows = 0, note_parts = 0, note_place = 0;
 
-    for (bool fresh = true; u < end && b < a.batch.batch; fresh = false) {
-        KvSeq seq = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
-        if (seq.n == 0) { ++b; off = 0; continue; }
+    // the sequence with unit u
+    int b = a.batch.batch;
+    int64_t off = u;
+    for (int c = 0; u < end && c * 64 < a.batch.batch; ++c) {
+        if (roster.chunk != c) roster.load(a, c);
+        const uint64_t hit = __ballot(off < roster.end);
+        if (hit) {
+            const int i = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+            b = c * 64 + i;
+            off -= kv_lane(roster.end - roster.units, i);
+            break;
+        }
+        off -= kv_lane(roster.end, 63);
+    }
+
+    for (int place = 0; u < end && b < a.batch.batch; place = 1) {
+        if (roster.chunk != b >> 6) roster.load(a, b >> 6);
+        if (off >= kv_lane(roster.units, b & 63)) {          // done with this one, or it has no rows
+            off = 0;
+            ++b;
+            continue;
+        }
+        const KvSeq seq = roster.get(b & 63);
         const Tiles tiles = visible_tiles(a, seq);
-        const int rows = seq.n * a.group, blocks = (rows + RB - 1) / RB;
-        if (off >= (int64_t)blocks * tiles.count) { ++b; off = 0; continue; }
+        const int rows = seq.n * a.group;
         const int rb = (int)(off / tiles.count), t0 = (int)(off - (int64_t)rb * tiles.count);
         const int count = (int)min((int64_t)(tiles.count - t0), end - u);
 
@@ -434,7 +470,13 @@ __global__ __launch_bounds__(kThreads, QT == 1 && D <= 128 ? 2 : 1) void kv_atte
         }
         __syncthreads();
         const bool whole = t0 == 0 && count == tiles.count;
-        const int64_t slot = ((int64_t)worker * 2 + (fresh ? 0 : 1)) * a.cache.n_kv + h;
+        const int64_t slot = ((int64_t)worker * 2 + place) * a.cache.n_kv + h;
+        if (t0 == 0 && !whole) {
+            note_row = seq.q0 * a.group + rb * RB;
+            note_rows = min(RB, rows - rb * RB);
+            note_parts = (int)((u + tiles.count - 1) / run) - worker + 1;
+            note_place = place;
+        }
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             float top = kNone;
@@ -459,17 +501,14 @@ __global__ __launch_bounds__(kThreads, QT == 1 && D <= 128 ? 2 : 1) void kv_atte
                 for (int v = 0; v < kWaves; ++v)
                     l += stat_l[v][t * 16 + row] * __builtin_amdgcn_exp2f(stat_m[v][t * 16 + row] - mm);
                 if (whole) {
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                     const int tok = r / a.group, hq = h * a.group + r - tok * a.group;
-                    const f16x2 x = {(_Float16)(o[0] * inv), (_Float16)(o[1] * inv)};
-                    const f16x2 y = {(_Float16)(o[2] * inv), (_Float16)(o[3] * inv)};
-                    *reinterpret_cast<u32x2 *>(a.out + ((int64_t)(seq.q0 + tok) * a.n_q + hq) * D + ch) =
-                        u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
+                    store_out(a.out + ((int64_t)(seq.q0 + tok) * a.n_q + hq) * D + ch, o, l);
                 } else {
-                    *reinterpret_cast<f32x4 *>(a.part + (slot * RB + t * 16 + row) * D + ch) = o;
+                    const int64_t to = slot * RB + t * 16 + row;
+                    *reinterpret_cast<f32x4 *>(a.part + to * D + ch) = o;
                     if (ch == 0) {
-                        a.stats[(slot * RB + t * 16 + row) * 2] = mm;
-                        a.stats[(slot * RB + t * 16 + row) * 2 + 1] = l;
+                        a.stats[to * 2] = mm;
+                        a.stats[to * 2 + 1] = l;
                     }
                 }
             }
@@ -478,101 +517,54 @@ __global__ __launch_bounds__(kThreads, QT == 1 && D <= 128 ? 2 : 1) void kv_atte
         u += count;
         off += count;
     }
+    if (h == 0 && threadIdx.x == 0) {
+        int32_t *n = a.notes + worker * 4;
+        n[0] = note_row;
+        n[1] = note_rows;
+        n[2] = note_parts;
+        n[3] = note_place;
+    }
 }
 
-// Joins the parts of row blocks that several workers shared: one workgroup per
-// query row and head, eight threads' worth of parts at a time.
+// Joins the parts of a row block that several workers shared: a wave per row,
+// D / 4 lanes side by side, as many parts at a time as the wave has room for.
 template <int D, int QT>
-__global__ __launch_bounds__(kThreads) void kv_join_kernel(Args a)
+__global__ __launch_bounds__(64) void kv_join_kernel(Args a)
 {
-    constexpr int RB = 16 * QT, PER = D / 4, LANES = kThreads / PER;     // parts read side by side
-    __shared__ float sum[LANES][D], sum_l[LANES];
-    const int64_t item = blockIdx.x;
-    const int hq = (int)(item % a.n_q), row_of_call = (int)(item / a.n_q), h = hq / a.group;
-    int b = 0;
-    int64_t off = 0;
-    // the sequence that holds the row
-    const int lane = threadIdx.x & 63;
-    bool found = false;
-    int64_t before = 0, units = 0;
-    for (int c = 0; c < a.batch.batch; c += 64) {
-        const int i = c + lane;
-        int64_t n = 0;
-        bool hit = false;
-        if (i < a.batch.batch) {
-            const KvSeq s = kv_seq(a.batch, i, a.cache.slots, a.page_shift);
-            if (s.n) {
-                n = seq_units<RB>(a, i);
-                hit = row_of_call >= s.q0 && row_of_call < s.q0 + s.n;
-            }
-        }
-        int64_t incl = n;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int64_t up = __shfl_up(incl, o);
-            if (lane >= o) incl += up;
-        }
-        const uint64_t any = __ballot(hit);
-        if (any && !found) {
-            found = true;
-            const int f = __ffsll((unsigned long long)any) - 1;
-            b = c + f;
-            before = units + __shfl(incl - n, f);
-        }
-        units += __shfl(incl, 63);
-    }
-    if (!found) return;
-    const KvSeq seq = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
-    const int count = visible_tiles(a, seq).count;
-    const int r = (row_of_call - seq.q0) * a.group + hq - h * a.group, rb = r / RB;
-    off = before + (int64_t)rb * count;
-    const int64_t used = used_workers(a, units);
-    // the workers that have its units [off, off + count): worker w starts at units * w / used
-    auto owner = [&](int64_t x) {
-        int64_t w = x * used / units;
-        while (units * (w + 1) / used <= x) ++w;
-        while (units * w / used > x) --w;
-        return w;
-    };
-    const int64_t w0 = owner(off), w1 = owner(off + count - 1);
-    if (w0 == w1) return;                                    // one worker had it whole
-    const int part = threadIdx.x / PER, ch = threadIdx.x % PER * 4;
-    auto slot_of = [&](int64_t w) {
-        // a worker's first row block of the run goes to place 0, its last to 1
-        const bool first = w > w0 || units * w / used == off;
-        return ((w * 2 + (first ? 0 : 1)) * a.cache.n_kv + h) * RB + r - rb * RB;
+    constexpr int RB = 16 * QT, PER = D / 4, SIDE = 64 / PER;
+    const int row = blockIdx.x % RB, h = blockIdx.x / RB % a.cache.n_kv, worker = blockIdx.x / RB / a.cache.n_kv;
+    const int32_t *n = a.notes + worker * 4;
+    const int parts = n[2];
+    if (row >= n[1] || parts == 0) return;
+    const int r = n[0] + row, tok = r / a.group, hq = h * a.group + r - tok * a.group, place = n[3];
+    const int lane = threadIdx.x, ch = lane % PER * 4;
+    auto slot = [&](int p) {
+        return (((int64_t)(worker + p) * 2 + (p == 0 ? place : 0)) * a.cache.n_kv + h) * RB + row;
     };
     float m = kNone;
-    for (int64_t w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, a.stats[slot_of(w) * 2]);
+    for (int p = lane; p < parts; p += 64) m = fmaxf(m, a.stats[slot(p) * 2]);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float l = 0.0f;
-    if (part < LANES) {
-        for (int64_t w = w0 + part; w <= w1; w += LANES) {
-            const int64_t s = slot_of(w);
+    if (lane < PER * SIDE) {
+#pragma unroll 8
+        for (int p = lane / PER; p < parts; p += SIDE) {
+            const int64_t s = slot(p);
             const float f = __builtin_amdgcn_exp2f(a.stats[s * 2] - m);
             l += a.stats[s * 2 + 1] * f;
             o += *reinterpret_cast<const f32x4 *>(a.part + s * D + ch) * f;
         }
-        *reinterpret_cast<f32x4 *>(&sum[part][ch]) = o;
-        if (ch == 0) sum_l[part] = l;
     }
-    __syncthreads();
-    if (threadIdx.x < PER) {
-        o = f32x4{0.f, 0.f, 0.f, 0.f};
-        l = 0.0f;
+    f32x4 sum = o;
+    float sum_l = l;
 #pragma unroll
-        for (int i = 0; i < LANES; ++i) {
-            o += *reinterpret_cast<const f32x4 *>(&sum[i][ch]);
-            l += sum_l[i];
-        }
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const f16x2 x = {(_Float16)(o[0] * inv), (_Float16)(o[1] * inv)};
-        const f16x2 y = {(_Float16)(o[2] * inv), (_Float16)(o[3] * inv)};
-        *reinterpret_cast<u32x2 *>(a.out + ((int64_t)row_of_call * a.n_q + hq) * D + ch) =
-            u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
+    for (int i = 1; i < SIDE; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += __shfl(o[e], lane + i * PER);
+        sum_l += __shfl(l, lane + i * PER);
     }
+    if (lane < PER) store_out(a.out + ((int64_t)tok * a.n_q + hq) * D + ch, sum, sum_l);
 }
 
 // Many rows of a sequence: a workgroup of NW waves holds 32 NW rows (a wave two
@@ -757,14 +749,8 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
         const int tok = r / a.group;
         const int64_t at_out = (int64_t)(seq.q0 + tok) * a.n_q + h * a.group + r - tok * a.group;
         if (splits == 1) {
-            const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const f16x2 x = {(_Float16)(o[t][d][0] * f), (_Float16)(o[t][d][1] * f)};
-                const f16x2 y = {(_Float16)(o[t][d][2] * f), (_Float16)(o[t][d][3] * f)};
-                *reinterpret_cast<u32x2 *>(a.out + at_out * D + d * 16 + g * 4) =
-                    u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
-            }
+            for (int d = 0; d < DT; ++d) store_out(a.out + at_out * D + d * 16 + g * 4, o[t][d], sum);
         } else {
             const int64_t slot = at_out * splits + split;
 #pragma unroll
@@ -803,10 +789,11 @@ __global__ __launch_bounds__(kThreads) void kv_join_rows_kernel(Args a, int spli
         l += a.stats[(row * splits + p) * 2 + 1] * f;
         o += *reinterpret_cast<const f32x4 *>(a.part + (row * splits + p) * D + ch) * f;
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const f16x2 x = {(_Float16)(o[0] * inv), (_Float16)(o[1] * inv)}, y = {(_Float16)(o[2] * inv), (_Float16)(o[3] * inv)};
-    *reinterpret_cast<u32x2 *>(a.out + row * D + ch) = u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
+    store_out(a.out + row * D + ch, o, l);
 }
+
+// Waves per SIMD that the split kernel's registers allow.
+constexpr int split_occupancy(int d, int qt) { return d <= 64 || (d <= 128 && qt == 1) ? 2 : 1; }
 
 // How a call is run.  qt > 0: the split kernel with qt blocks of 16 rows, as many
 // as an average sequence fills.  qt == 0: the rows kernel with `waves` waves and
@@ -822,7 +809,8 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d)
     const int64_t group = n_q / n_kv, rows = (tokens + batch - 1) / batch * group;
     if (rows <= (d <= 128 ? 32 : 16)) {
         p.qt = rows <= 16 ? 1 : 2;
-        p.workers = n_kv < 512 ? (512 + n_kv - 1) / n_kv : 1;    // two workgroups per CU: 512 on the 256 CUs
+        const int groups = 256 * split_occupancy(d, p.qt);       // workgroups that the 256 CUs hold at once
+        p.workers = n_kv < groups ? (groups + n_kv - 1) / n_kv : 1;
         p.parts = (int64_t)p.workers * n_kv * 2 * 16 * p.qt;
         return p;
     }
@@ -839,10 +827,11 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d)
 template <int D, int QT>
 hipError_t launch_split(const Args &a, hipStream_t stream)
 {
-    kv_attend_split_kernel<D, QT><<<(unsigned)(a.workers * a.cache.n_kv), kThreads, 0, stream>>>(a);
+    const unsigned groups = (unsigned)(a.workers * a.cache.n_kv);
+    kv_attend_split_kernel<D, QT, split_occupancy(D, QT)><<<groups, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    kv_join_kernel<D, QT><<<(unsigned)(a.batch.tokens * a.n_q), kThreads, 0, stream>>>(a);
+    kv_join_kernel<D, QT><<<groups * 16 * QT, 64, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -878,7 +867,8 @@ hipError_t launch(const Args &a, const Plan &p, hipStream_t stream)
 
 int64_t kv_attention_workspace(int64_t tokens, int batch, int n_q, int n_kv, int d)
 {
-    return plan_for(tokens, batch, n_q, n_kv, d).parts * (d + 2) * 4 + 16;
+    const Plan p = plan_for(tokens, batch, n_q, n_kv, d);
+    return p.parts * (d + 2) * 4 + (int64_t)(p.workers + 1) * 16;
 }
 
 hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch &batch, const uint16_t *q,
@@ -887,8 +877,10 @@ hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch
 {
     const Plan p = plan_for(batch.tokens, batch.batch, n_q, cache.n_kv, cache.d);
     float *part = (float *)workspace;
+    float *stats = part + p.parts * cache.d;
     const Args a = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, window, sinks,
-                    __builtin_ctz(cache.page), p.workers, part + p.parts * cache.d, part, out};
+                    __builtin_ctz(cache.page), p.workers, p.workers ? 1.0 / p.workers : 0.0, part, stats,
+                    reinterpret_cast<int32_t *>(stats + p.parts * 2), out};
     switch (cache.d) {
     case 64: return launch<64>(a, p, stream);
     case 96: return launch<96>(a, p, stream);

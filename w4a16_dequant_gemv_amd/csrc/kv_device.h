@@ -59,6 +59,34 @@ __device__ __forceinline__ KvSeq kv_seq(const kv_paged_batch &p, int b, int64_t 
     return s;
 }
 
+// Inclusive sum over the lanes of a wave: row shifts, then broadcasts of the
+// last lane of a row of 16 and of the first half, all on the VALU.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t kv_scan_step(int64_t v)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+    return v + (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ int64_t kv_wave_scan(int64_t v)
+{
+    v = kv_scan_step<0x111, 0xF>(v);       // row_shr:1
+    v = kv_scan_step<0x112, 0xF>(v);       // row_shr:2
+    v = kv_scan_step<0x114, 0xF>(v);       // row_shr:4
+    v = kv_scan_step<0x118, 0xF>(v);       // row_shr:8
+    v = kv_scan_step<0x142, 0xA>(v);       // row_bcast:15 into rows 1 and 3
+    return kv_scan_step<0x143, 0xC>(v);    // row_bcast:31 into rows 2 and 3
+}
+
+// The value of v in lane i, the same i in every lane.
+__device__ __forceinline__ int64_t kv_lane(int64_t v, int i)
+{
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, i);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), i);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Finds which of the batch's sequences item `u` falls in when sequence b has
 // count(b) items: every lane of a wave calls it, 64 sequences a step.  False if
 // there are not that many.
@@ -68,21 +96,15 @@ __device__ __forceinline__ bool kv_locate(int batch, int64_t u, F count, int &b,
     const int lane = threadIdx.x & 63;
     int64_t base = 0;
     for (int c = 0; c < batch; c += 64) {
-        const int64_t n = c + lane < batch ? (int64_t)count(c + lane) : 0;
-        int64_t incl = n;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int64_t up = __shfl_up(incl, o);
-            if (lane >= o) incl += up;
-        }
+        const int64_t n = c + lane < batch ? (int64_t)count(c + lane) : 0, incl = kv_wave_scan(n);
         const uint64_t hit = __ballot(u < base + incl);
         if (hit) {
-            const int f = __ffsll((unsigned long long)hit) - 1;
+            const int f = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
             b = c + f;
-            off = u - base - __shfl(incl - n, f);
+            off = u - base - kv_lane(incl - n, f);
             return true;
         }
-        base += __shfl(incl, 63);
+        base += kv_lane(incl, 63);
     }
     return false;
 }

@@ -7,6 +7,7 @@ Only argument marshalling happens here: tensors must already live on the GPU
 and the library does all of the arithmetic on torch's current stream.
 """
 import contextlib
+import operator
 from ctypes import byref
 
 import torch
@@ -192,6 +193,7 @@ class PagedKVCache:
         if pool_pages < 1 or slots < 1 or not 1 <= n_kv <= 1024:
             raise W4A16Error("pool_pages and slots must be positive, n_kv in [1, 1024]")
         self.n_kv, self.d, self.page = n_kv, d, page
+        self._known = None
         kshape, vshape = self._shapes()
         self.k = torch.zeros((pool_pages, *kshape), dtype=torch.int8, device=device)
         self.v = torch.zeros((pool_pages, *vshape), dtype=torch.int8, device=device)
@@ -213,7 +215,11 @@ class PagedKVCache:
         return self.k_tail.shape[0]
 
     def _checked(self):
-        """The six tensors, checked, as the library's struct."""
+        """The six tensors as the library's struct, checked when one was replaced."""
+        now = (self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
+        at = [t.data_ptr() for t in now]
+        if self._known is not None and at == self._known[1] and all(map(operator.is_, now, self._known[0])):
+            return self._known[2]
         kshape, vshape = self._shapes()
         P, S = self.pool_pages, self.slots
         _need(self.k, torch.int8, (P, *kshape), "k")
@@ -223,8 +229,8 @@ class PagedKVCache:
         _need(self.k_tail, torch.float16, (S, 2, *kshape), "k_tail")
         _need(self.v_tail, torch.float16, (S, 2, *vshape), "v_tail")
         _same_device(self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
-        return _lib.PagedCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                               self.k_tail.data_ptr(), self.v_tail.data_ptr(), P, S, self.n_kv, self.d, self.page)
+        self._known = now, at, _lib.PagedCache(*at, P, S, self.n_kv, self.d, self.page)
+        return self._known[2]
 
     def append(self, k, v, batch, q=None, rope=None, positions=None, interleaved=False, q_out=None):
         """Put fp16 k, v [T, n_kv, d] behind each sequence's ctx_lens tokens; with
