@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kTile = 64;                  // tokens
+constexpr int kStart = 4;                  // what a row block's beginning costs, in tiles
 constexpr float kNone = -1e30f;            // running maximum before any token: below every score
 constexpr float kLift = 14.0f;             // P is at most 2^14: fp16 keeps weights down to 2^-28 of the largest normal
 
@@ -115,8 +116,9 @@ __device__ __forceinline__ Tiles visible_tiles(const Args &a, const KvSeq &s)
 }
 
 // The split kernel's work as numbered units: sequence after sequence, its row
-// blocks of RB rows one after the other, each with the sequence's tiles.  Lane i
-// of a wave holds sequence 64 chunk + i.
+// blocks of RB rows one after the other, each with kStart units for the latency
+// of beginning it and then one for each of the sequence's tiles.  Lane i of a
+// wave holds sequence 64 chunk + i.
 template <int RB>
 struct Roster {
     int chunk = -1;
@@ -131,7 +133,7 @@ struct Roster {
         s = {0, 0, 0, 0};
         if (b < a.batch.batch) {
             s = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
-            if (s.n) units = (int64_t)((s.n * a.group + RB - 1) / RB) * visible_tiles(a, s).count;
+            if (s.n) units = (int64_t)((s.n * a.group + RB - 1) / RB) * (visible_tiles(a, s).count + kStart);
         }
         end = kv_wave_scan(units);
     }
@@ -424,7 +426,7 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         off -= kv_lane(roster.end, 63);
     }
 
-    for (int place = 0; u < end && b < a.batch.batch; place = 1) {
+    for (int place = 0; u < end && b < a.batch.batch;) {
         if (roster.chunk != b >> 6) roster.load(a, b >> 6);
         if (off >= kv_lane(roster.units, b & 63)) {          // done with this one, or it has no rows
             off = 0;
@@ -434,8 +436,13 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         const KvSeq seq = roster.get(b & 63);
         const Tiles tiles = visible_tiles(a, seq);
         const int rows = seq.n * a.group;
-        const int rb = (int)(off / tiles.count), t0 = (int)(off - (int64_t)rb * tiles.count);
-        const int count = (int)min((int64_t)(tiles.count - t0), end - u);
+        const int per_block = tiles.count + kStart, rb = (int)(off / per_block), at = (int)(off - (int64_t)rb * per_block);
+        const int take = (int)min((int64_t)(per_block - at), end - u);
+        const int t0 = max(at - kStart, 0), count = max(at + take - kStart, 0) - t0;
+        const int64_t last = u - at + per_block - 1;         // the row block's last unit
+        u += take;
+        off += take;
+        if (count == 0) continue;                            // only the beginning is this worker's
 
         Wave<D, QT> s;
 #pragma unroll
@@ -474,7 +481,7 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         if (t0 == 0 && !whole) {
             note_row = seq.q0 * a.group + rb * RB;
             note_rows = min(RB, rows - rb * RB);
-            note_parts = (int)((u + tiles.count - 1) / run) - worker + 1;
+            note_parts = (int)(last / run) - worker + 1;
             note_place = place;
         }
 #pragma unroll
@@ -514,8 +521,7 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
             }
             __syncthreads();
         }
-        u += count;
-        off += count;
+        place = 1;
     }
     if (h == 0 && threadIdx.x == 0) {
         int32_t *n = a.notes + worker * 4;
@@ -526,36 +532,67 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
     }
 }
 
-// Joins the parts of a row block that several workers shared: a wave per row,
-// D / 4 lanes side by side, as many parts at a time as the wave has room for.
-template <int D, int QT>
-__global__ __launch_bounds__(64) void kv_join_kernel(Args a)
+// Joins the parts of a row block that several workers shared: a workgroup per
+// row, D / 4 lanes side by side, the parts dealt out to its NW waves and to as
+// many places in a wave as there is room for.
+template <int D, int QT, int NW>
+__global__ __launch_bounds__(64 * NW) void kv_join_kernel(Args a)
 {
     constexpr int RB = 16 * QT, PER = D / 4, SIDE = 64 / PER;
+    __shared__ float wave_m[NW], wave_l[NW];
+    __shared__ f32x4 wave_o[NW][PER];
     const int row = blockIdx.x % RB, h = blockIdx.x / RB % a.cache.n_kv, worker = blockIdx.x / RB / a.cache.n_kv;
     const int32_t *n = a.notes + worker * 4;
     const int parts = n[2];
     if (row >= n[1] || parts == 0) return;
     const int r = n[0] + row, tok = r / a.group, hq = h * a.group + r - tok * a.group, place = n[3];
-    const int lane = threadIdx.x, ch = lane % PER * 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = lane % PER * 4;
     auto slot = [&](int p) {
         return (((int64_t)(worker + p) * 2 + (p == 0 ? place : 0)) * a.cache.n_kv + h) * RB + row;
     };
-    float m = kNone;
-    for (int p = lane; p < parts; p += 64) m = fmaxf(m, a.stats[slot(p) * 2]);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.0f;
+    float m = kNone, l = 0.0f;
     if (lane < PER * SIDE) {
-#pragma unroll 8
-        for (int p = lane / PER; p < parts; p += SIDE) {
-            const int64_t s = slot(p);
-            const float f = __builtin_amdgcn_exp2f(a.stats[s * 2] - m);
-            l += a.stats[s * 2 + 1] * f;
-            o += *reinterpret_cast<const f32x4 *>(a.part + s * D + ch) * f;
+        // eight parts on their way at a time, each group against its own maximum
+        for (int p0 = wave * SIDE + lane / PER; p0 < parts; p0 += 8 * NW * SIDE) {
+            f32x4 x[8];
+            float pm[8], pl[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int p = p0 + i * NW * SIDE;
+                pm[i] = kNone;
+                pl[i] = 0.0f;
+                x[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (p < parts) {
+                    const int64_t s = slot(p);
+                    pm[i] = a.stats[s * 2];
+                    pl[i] = a.stats[s * 2 + 1];
+                    x[i] = *reinterpret_cast<const f32x4 *>(a.part + s * D + ch);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, pm[i]);
+            const float keep = __builtin_amdgcn_exp2f(m - top);
+            o *= keep;
+            l *= keep;
+            m = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = __builtin_amdgcn_exp2f(pm[i] - m);
+                o += x[i] * f;
+                l += pl[i] * f;
+            }
         }
     }
+    // the places of a wave, then the waves
+    float top = m;
+#pragma unroll
+    for (int i = 1; i < SIDE; ++i) top = fmaxf(top, __shfl(m, (lane % PER) + i * PER));
+    top = fmaxf(top, __shfl(m, lane % PER));
+    const float f = __builtin_amdgcn_exp2f(m - top);
+    o *= f;
+    l *= f;
     f32x4 sum = o;
     float sum_l = l;
 #pragma unroll
@@ -564,7 +601,27 @@ __global__ __launch_bounds__(64) void kv_join_kernel(Args a)
         for (int e = 0; e < 4; ++e) sum[e] += __shfl(o[e], lane + i * PER);
         sum_l += __shfl(l, lane + i * PER);
     }
-    if (lane < PER) store_out(a.out + ((int64_t)tok * a.n_q + hq) * D + ch, sum, sum_l);
+    if (lane < PER) {
+        wave_o[wave][lane] = sum;
+        if (lane == 0) {
+            wave_m[wave] = top;
+            wave_l[wave] = sum_l;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x >= PER) return;
+    top = kNone;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) top = fmaxf(top, wave_m[v]);
+    sum = f32x4{0.f, 0.f, 0.f, 0.f};
+    sum_l = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) {
+        const float w = __builtin_amdgcn_exp2f(wave_m[v] - top);
+        sum += wave_o[v][lane] * w;
+        sum_l += wave_l[v] * w;
+    }
+    store_out(a.out + ((int64_t)tok * a.n_q + hq) * D + ch, sum, sum_l);
 }
 
 // Many rows of a sequence: a workgroup of NW waves holds 32 NW rows (a wave two
@@ -831,7 +888,9 @@ hipError_t launch_split(const Args &a, hipStream_t stream)
     kv_attend_split_kernel<D, QT, split_occupancy(D, QT)><<<groups, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    kv_join_kernel<D, QT><<<groups * 16 * QT, 64, 0, stream>>>(a);
+    // with 16 parts a sequence or more, four waves join a row
+    if (a.workers >= 16 * a.batch.batch) kv_join_kernel<D, QT, 4><<<groups * 16 * QT, 256, 0, stream>>>(a);
+    else kv_join_kernel<D, QT, 1><<<groups * 16 * QT, 64, 0, stream>>>(a);
     return hipGetLastError();
 }
 
