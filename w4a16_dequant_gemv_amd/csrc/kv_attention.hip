@@ -26,7 +26,8 @@ constexpr int kThreads = 256, kWaves = 4;
 constexpr int kTile = 64;                  // tokens
 constexpr int kStart = 4;                  // what a row block's beginning costs, in tiles
 constexpr float kNone = -1e30f;            // running maximum before any token: below every score
-constexpr float kLift = 14.0f;             // P is at most 2^14: fp16 keeps weights down to 2^-28 of the largest normal
+constexpr float kSlack = 5.0f;             // a query's maximum is raised only by more than this many powers of two,
+constexpr float kLift = 10.0f;             // so P is at most 2^15 and fp16 keeps weights down to 2^-24 of that at least
 
 // 16 codes of a lane as two operands, channel or token order kept.  The byte
 // c + 128 under the exponent of 1024 is the fp16 value 1152 + c, exactly.
@@ -154,60 +155,70 @@ struct Wave {
     int at[QT];                  // the row's index in its sequence
 };
 
-// Scores x[a][i] of one query (row index `at`) to weights: masks, the running
-// maximum, P in fp16 and, with SPLIT, the rest of P beside it.  c1 = scale
-// log2(e) ks > 0, w = log2(vs), inv = 1 / vs.  Returns the factor that what was
-// summed before has to be multiplied with.
-template <bool SPLIT>
-__device__ __forceinline__ float weights(f32x4 x[4], const Args &a, int at, bool masked, int tile0, float c1, float w,
-                                         float inv, float &m_run, float &l_run, f16x8 hi[2], f16x8 lo[2])
+// Scores x[a][i] of one query (row index `at`): those of tokens that it does not
+// see become -inf.
+__device__ __forceinline__ void hide(f32x4 x[4], const Args &a, int at, int tile0)
 {
     const int g = (threadIdx.x & 63) >> 4;
-    if (masked) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int tok = tile0 + 16 * g + 4 * i + j;
-                const bool see = tok <= at && (a.window == 0 || at - tok < a.window || tok < a.sinks);
-                x[i][j] = see ? x[i][j] : -INFINITY;
-            }
-    }
+        for (int j = 0; j < 4; ++j) {
+            const int tok = tile0 + 16 * g + 4 * i + j;
+            const bool see = tok <= at && (a.window == 0 || at - tok < a.window || tok < a.sinks);
+            x[i][j] = see ? x[i][j] : -INFINITY;
+        }
+}
+
+// Scores to weights.  First the running maximum, which follows the scores only
+// in steps (each step costs a pass over O); returns the factor for what was
+// summed before, 1 nearly always.  c1 = scale log2(e) ks > 0, w = log2(vs).
+__device__ __forceinline__ float weigh_max(const f32x4 x[4], float c1, float w, float &m_run)
+{
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) top = fmaxf(top, x[i][j]);
-    const float m = fmaxf(m_run, column_max(top) * c1 + w);
+    const float now = column_max(top) * c1 + w, m = now > m_run + kSlack ? now : m_run;
     const float keep = __builtin_amdgcn_exp2f(m_run - m);
     m_run = m;
-    const float add = w - m + kLift;
-    float sum = 0.0f;
+    return keep;
+}
+
+// Then P in fp16, and where `lo` is given the rest of P there, for the tokens of
+// the second product's step `half`; sum gets this lane's sum of P.  add = w - m +
+// kLift.
+__device__ __forceinline__ void weigh_exp(const f32x4 x[4], int half, float c1, float add, f16x8 hi[2], float &sum,
+                                          f16x8 *lo = nullptr)
+{
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(x[i][j] * c1 + add);
-            const float p1 = __builtin_amdgcn_exp2f(x[i][j + 1] * c1 + add);
+            const float p0 = __builtin_amdgcn_exp2f(x[2 * half + i][j] * c1 + add);
+            const float p1 = __builtin_amdgcn_exp2f(x[2 * half + i][j + 1] * c1 + add);
             sum += p0 + p1;
             const f16x2 h = {(_Float16)p0, (_Float16)p1};
-            const int at8 = (i & 1) * 4 + j;
-            hi[i >> 1][at8] = h[0];
-            hi[i >> 1][at8 + 1] = h[1];
-            if (SPLIT) {
-                lo[i >> 1][at8] = (_Float16)(p0 - (float)h[0]);
-                lo[i >> 1][at8 + 1] = (_Float16)(p1 - (float)h[1]);
+            hi[half][i * 4 + j] = h[0];
+            hi[half][i * 4 + j + 1] = h[1];
+            if (lo) {
+                lo[half][i * 4 + j] = (_Float16)(p0 - (float)h[0]);
+                lo[half][i * 4 + j + 1] = (_Float16)(p1 - (float)h[1]);
             }
         }
-    l_run = l_run * keep + sum * inv;
-    return keep;
 }
 
 template <int D, int QT>
 __device__ __forceinline__ void weigh(Wave<D, QT> &s, int t, f32x4 x[4], const Args &a, bool masked, int tile0, float c1,
                                       float w, float inv, f16x8 hi[2], f16x8 lo[2])
 {
-    const float keep = weights<true>(x, a, s.at[t], masked, tile0, c1, w, inv, s.m[t], s.l[t], hi, lo);
+    if (masked) hide(x, a, s.at[t], tile0);
+    const float keep = weigh_max(x, c1, w, s.m[t]);
+    float sum = 0.0f;
+    weigh_exp(x, 0, c1, w - s.m[t] + kLift, hi, sum, lo);
+    weigh_exp(x, 1, c1, w - s.m[t] + kLift, hi, sum, lo);
+    s.l[t] = s.l[t] * keep + sum * inv;
     if (__ballot(keep != 1.0f)) {
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) s.o[t][d] *= keep;
@@ -394,7 +405,8 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
     constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 16 * QT;
     constexpr int PAD = D + 4;                       // floats a row of the joining buffer: four banks on per row
     __shared__ float joint[kWaves][16 * PAD], stat_m[kWaves][RB], stat_l[kWaves][RB];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, m16 = lane & 15;
+    const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);          // a scalar: its branches are uniform
     const int h = blockIdx.x % a.cache.n_kv, worker = blockIdx.x / a.cache.n_kv;
 
     // how many units there are, and what a worker takes: no less than a tile for each wave
@@ -627,8 +639,12 @@ __global__ __launch_bounds__(64 * NW) void kv_join_kernel(Args a)
 // Many rows of a sequence: a workgroup of NW waves holds 32 NW rows (a wave two
 // blocks of 16) and walks the tiles they see; each tile is converted to fp16
 // once, into LDS, in the order of the operands (a wave reads 1 KiB in a row).
-// Two buffers: while one tile is multiplied, the next is written and the one
-// after it is on its way in registers.  With few row blocks the tiles are cut
+// Two buffers each for K and V; the tiles after them are on their way in registers.
+// A wave's matrix work (a tile's scores, the last one's second product) and its
+// vector work (weights, conversion of tiles) do not overlap by themselves, and
+// waves that meet at barriers do the same at the same time; so with eight waves
+// the two that share a SIMD take turns: waves 4 .. 7 run half a tile behind, and
+// each barrier hands the matrix cores to the other wave.  With few row blocks the tiles are cut
 // into `splits` runs and joined by kv_join_rows_kernel.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kernel(Args a, int splits)
@@ -636,8 +652,10 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
     constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 32 * NW, THREADS = 64 * NW;
     constexpr int UNITS = 4 * D, UN = (UNITS + THREADS - 1) / THREADS;     // 16-byte units of a tile's K (and V)
     constexpr int KF = 8 * KS, VF = 2 * DT;                                // operands of 1 KiB
-    extern __shared__ f16x8 tile[];                        // [2][KF + VF][64]
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, m16 = lane & 15;
+    extern __shared__ f16x8 k_tile[];                      // [2][KF][64], then V's [2][VF][64]
+    f16x8 *v_tile = k_tile + 2 * KF * 64;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);                  // a scalar: its branches are uniform
     const int n_kv = a.cache.n_kv, page = 1 << a.page_shift, head = page * D;
     const int h = blockIdx.x % n_kv, split = blockIdx.x / n_kv % splits;
     int b;
@@ -653,7 +671,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
 
     // this wave's rows
     const int first = row0 + wave * 32;
-    const bool live = first < rows;
+    const int turn = NW > 4 && wave >= 4 ? 1 : 0;
     const int at_min = seq.ctx + first / a.group, at_max = seq.ctx + (min(first + 32, rows) - 1) / a.group;
     f16x8 q[2][2 * KS];
     f32x4 o[2][DT];
@@ -677,125 +695,200 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
         }
     }
     if (D % 64 != 0) {                                     // channels that a last K operand has beyond D
-        for (int i = tid; i < 2 * (KF + VF) * 64; i += THREADS) tile[i] = f16x8{};
+        for (int i = tid; i < 2 * KF * 64; i += THREADS) k_tile[i] = f16x8{};
         __syncthreads();
     }
 
-    for (int base = t0; base < t1; base += 64) {
-        const int many = min(t1 - base, 64);
-        int tok0 = 0, id = 0;
-        PageScales ps;
-        if (lane < many) {
-            tok0 = tiles.at(base + lane) * kTile;
-            if (tok0 >= full) {
-                ps.set(a.scale, 1.0f, 1.0f);
-            } else {
-                const int e = a.batch.block_table[(int64_t)b * a.batch.table_cols + (tok0 >> a.page_shift)];
-                if (e >= 0 && e < a.cache.pages) {
-                    id = e;
-                    ps.set(a.scale, a.cache.k_scale[(int64_t)e * n_kv + h], a.cache.v_scale[(int64_t)e * n_kv + h]);
+    // Four operands each: for K tiles a = 2 jp, 2 jp + 1 of 16 tokens and 64 channels,
+    // for V 32 channels.
+    auto read_k = [&](int i, int n, f16x8 f[4]) {
+        const f16x8 *from = k_tile + (i & 1) * KF * 64 + lane;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = from[((n / KS * 2 + (e >> 1)) * 2 * KS + n % KS * 2 + (e & 1)) * 64];
+    };
+    auto read_v = [&](int i, int n, f16x8 f[4]) {
+        const f16x8 *from = v_tile + (i & 1) * VF * 64 + n * 256 + lane;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = from[e * 64];
+    };
+    // where unit u of a tile goes
+    auto k_place = [&](int i, int unit) {
+        const int c = unit / 16 % DT, ka = unit / 16 / DT;
+        return k_tile + (i & 1) * KF * 64 + (ka * KS + (c >> 2)) * 128 + (c & 3) * 16 + (unit & 15);
+    };
+    auto v_place = [&](int i, int unit) {
+        const int ch = unit % D;
+        return v_tile + (i & 1) * VF * 64 + ch / 16 * 128 + unit / D * 16 + (ch & 15);
+    };
+    f32x4 x[2][4];
+    f16x8 p[2][2];
+    // O += P V of tile i - 1, and the scores of tile i.  Operands are read ahead, and
+    // an accumulator comes up again after three others.  `between` is run twice, after two
+    // pieces of the scores.
+    auto matrix_work = [&](int i, bool second, bool first, auto between) {
+        constexpr int VP = DT / 2, NP = VP + 2 * KS, AHEAD = D <= 128 ? 2 : 1;
+        f16x8 f[AHEAD + 1][4];
+        auto fetch = [&](int n) {
+            if (n < VP) { if (second) read_v(i - 1, n, f[n % (AHEAD + 1)]); }
+            else if (n < NP) { if (first) read_k(i, n - VP, f[n % (AHEAD + 1)]); }
+        };
+        __builtin_amdgcn_s_setprio(1);                     // before the SIMD's other wave, whose work is long enough
+#pragma unroll
+        for (int n = second ? 0 : VP, k = 0; k < AHEAD; ++k) fetch(n + k);
+#pragma unroll
+        for (int n = second ? 0 : VP; n < (first ? NP : VP); ++n) {
+            fetch(n + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int one = e & 1, half = e >> 1;                  // operand 2 one + half
+                const f16x8 v = f[n % (AHEAD + 1)][2 * one + half];
+                if (n < VP) {
+                    o[0][2 * n + one] = mfma(v, p[0][half], o[0][2 * n + one]);
+                    o[1][2 * n + one] = mfma(v, p[1][half], o[1][2 * n + one]);
+                } else {
+                    const int j = (n - VP) / KS * 2 + one, c = (n - VP) % KS * 2 + half;
+                    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                    x[0][j] = mfma(v, q[0][c], c == 0 ? zero : x[0][j]);
+                    x[1][j] = mfma(v, q[1][c], c == 0 ? zero : x[1][j]);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
+            if (n == NP - (KS == 1 ? 2 : 4)) between(0);
+            if (n == NP - (KS == 1 ? 1 : 2)) between(1);
         }
-        const int in_pages = __popcll(__ballot(lane < many && tok0 < full));
+        __builtin_amdgcn_s_setprio(0);
+    };
+    // x to p
+    auto vector_work = [&](int tile0, float c1, float w, float inv) {
+        if (tile0 + kTile - 1 > at_min || (a.window > 0 && at_max - tile0 >= a.window && tile0 + kTile > a.sinks)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) hide(x[t], a, at[t], tile0);
+        }
+        float keep[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            keep[t] = weigh_max(x[t], c1, w, m[t]);
+            const float add = w - m[t] + kLift;
+            float sum = 0.0f;
+            weigh_exp(x[t], 0, c1, add, p[t], sum);
+            weigh_exp(x[t], 1, c1, add, p[t], sum);
+            l[t] = l[t] * keep[t] + sum * inv;
+        }
+        if (__ballot(keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[t][d] *= keep[t];
+        }
+    };
 
+    // finished pages
+    int base = t0;
+    for (bool more = true; more && base < t1;) {
+        int tok0 = 0, id = -1;
+        if (base + lane < t1) {
+            tok0 = tiles.at(base + lane) * kTile;
+            if (tok0 < full) id = a.batch.block_table[(int64_t)b * a.batch.table_cols + (tok0 >> a.page_shift)];
+        }
+        const int many = __popcll(__ballot(base + lane < t1 && tok0 < full));
+        if (many == 0) break;
+        const bool there = id >= 0 && id < a.cache.pages;
+        id = there ? id : 0;                               // a page that is not there: read page 0, weigh it 0
+        PageScales ps;
+        if (there) ps.set(a.scale, a.cache.k_scale[(int64_t)id * n_kv + h], a.cache.v_scale[(int64_t)id * n_kv + h]);
+        const int64_t at0 = ((int64_t)id * n_kv + h) * head + (tok0 & (page - 1)) * D;
+
+        // tile i's codes into registers, and from there into its buffer; behind the last
+        // tile the last one once more, which nothing reads
         u32x4 kr[UN], vr[UN];
-        auto load = [&](int i) {                           // a tile of a finished page, into registers
-            const int64_t at0 = ((int64_t)__builtin_amdgcn_readlane(id, i) * n_kv + h) * head +
-                                (__builtin_amdgcn_readlane(tok0, i) & (page - 1)) * D;
+        auto load = [&](const int8_t *pool, int i, u32x4 r[UN]) {
+            const int8_t *from = pool + kv_lane(at0, min(i, many - 1)) + tid * 16;
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
+                if (UNITS % THREADS == 0 || tid + u * THREADS < UNITS)
+                    r[u] = *reinterpret_cast<const u32x4 *>(from + u * THREADS * 16);
+        };
+        auto put_k = [&](int i) {
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
                 if (UNITS % THREADS != 0 && tid + u * THREADS >= UNITS) continue;
-                kr[u] = *reinterpret_cast<const u32x4 *>(a.cache.k + at0 + (tid + u * THREADS) * 16);
-                vr[u] = *reinterpret_cast<const u32x4 *>(a.cache.v + at0 + (tid + u * THREADS) * 16);
+                f16x8 lo, hi, *to = k_place(i, tid + u * THREADS);
+                codes_to_half(kr[u], lo, hi);
+                to[0] = lo;
+                to[64] = hi;
             }
         };
-        auto put = [&](int i) {                            // tile i into its buffer
-            f16x8 *to = tile + (i & 1) * (KF + VF) * 64;
+        auto put_v = [&](int i) {
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
-                const int unit = tid + u * THREADS;
-                if (UNITS % THREADS != 0 && unit >= UNITS) continue;
-                const int c = unit / 16 % DT, ka = unit / 16 / DT, kl = (c & 3) * 16 + (unit & 15);
-                const int ch = unit % D, vl = unit / D * 16 + (ch & 15);
-                f16x8 k0, k1, v0, v1;
-                if (i < in_pages) {
-                    codes_to_half(kr[u], k0, k1);
-                    codes_to_half(vr[u], v0, v1);
-                } else {
-                    const int tile0 = __builtin_amdgcn_readlane(tok0, i);
-                    const int64_t at0 = (((int64_t)seq.slot * 2 + (tile0 >> a.page_shift & 1)) * n_kv + h) * head +
-                                        (tile0 & (page - 1)) * D + unit * 16;
-                    const f16x8 *kp = reinterpret_cast<const f16x8 *>(a.cache.k_tail + at0);
-                    const u32x4 *vp = reinterpret_cast<const u32x4 *>(a.cache.v_tail + at0);
-                    k0 = kp[0];
-                    k1 = kp[1];
-                    // places behind the last token hold anything: zero them, 0 * NaN is not 0
-                    const int left = seq.total() - tile0 - 16 * (unit / D);
-                    u32x4 x = vp[0], y = vp[1];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[e] &= left >= 2 * e + 2 ? 0xFFFFFFFFu : left == 2 * e + 1 ? 0xFFFFu : 0u;
-                        y[e] &= left >= 2 * e + 10 ? 0xFFFFFFFFu : left == 2 * e + 9 ? 0xFFFFu : 0u;
-                    }
-                    v0 = bitcast<f16x8>(x);
-                    v1 = bitcast<f16x8>(y);
-                }
-                f16x8 *kt = to + ((ka * KS + (c >> 2)) * 2) * 64 + kl;
-                kt[0] = k0;
-                kt[64] = k1;
-                f16x8 *vt = to + (KF + ch / 16 * 2) * 64 + vl;
-                vt[0] = v0;
-                vt[64] = v1;
+                if (UNITS % THREADS != 0 && tid + u * THREADS >= UNITS) continue;
+                f16x8 lo, hi, *to = v_place(i, tid + u * THREADS);
+                codes_to_half(vr[u], lo, hi);
+                to[0] = lo;
+                to[64] = hi;
+            }
+        };
+        // the tiles after tile i, in two parts of its matrix work
+        auto move_on = [&](int i, int part) {
+            if (part == 0) {
+                put_k(i + 1);
+                load(a.cache.k, i + 2, kr);
+            }
+            if (part == 1) {
+                put_v(i);
+                load(a.cache.v, i + 1, vr);
             }
         };
 
-        if (in_pages > 0) load(0);
-        __syncthreads();                                   // the last batch of tiles has been read
-        put(0);
-        if (in_pages > 1) load(1);
+        load(a.cache.k, 0, kr);
+        load(a.cache.v, 0, vr);
+        __syncthreads();                                   // the tiles before have been read
+        put_k(0);
+        load(a.cache.k, 1, kr);
+        __syncthreads();
+        if (turn) __syncthreads();
+        matrix_work(0, false, true, [&](int part) { move_on(0, part); });
         __syncthreads();
         for (int i = 0; i < many; ++i) {
-            const int tile0 = __builtin_amdgcn_readlane(tok0, i);
-            const f16x8 *from = tile + (i & 1) * (KF + VF) * 64 + lane;
-            const bool see = live && tile0 <= at_max;
-            if (see) {
-                const float c1 = lane_value(ps.c1, i), w = lane_value(ps.w, i), inv = lane_value(ps.inv, i);
-                const bool masked = tile0 + kTile - 1 > at_min ||
-                                    (a.window > 0 && at_max - tile0 >= a.window && tile0 + kTile > a.sinks);
-                f32x4 x[2][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[0][j] = x[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 2 * KS; ++e) {
-                        const f16x8 k = from[(j * 2 * KS + e) * 64];
-                        x[0][j] = mfma(k, q[0][e], x[0][j]);
-                        x[1][j] = mfma(k, q[1][e], x[1][j]);
-                    }
-                }
-                f16x8 p[2][2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float keep = weights<false>(x[t], a, at[t], masked, tile0, c1, w, inv, m[t], l[t], p[t], nullptr);
-                    if (__ballot(keep != 1.0f)) {
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) o[t][d] *= keep;
-                    }
-                }
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const f16x8 v = from[(KF + d * 2 + e) * 64];
-                        o[0][d] = mfma(v, p[0][e], o[0][d]);
-                        o[1][d] = mfma(v, p[1][e], o[1][d]);
-                    }
-            }
-            if (i + 1 < many) put(i + 1);
-            if (i + 2 < in_pages) load(i + 2);
+            vector_work(__builtin_amdgcn_readlane(tok0, i), lane_value(ps.c1, i), lane_value(ps.w, i), lane_value(ps.inv, i));
+            if (NW > 4) __syncthreads();
+            // behind the last tile the scores are computed from old values and not used
+            matrix_work(i + 1, true, true, [&](int part) { move_on(i + 1, part); });
             __syncthreads();
         }
+        if (NW > 4 && !turn) __syncthreads();
+        base += many;
+        more = many == 64;
+    }
+    // the unfinished page, from the ring
+    for (; base < t1; ++base) {
+        const int tile0 = tiles.at(base) * kTile;
+        const int64_t at0 = (((int64_t)seq.slot * 2 + (tile0 >> a.page_shift & 1)) * n_kv + h) * head +
+                            (tile0 & (page - 1)) * D;
+        __syncthreads();                                   // the tile before has been read
+        for (int unit = tid; unit < UNITS; unit += THREADS) {
+            const u32x4 *kp = reinterpret_cast<const u32x4 *>(a.cache.k_tail + at0 + unit * 16);
+            const u32x4 *vp = reinterpret_cast<const u32x4 *>(a.cache.v_tail + at0 + unit * 16);
+            f16x8 *to = k_place(0, unit);
+            to[0] = bitcast<f16x8>(kp[0]);
+            to[64] = bitcast<f16x8>(kp[1]);
+            // places behind the last token hold anything: zero them, 0 * NaN is not 0
+            const int left = seq.total() - tile0 - 16 * (unit / D);
+            u32x4 lo = vp[0], hi = vp[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lo[e] &= left >= 2 * e + 2 ? 0xFFFFFFFFu : left == 2 * e + 1 ? 0xFFFFu : 0u;
+                hi[e] &= left >= 2 * e + 10 ? 0xFFFFFFFFu : left == 2 * e + 9 ? 0xFFFFu : 0u;
+            }
+            to = v_place(0, unit);
+            to[0] = bitcast<f16x8>(lo);
+            to[64] = bitcast<f16x8>(hi);
+        }
+        __syncthreads();
+        matrix_work(0, false, true, [](int) {});
+        vector_work(tile0, a.scale, 0.0f, 1.0f);
+        matrix_work(1, true, false, [](int) {});           // its V is in buffer 0
     }
 
 #pragma unroll
