@@ -17,6 +17,8 @@
 // 16 g .. 16 g + 15 at a time: its own registers, since K rows are stored in the
 // order that puts them there (kv_k_index).  P never leaves the lane, and K and
 // V pages are read straight into operand registers in contiguous 16-byte loads.
+#include <algorithm>
+
 #include "kv_device.h"
 #include "q4_launch.h"
 
@@ -636,8 +638,8 @@ __global__ __launch_bounds__(64 * NW) void kv_join_kernel(Args a)
     store_out(a.out + ((int64_t)tok * a.n_q + hq) * D + ch, sum, sum_l);
 }
 
-// Many rows of a sequence: a workgroup of NW waves holds 32 NW rows (a wave two
-// blocks of 16) and walks the tiles they see; each tile is converted to fp16
+// Many rows of a sequence: a workgroup of NW waves holds 16 QT NW rows (a wave QT
+// blocks of 16; one for D = 256, whose sums fill the registers) and walks the tiles they see; each tile is converted to fp16
 // once, into LDS, in the order of the operands (a wave reads 1 KiB in a row).
 // Two buffers each for K and V; the tiles after them are on their way in registers.
 // A wave's matrix work (a tile's scores, the last one's second product) and its
@@ -646,10 +648,10 @@ __global__ __launch_bounds__(64 * NW) void kv_join_kernel(Args a)
 // the two that share a SIMD take turns: waves 4 .. 7 run half a tile behind, and
 // each barrier hands the matrix cores to the other wave.  With few row blocks the tiles are cut
 // into `splits` runs and joined by kv_join_rows_kernel.
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kernel(Args a, int splits)
+template <int D, int NW, int QT>
+__global__ __launch_bounds__(64 * NW, 2) void kv_attend_rows_kernel(Args a, int splits)
 {
-    constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 32 * NW, THREADS = 64 * NW;
+    constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 16 * QT * NW, THREADS = 64 * NW;
     constexpr int UNITS = 4 * D, UN = (UNITS + THREADS - 1) / THREADS;     // 16-byte units of a tile's K (and V)
     constexpr int KF = 8 * KS, VF = 2 * DT;                                // operands of 1 KiB
     extern __shared__ f16x8 k_tile[];                      // [2][KF][64], then V's [2][VF][64]
@@ -670,15 +672,15 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
     const int t0 = (int)((int64_t)tiles.count * split / splits), t1 = (int)((int64_t)tiles.count * (split + 1) / splits);
 
     // this wave's rows
-    const int first = row0 + wave * 32;
+    const int first = row0 + wave * 16 * QT;
     const int turn = NW > 4 && wave >= 4 ? 1 : 0;
-    const int at_min = seq.ctx + first / a.group, at_max = seq.ctx + (min(first + 32, rows) - 1) / a.group;
-    f16x8 q[2][2 * KS];
-    f32x4 o[2][DT];
-    float m[2], l[2];
-    int at[2];
+    const int at_min = seq.ctx + first / a.group, at_max = seq.ctx + (min(first + 16 * QT, rows) - 1) / a.group;
+    f16x8 q[QT][2 * KS];
+    f32x4 o[QT][DT];
+    float m[QT], l[QT];
+    int at[QT];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < QT; ++t) {
         const int r = first + t * 16 + m16, tok = r / a.group;
         at[t] = seq.ctx + tok;
         m[t] = kNone;
@@ -720,13 +722,13 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
         const int ch = unit % D;
         return v_tile + (i & 1) * VF * 64 + ch / 16 * 128 + unit / D * 16 + (ch & 15);
     };
-    f32x4 x[2][4];
-    f16x8 p[2][2];
+    f32x4 x[QT][4];
+    f16x8 p[QT][2];
     // O += P V of tile i - 1, and the scores of tile i.  Operands are read ahead, and
-    // an accumulator comes up again after three others.  `between` is run twice, after two
+    // an accumulator comes up again after one or three others.  `between` is run twice, after two
     // pieces of the scores.
     auto matrix_work = [&](int i, bool second, bool first, auto between) {
-        constexpr int VP = DT / 2, NP = VP + 2 * KS, AHEAD = D <= 128 ? 2 : 1;
+        constexpr int VP = DT / 2, NP = VP + 2 * KS, AHEAD = 2;
         f16x8 f[AHEAD + 1][4];
         auto fetch = [&](int n) {
             if (n < VP) { if (second) read_v(i - 1, n, f[n % (AHEAD + 1)]); }
@@ -744,13 +746,13 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
                 const int one = e & 1, half = e >> 1;                  // operand 2 one + half
                 const f16x8 v = f[n % (AHEAD + 1)][2 * one + half];
                 if (n < VP) {
-                    o[0][2 * n + one] = mfma(v, p[0][half], o[0][2 * n + one]);
-                    o[1][2 * n + one] = mfma(v, p[1][half], o[1][2 * n + one]);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) o[t][2 * n + one] = mfma(v, p[t][half], o[t][2 * n + one]);
                 } else {
                     const int j = (n - VP) / KS * 2 + one, c = (n - VP) % KS * 2 + half;
                     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                    x[0][j] = mfma(v, q[0][c], c == 0 ? zero : x[0][j]);
-                    x[1][j] = mfma(v, q[1][c], c == 0 ? zero : x[1][j]);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) x[t][j] = mfma(v, q[t][c], c == 0 ? zero : x[t][j]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -763,21 +765,23 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
     auto vector_work = [&](int tile0, float c1, float w, float inv) {
         if (tile0 + kTile - 1 > at_min || (a.window > 0 && at_max - tile0 >= a.window && tile0 + kTile > a.sinks)) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) hide(x[t], a, at[t], tile0);
+            for (int t = 0; t < QT; ++t) hide(x[t], a, at[t], tile0);
         }
-        float keep[2];
+        float keep[QT];
+        bool moved = false;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < QT; ++t) {
             keep[t] = weigh_max(x[t], c1, w, m[t]);
             const float add = w - m[t] + kLift;
             float sum = 0.0f;
             weigh_exp(x[t], 0, c1, add, p[t], sum);
             weigh_exp(x[t], 1, c1, add, p[t], sum);
             l[t] = l[t] * keep[t] + sum * inv;
+            moved |= keep[t] != 1.0f;
         }
-        if (__ballot(keep[0] != 1.0f || keep[1] != 1.0f)) {
+        if (__ballot(moved)) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < QT; ++t)
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[t][d] *= keep[t];
         }
@@ -892,7 +896,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void kv_attend_rows_kern
     }
 
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < QT; ++t) {
         const int r = first + t * 16 + m16;
         const float sum = column_sum(l[t]);
         if (r >= rows) continue;
@@ -943,7 +947,7 @@ __global__ __launch_bounds__(kThreads) void kv_join_rows_kernel(Args a, int spli
 }
 
 // Waves per SIMD that the split kernel's registers allow.
-constexpr int split_occupancy(int d, int qt) { return d <= 64 || (d <= 128 && qt == 1) ? 2 : 1; }
+constexpr int split_occupancy(int d, int qt) { return (d <= 64 && qt <= 2) || (d <= 128 && qt == 1) ? 2 : 1; }
 
 // How a call is run.  qt > 0: the split kernel with qt blocks of 16 rows, as many
 // as an average sequence fills.  qt == 0: the rows kernel with `waves` waves and
@@ -953,23 +957,36 @@ struct Plan {
     int64_t items, parts;        // row blocks of the rows kernel (an upper bound); rows of workspace
 };
 
-Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d)
+// Sequences have at most `most` tokens, and a row sees at most `span` of them.
+Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most, int64_t span)
 {
     Plan p = {};
     const int64_t group = n_q / n_kv, rows = (tokens + batch - 1) / batch * group;
-    if (rows <= (d <= 128 ? 32 : 16)) {
-        p.qt = rows <= 16 ? 1 : 2;
+    if (rows <= (d <= 128 ? 48 : 16)) {
+        p.qt = (int)(rows + 15) / 16;
         const int groups = 256 * split_occupancy(d, p.qt);       // workgroups that the 256 CUs hold at once
         p.workers = n_kv < groups ? (groups + n_kv - 1) / n_kv : 1;
         p.parts = (int64_t)p.workers * n_kv * 2 * 16 * p.qt;
         return p;
     }
     // 256 rows a workgroup while that gives every CU one, else 128
-    p.waves = rows >= 256 && tokens * group / 256 * n_kv >= 256 && d <= 128 ? 8 : 4;
-    const int64_t rb = 32 * p.waves;
+    p.waves = d == 256 || (rows >= 256 && tokens * group / 256 * n_kv >= 256) ? 8 : 4;
+    const int64_t rb = (d == 256 ? 16 : 32) * p.waves;
     p.items = tokens * group / rb + batch;
-    const int64_t groups = (tokens * group + rb - 1) / rb * n_kv;
-    p.splits = (int)(groups >= 256 ? 1 : (511 + groups) / groups < 16 ? (511 + groups) / groups : 16);
+    // Cuts of the tiles, by what they cost: rounds of workgroups on 256 CUs (two of
+    // four waves fit a CU, one of eight) at 2 us a tile, 1.3 where four waves have a CU
+    // to themselves, against a second launch and the parts' way out and back at 4 TB/s.
+    // (1 x 512 queries on 8k tokens: uncut 310 us, in two 159; 2 x 1500 in a window of
+    // 1024, d = 256: uncut 102 us, in two 120; 32 x 8 on 2k: uncut 52, in two 62.)
+    const int64_t groups = (tokens * group + rb - 1) / rb * n_kv, places = p.waves == 4 ? 512 : 256;
+    const double tiles = (double)std::min(most, span + rb / group + 2 * kTile) / kTile;
+    auto cost = [&](int cuts) {
+        const double rounds = (double)((groups * cuts + places - 1) / places) / cuts;
+        return rounds * tiles * (p.waves == 4 && groups * cuts <= 256 ? 1.3 : 2.0) + (cuts > 1 ? 5.0 + (double)(tokens * n_q) * cuts * d * 8 / 4e6 : 0.0);
+    };
+    p.splits = 1;
+    for (int cuts = 2; cuts <= 16; ++cuts)
+        if (cost(cuts) < cost(p.splits)) p.splits = cuts;
     p.parts = p.splits > 1 ? tokens * n_q * p.splits : 0;
     return p;
 }
@@ -987,16 +1004,16 @@ hipError_t launch_split(const Args &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <int D, int NW>
+template <int D, int NW, int QT>
 hipError_t launch_rows(const Args &a, const Plan &p, hipStream_t stream)
 {
     constexpr int LDS = 2 * (8 * ((D + 63) / 64) + D / 8) * 1024;
     if (LDS > 65536) {
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv_attend_rows_kernel<D, NW>),
+        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv_attend_rows_kernel<D, NW, QT>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
         if (e != hipSuccess) return e;
     }
-    kv_attend_rows_kernel<D, NW><<<(unsigned)(p.items * a.cache.n_kv * p.splits), 64 * NW, LDS, stream>>>(a, p.splits);
+    kv_attend_rows_kernel<D, NW, QT><<<(unsigned)(p.items * a.cache.n_kv * p.splits), 64 * NW, LDS, stream>>>(a, p.splits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t threads = a.batch.tokens * a.n_q * (D / 4);
@@ -1008,18 +1025,20 @@ template <int D>
 hipError_t launch(const Args &a, const Plan &p, hipStream_t stream)
 {
     if (p.qt == 1) return launch_split<D, 1>(a, stream);
-    if constexpr (D <= 128) {
+    if constexpr (D == 256) {
+        return launch_rows<D, 8, 1>(a, p, stream);
+    } else {
         if (p.qt == 2) return launch_split<D, 2>(a, stream);
-        if (p.waves == 8) return launch_rows<D, 8>(a, p, stream);
+        if (p.qt == 3) return launch_split<D, 3>(a, stream);
+        return p.waves == 8 ? launch_rows<D, 8, 2>(a, p, stream) : launch_rows<D, 4, 2>(a, p, stream);
     }
-    return launch_rows<D, 4>(a, p, stream);
 }
 
 }  // namespace
 
 int64_t kv_attention_workspace(int64_t tokens, int batch, int n_q, int n_kv, int d)
 {
-    const Plan p = plan_for(tokens, batch, n_q, n_kv, d);
+    const Plan p = plan_for(tokens, batch, n_q, n_kv, d, int64_t(1) << 40, int64_t(1) << 40);
     return p.parts * (d + 2) * 4 + (int64_t)(p.workers + 1) * 16;
 }
 
@@ -1027,7 +1046,9 @@ hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch
                                int64_t q_stride, int n_q, float scale, int window, int sinks, void *workspace,
                                uint16_t *out, hipStream_t stream)
 {
-    const Plan p = plan_for(batch.tokens, batch.batch, n_q, cache.n_kv, cache.d);
+    const int64_t most = (int64_t)(batch.table_cols + 1) * cache.page;
+    const Plan p = plan_for(batch.tokens, batch.batch, n_q, cache.n_kv, cache.d, most,
+                            window > 0 ? (int64_t)window + sinks : most);
     float *part = (float *)workspace;
     float *stats = part + p.parts * cache.d;
     const Args a = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, window, sinks,
