@@ -65,46 +65,77 @@ __device__ __forceinline__ uint32_t pack_once(double a, double b)
     return bitcast<uint32_t>(h);
 }
 
-// Channels 16c .. 16c + 15 of one head's row, rotated to `row`'s position.
-__device__ __forceinline__ Chunk rotated_chunk(const uint16_t *x, int c, int64_t row, const Rope &rope)
+// Rotation works on units of 16 channels of a head: pairs 8 pc .. 8 pc + 7 as their
+// two halves, channels c0 .. c0 + 7 and c1 .. c1 + 7 (with interleaved pairs, and
+// for the channels behind rope.dim that are only copied, 16 neighbours).
+struct Unit {
+    int c0, c1;
+    bool turned;
+    __device__ Unit(const Rope &rope, int pc)
+    {
+        const int half = rope.dim / 2;
+        turned = pc * 8 < half;
+        c0 = turned && !rope.interleaved ? pc * 8 : pc * 16;
+        c1 = turned && !rope.interleaved ? c0 + half : c0 + 8;
+    }
+};
+
+struct Angles {                  // of a unit's pairs at one position
+    double co[8], si[8];
+    bool nan;
+};
+
+__device__ __forceinline__ Angles load_angles(const Rope &rope, int64_t row, int pc)
 {
-    const Chunk own = load_chunk(x + c * 16);
-    if (!rope.table || c * 16 >= rope.dim) return own;
+    Angles r;
     const int64_t pos = rope.positions[row];
-    if (pos < 0 || pos >= rope.rows) {
-        const u32x4 nan = {0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
-        return {nan, nan};
-    }
-    const int half = rope.dim / 2;
-    const float *cs = rope.table + pos * rope.dim;
-    Chunk r;
-    if (rope.interleaved) {
+    r.nan = pos < 0 || pos >= rope.rows;
+    const float *cs = rope.table + (r.nan ? 0 : pos) * rope.dim + pc * 16;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const double co = cs[(c * 8 + j) * 2], si = cs[(c * 8 + j) * 2 + 1];
-            const double a = half_at(own, 2 * j), b = half_at(own, 2 * j + 1);
-            const uint32_t w = pack_once(__builtin_fma(a, co, -(b * si)), __builtin_fma(b, co, a * si));
-            if (j < 4) r.lo[j] = w; else r.hi[j - 4] = w;
-        }
-        return r;
-    }
-    const bool first = c * 16 < half;
-    const Chunk other = load_chunk(x + (first ? c * 16 + half : c * 16 - half));
-    cs += (first ? c * 16 : c * 16 - half) * 2;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const f32x4 t = *reinterpret_cast<const f32x4 *>(cs + 4 * j);      // two pairs' cosine and sine
-        double v[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const double co = t[2 * i], si = t[2 * i + 1];
-            const double a = half_at(own, 2 * j + i), b = half_at(other, 2 * j + i);
-            v[i] = __builtin_fma(a, co, first ? -(b * si) : b * si);        // the product is exact
-        }
-        const uint32_t w = pack_once(v[0], v[1]);
-        if (j < 4) r.lo[j] = w; else r.hi[j - 4] = w;
+    for (int j = 0; j < 8; j += 2) {
+        const f32x4 t = *reinterpret_cast<const f32x4 *>(cs + 2 * j);
+        r.co[j] = t[0], r.si[j] = t[1], r.co[j + 1] = t[2], r.si[j + 1] = t[3];
     }
     return r;
+}
+
+__device__ __forceinline__ Chunk load_unit(const uint16_t *x, const Unit &u)
+{
+    return {*reinterpret_cast<const u32x4 *>(x + u.c0), *reinterpret_cast<const u32x4 *>(x + u.c1)};
+}
+
+// The products are exact in binary64, so each fma rounds once.
+__device__ __forceinline__ Chunk turn(const Chunk &x, const Angles &t, bool interleaved)
+{
+    Chunk r;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        double u[2], v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = 2 * w + i, at = interleaved ? 2 * j : j, bt = interleaved ? 2 * j + 1 : j + 8;
+            const double a = half_at(x, at), b = half_at(x, bt);
+            u[i] = __builtin_fma(a, t.co[j], -(b * t.si[j]));
+            v[i] = __builtin_fma(b, t.co[j], a * t.si[j]);
+        }
+        if (interleaved) {
+            const uint32_t p0 = pack_once(u[0], v[0]), p1 = pack_once(u[1], v[1]);
+            if (w < 2) r.lo[2 * w] = p0, r.lo[2 * w + 1] = p1;
+            else r.hi[2 * w - 4] = p0, r.hi[2 * w - 3] = p1;
+        } else {
+            r.lo[w] = pack_once(u[0], u[1]);
+            r.hi[w] = pack_once(v[0], v[1]);
+        }
+    }
+    if (t.nan) r.lo = r.hi = u32x4{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
+    return r;
+}
+
+// A unit of one row of one head.
+__device__ __forceinline__ Chunk rotated_unit(const uint16_t *x, int64_t row, int pc, const Unit &u, const Rope &rope)
+{
+    const Chunk r = load_unit(x, u);
+    return u.turned ? turn(r, load_angles(rope, row, pc), rope.interleaved) : r;
 }
 
 // Largest of a value over the workgroup; `red` holds one float per wave.
@@ -129,14 +160,20 @@ __device__ void quantize_k_page(const uint16_t *src, int64_t stride, const KvSeq
     const int tid = threadIdx.x;
     const int old = max(s.ctx - page_no * T, 0);               // tokens of the page that the ring holds
     const int64_t row0 = (int64_t)s.q0 + page_no * T - s.ctx;  // row of the page's token 0
+    auto place = [](int tok, int c) { return kv_k_index(tok, c >> 4, DC) + (c & 15); };
     Chunk x[KN];
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
-        const int u = tid + i * kThreads, c = (u >> 2) % DC, tok = (u >> 2) / DC * 4 + (u & 3);
+        // four tokens, whose codes lie side by side, in neighbouring threads
+        const int u = tid + i * kThreads, pc = (u >> 2) % DC, tok = (u >> 2) / DC * 4 + (u & 3);
         if (u < KU) {
-            x[i] = tok < old ? load_chunk(ring + kv_k_index(tok, c, DC))
-                             : rotated_chunk(src + (row0 + tok) * stride, c, row0 + tok, rope);
+            const Unit unit(rope, pc);
+            if (tok < old)
+                x[i] = {*reinterpret_cast<const u32x4 *>(ring + place(tok, unit.c0)),
+                        *reinterpret_cast<const u32x4 *>(ring + place(tok, unit.c1))};
+            else
+                x[i] = rotated_unit(src + (row0 + tok) * stride, row0 + tok, pc, unit, rope);
 #pragma unroll
             for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(half_at(x[i], e)));
         }
@@ -145,12 +182,33 @@ __device__ void quantize_k_page(const uint16_t *src, int64_t stride, const KvSeq
     if (tid == 0) *scale_out = scale;
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
-        const int u = tid + i * kThreads, c = (u >> 2) % DC, tok = (u >> 2) / DC * 4 + (u & 3);
+        const int u = tid + i * kThreads, pc = (u >> 2) % DC, tok = (u >> 2) / DC * 4 + (u & 3);
         if (u < KU) {
+            const Unit unit(rope, pc);
             u32x4 w = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[e >> 2] |= kv_code(half_at(x[i], e), scale, r, 127.0f) << (8 * (e & 3));
-            *reinterpret_cast<u32x4 *>(codes + kv_k_index(tok, c, DC)) = w;
+            *reinterpret_cast<u32x2 *>(codes + place(tok, unit.c0)) = u32x2{w[0], w[1]};
+            *reinterpret_cast<u32x2 *>(codes + place(tok, unit.c1)) = u32x2{w[2], w[3]};
+        }
+    }
+}
+
+// 16 tokens' values of four channels, each channel's in the order of tokens; those
+// of tokens before `old` come from `x` as it is.
+__device__ __forceinline__ void gather_v(Chunk x[4], const uint16_t *src, int64_t stride, int from, int to)
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (j < from || j >= to) continue;
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(src + j * stride);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+            uint32_t v = j < 8 ? x[e].lo[j >> 1] : x[e].hi[(j - 8) >> 1];
+            v = j & 1 ? (v & 0xFFFFu) | h << 16 : (v & 0xFFFF0000u) | h;
+            if (j < 8) x[e].lo[j >> 1] = v;
+            else x[e].hi[(j - 8) >> 1] = v;
         }
     }
 }
@@ -175,18 +233,7 @@ __device__ void quantize_v_page(const uint16_t *src, int64_t stride, const KvSeq
             x[i][e].lo = x[i][e].hi = u32x4{0u, 0u, 0u, 0u};
             if (t0 < old) x[i][e] = load_chunk(ring + kv_v_index(t0, ch + e, D));
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (t0 + j < old) continue;
-            const u32x2 w = *reinterpret_cast<const u32x2 *>(src + (row0 + t0 + j) * stride + ch);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t h = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-                uint32_t &to = j < 8 ? reinterpret_cast<uint32_t *>(&x[i][e].lo)[j >> 1]
-                                     : reinterpret_cast<uint32_t *>(&x[i][e].hi)[(j - 8) >> 1];
-                to = j & 1 ? (to & 0xFFFFu) | h << 16 : (to & 0xFFFF0000u) | h;
-            }
-        }
+        gather_v(x[i], src + (row0 + t0) * stride + ch, stride, old - t0, 16);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -216,27 +263,42 @@ __device__ void ring_k(const uint16_t *src, int64_t stride, const KvSeq &s, cons
     constexpr int DC = D / 16;
     const int first = max(s.ctx, ((s.total() - 1) / T - 1) * T), count = s.total() - first;
     const int64_t row0 = (int64_t)s.q0 + first - s.ctx;
+#pragma unroll 2
     for (int u = threadIdx.x; u < count * DC; u += kThreads) {
-        const int i = u / DC, c = u - i * DC, tok = first + i;
-        store_chunk(ring + (tok / T & 1) * other + kv_k_index(tok & (T - 1), c, DC),
-                    rotated_chunk(src + (row0 + i) * stride, c, row0 + i, rope));
+        const int i = u / DC, pc = u - i * DC, tok = first + i;
+        const Unit unit(rope, pc);
+        const Chunk x = rotated_unit(src + (row0 + i) * stride, row0 + i, pc, unit, rope);
+        uint16_t *to = ring + (tok / T & 1) * other;
+        *reinterpret_cast<u32x4 *>(to + kv_k_index(tok & (T - 1), unit.c0 >> 4, DC) + (unit.c0 & 15)) = x.lo;
+        *reinterpret_cast<u32x4 *>(to + kv_k_index(tok & (T - 1), unit.c1 >> 4, DC) + (unit.c1 & 15)) = x.hi;
     }
 }
 
+// V in groups of 16 tokens and four channels: a whole group's tokens are one store
+// for each channel, a part of one is stored value by value.
 template <int D, int T>
 __device__ void ring_v(const uint16_t *src, int64_t stride, const KvSeq &s, uint16_t *ring, int64_t other)
 {
-    constexpr int DC = D / 16;
-    const int first = max(s.ctx, ((s.total() - 1) / T - 1) * T), count = s.total() - first;
-    const int64_t row0 = (int64_t)s.q0 + first - s.ctx;
-    for (int u = threadIdx.x; u < count * DC; u += kThreads) {
-        const int i = u / DC, c = u - i * DC, tok = first + i;
-        const Chunk x = load_chunk(src + (row0 + i) * stride + c * 16);
-        uint16_t *to = ring + (tok / T & 1) * other + kv_v_index(tok & (T - 1), c * 16, D);
+    const int first = max(s.ctx, ((s.total() - 1) / T - 1) * T), g0 = first / 16, groups = (s.total() + 15) / 16 - g0;
+    const int64_t row0 = (int64_t)s.q0 - s.ctx;                // row of token 0, were it in the call
+    for (int u = threadIdx.x; u < groups * (D / 4); u += kThreads) {
+        const int t0 = (g0 + u / (D / 4)) * 16, ch = u % (D / 4) * 4;
+        const int from = max(first - t0, 0), to = min(s.total() - t0, 16);
+        uint16_t *out = ring + (t0 / T & 1) * other + kv_v_index(t0 & (T - 1), ch, D);
+        const uint16_t *in = src + (row0 + t0) * stride + ch;
+        if (to - from == 16) {
+            Chunk x[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const uint32_t w = e < 8 ? x.lo[e >> 1] : x.hi[(e - 8) >> 1];
-            to[e * 16] = (uint16_t)(w >> (16 * (e & 1)));
+            for (int e = 0; e < 4; ++e) x[e].lo = x[e].hi = u32x4{0u, 0u, 0u, 0u};
+            gather_v(x, in, stride, 0, 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store_chunk(out + e * 16, x[e]);
+        } else {
+            for (int j = from; j < to; ++j) {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(in + j * stride);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[e * 16 + j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            }
         }
     }
 }
@@ -247,78 +309,42 @@ struct Source {                  // the call's rows
     int n_q, q_heads;            // heads of q, and how many of them a thread rotates
 };
 
-// Pairs 8 pc .. 8 pc + 7 of a row's heads head, head + step, ...: the angles are
-// read and widened once for all of them.
+// Unit pc of a row's heads head, head + step, ...: the angles are read and widened
+// once for all of them.
 template <int D>
 __device__ __forceinline__ void rotate_q(const Source &src, const Rope &rope, int64_t row, int pc, int head, int step,
                                          uint16_t *out)
 {
-    // the two chunks of 8 channels: the pairs' first and second halves, or one after the other
-    const int half = rope.dim / 2;
-    const bool turned = pc * 8 < half;
-    int c0, c1;
-    if (!turned) c0 = rope.dim + (pc * 8 - half) * 2, c1 = c0 + 8;             // channels that are only copied
-    else if (rope.interleaved) c0 = pc * 16, c1 = c0 + 8;
-    else c0 = pc * 8, c1 = c0 + half;
-    double co[8], si[8];
-    bool nan = false;
-    if (turned) {
-        const int64_t pos = rope.positions[row];
-        nan = pos < 0 || pos >= rope.rows;
-        const float *cs = rope.table + (nan ? 0 : pos) * rope.dim + pc * 16;
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const f32x4 t = *reinterpret_cast<const f32x4 *>(cs + 2 * j);
-            co[j] = t[0], si[j] = t[1], co[j + 1] = t[2], si[j + 1] = t[3];
-        }
-    }
+    const Unit unit(rope, pc);
+    Angles t = {};
+    if (unit.turned) t = load_angles(rope, row, pc);
     const uint16_t *from = src.q + row * src.q_stride;
     uint16_t *to = out + row * src.n_q * D;
     for (int h = head; h < src.n_q; h += step) {
-        Chunk x = {*reinterpret_cast<const u32x4 *>(from + h * D + c0), *reinterpret_cast<const u32x4 *>(from + h * D + c1)};
-        if (turned) {
-            Chunk r;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                double u[2], v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    // interleaved: pairs lie in neighbouring channels, four of them in each chunk
-                    const int j = 2 * w + i, at = rope.interleaved ? 2 * j : j, bt = rope.interleaved ? 2 * j + 1 : j + 8;
-                    const double a = half_at(x, at), b = half_at(x, bt);
-                    u[i] = __builtin_fma(a, co[j], -(b * si[j]));                // the products are exact
-                    v[i] = __builtin_fma(b, co[j], a * si[j]);
-                }
-                if (rope.interleaved) {
-                    const uint32_t p0 = pack_once(u[0], v[0]), p1 = pack_once(u[1], v[1]);
-                    if (w < 2) r.lo[2 * w] = p0, r.lo[2 * w + 1] = p1;
-                    else r.hi[2 * w - 4] = p0, r.hi[2 * w - 3] = p1;
-                } else {
-                    r.lo[w] = pack_once(u[0], u[1]);
-                    r.hi[w] = pack_once(v[0], v[1]);
-                }
-            }
-            x = r;
-            if (nan) x.lo = x.hi = u32x4{0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
-        }
-        *reinterpret_cast<u32x4 *>(to + h * D + c0) = x.lo;
-        *reinterpret_cast<u32x4 *>(to + h * D + c1) = x.hi;
+        Chunk x = load_unit(from + h * D, unit);
+        if (unit.turned) x = turn(x, t, rope.interleaved);
+        *reinterpret_cast<u32x4 *>(to + h * D + unit.c0) = x.lo;
+        *reinterpret_cast<u32x4 *>(to + h * D + unit.c1) = x.hi;
     }
 }
 
 template <int D, int T>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(kv_paged_cache cache, kv_paged_batch batch, Source src,
                                                              Rope rope, uint16_t *__restrict__ q_out, int edge_groups,
-                                                             int page_groups)
+                                                             int page_groups, int mix)
 {
     constexpr int PC = D / 16, SHIFT = T == 64 ? 6 : T == 128 ? 7 : 8;
     constexpr int PAGE = D * T;
     __shared__ float red[4];
     const int n_kv = cache.n_kv;
-    int g = blockIdx.x;
-
-    if (g >= edge_groups + page_groups) {
-        const int64_t u = (int64_t)(g - edge_groups - page_groups) * kThreads + threadIdx.x;
+    int g = blockIdx.x - edge_groups;                          // behind the edges, pages and q mixed: every
+    int page_item = -1;                                        // `mix`-th workgroup is a page's while there are any
+    if (g >= 0) {
+        if (g % mix == 0 && g / mix < page_groups) page_item = g / mix;
+        else g -= min(page_groups, g / mix + 1);
+    }
+    if (g >= 0 && page_item < 0) {
+        const int64_t u = (int64_t)g * kThreads + threadIdx.x;
         const int step = (src.n_q + src.q_heads - 1) / src.q_heads;            // threads that share a row's pairs
         const int64_t row = u / (PC * step);
         if (row >= batch.tokens) return;
@@ -327,8 +353,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(kv_paged_cache cach
         return;
     }
 
-    const bool edge = g < edge_groups;
-    if (!edge) g -= edge_groups;
+    const bool edge = page_item < 0;
+    g = edge ? blockIdx.x : page_item;
     const bool of_v = g & 1;
     const int h = g / 2 % n_kv;
     int b = g / 2 / n_kv, page_no = 0;
@@ -448,9 +474,11 @@ hipError_t kv_launch_append(const kv_paged_cache &cache, const kv_paged_batch &b
     const Source src = {k, v, q, k_stride, v_stride, q_stride, n_q, per};
     const int edge = batch.batch * cache.n_kv * 2, pages = (int)(batch.tokens / cache.page) * cache.n_kv * 2;
     const int64_t rows = q ? (batch.tokens * ((n_q + per - 1) / per) * (cache.d / 16) + kThreads - 1) / kThreads : 0;
+    // pages are bound by their arithmetic, q by memory: one in `mix` workgroups a page's
+    const int mix = pages > 0 ? (int)((pages + rows) / pages) : 1;
     return by_size(cache.d, cache.page, [&](auto D, auto T) {
         kv_append_kernel<D.value, T.value><<<(unsigned)(edge + pages + rows), kThreads, 0, stream>>>(
-            cache, batch, src, r, q_out, edge, pages);
+            cache, batch, src, r, q_out, edge, pages, mix);
         return hipGetLastError();
     });
 }
