@@ -399,43 +399,49 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(kv_paged_cache cach
     keep_new();
 }
 
-// One page of one head in the order of tokens.
+// K or V of one page of one head in the order of tokens.
 template <int D, int T>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(kv_paged_cache cache, const int32_t *__restrict__ ids,
                                                            uint16_t *__restrict__ k_out, uint16_t *__restrict__ v_out)
 {
     constexpr int DC = D / 16, PAGE = D * T;
-    const int h = blockIdx.x % cache.n_kv;
-    const int64_t i = blockIdx.x / cache.n_kv, id = ids[i];
+    const int h = blockIdx.x / 2 % cache.n_kv;
+    const int64_t i = blockIdx.x / 2 / cache.n_kv, id = ids[i];
     if (id < 0 || id >= cache.pages) return;
     const int64_t at = id * cache.n_kv + h, to = (i * cache.n_kv + h) * PAGE;
-    const float ks = cache.k_scale[at], vs = cache.v_scale[at];
-    const int8_t *kp = cache.k + at * PAGE, *vp = cache.v + at * PAGE;
     auto value = [](const u32x4 &w, int e, float s) {
         return bitcast<uint16_t>((_Float16)((float)(int8_t)(w[e >> 2] >> (8 * (e & 3))) * s));
     };
+    if (blockIdx.x & 1) {
+        const float s = cache.v_scale[at];
+        const int8_t *codes = cache.v + at * PAGE;
+        for (int u = threadIdx.x; u < T / 16 * (D / 4); u += kThreads) {
+            const int ch = u % (D / 4) * 4, t0 = u / (D / 4) * 16;
+            u32x4 w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const u32x4 *>(codes + kv_v_index(t0, ch + e, D));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const u32x2 r = {value(w[0], j, s) | (uint32_t)value(w[1], j, s) << 16,
+                                 value(w[2], j, s) | (uint32_t)value(w[3], j, s) << 16};
+                *reinterpret_cast<u32x2 *>(v_out + to + (t0 + j) * D + ch) = r;
+            }
+        }
+        return;
+    }
+    const float s = cache.k_scale[at];
+    const int8_t *codes = cache.k + at * PAGE;
+#pragma unroll 4
     for (int u = threadIdx.x; u < T * DC; u += kThreads) {
         const int c = (u >> 2) % DC, tok = (u >> 2) / DC * 4 + (u & 3);
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(kp + kv_k_index(tok, c, DC));
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(codes + kv_k_index(tok, c, DC));
         Chunk r;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            r.lo[e >> 1] = value(w, e, ks) | (uint32_t)value(w, e + 1, ks) << 16;
-            r.hi[e >> 1] = value(w, e + 8, ks) | (uint32_t)value(w, e + 9, ks) << 16;
+            r.lo[e >> 1] = value(w, e, s) | (uint32_t)value(w, e + 1, s) << 16;
+            r.hi[e >> 1] = value(w, e + 8, s) | (uint32_t)value(w, e + 9, s) << 16;
         }
         store_chunk(k_out + to + tok * D + c * 16, r);
-    }
-    for (int u = threadIdx.x; u < T / 16 * (D / 4); u += kThreads) {
-        const int ch = u % (D / 4) * 4, t0 = u / (D / 4) * 16;
-        u32x4 w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const u32x4 *>(vp + kv_v_index(t0, ch + e, D));
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const u32x2 r = {value(w[0], j, vs) | (uint32_t)value(w[1], j, vs) << 16,
-                             value(w[2], j, vs) | (uint32_t)value(w[3], j, vs) << 16};
-            *reinterpret_cast<u32x2 *>(v_out + to + (t0 + j) * D + ch) = r;
-        }
     }
 }
 
@@ -487,7 +493,7 @@ hipError_t kv_launch_read(const kv_paged_cache &cache, const int32_t *ids, int64
                           hipStream_t stream)
 {
     return by_size(cache.d, cache.page, [&](auto D, auto T) {
-        kv_read_kernel<D.value, T.value><<<(unsigned)(n * cache.n_kv), kThreads, 0, stream>>>(cache, ids, k_out, v_out);
+        kv_read_kernel<D.value, T.value><<<(unsigned)(n * cache.n_kv * 2), kThreads, 0, stream>>>(cache, ids, k_out, v_out);
         return hipGetLastError();
     });
 }

@@ -131,6 +131,14 @@ def rope_table(rows, dim, base=10000.0, device="cuda"):
     return torch.stack((a.cos(), a.sin()), -1).float()
 
 
+def _fits(t, dtype, shape, device, name):
+    """Raise unless t is a contiguous GPU tensor of this dtype and shape on `device`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _need(t, dtype, shape, name)
+        raise W4A16Error("all tensors must be on the same GPU")
+
+
 def _on(device):
     """torch.cuda.device(device), or nothing where that is the current one."""
     return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
@@ -141,15 +149,16 @@ def _heads(t, heads, d, name, device):
     a fused projection's output is)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise W4A16Error(f"{name} must be a GPU tensor (there is no CPU implementation)")
-    if t.dtype != torch.float16 or t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if t.dtype is not torch.float16 or len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads):
         raise W4A16Error(f"{name} must be float16 [tokens, {'heads' if heads is None else heads}, {d}], got "
-                         f"{t.dtype} {tuple(t.shape)}")
+                         f"{t.dtype} {tuple(shape)}")
     if t.device != device:
         raise W4A16Error("all tensors must be on the same GPU")
     row, head, one = t.stride()
-    if one != 1 or (head != d and t.shape[1] > 1):
+    if one != 1 or (head != d and shape[1] > 1):
         raise W4A16Error(f"{name}: a token's heads must lie side by side")
-    return row if t.shape[0] > 1 else t.shape[1] * d
+    return row if shape[0] > 1 else shape[1] * d
 
 
 class PagedBatch:
@@ -170,13 +179,18 @@ class PagedBatch:
                                (block_table, (B, block_table.shape[1]), "block_table"), (slots, (B,), "slots")):
             _need(t, torch.int32, shape, name)
         _same_device(cu_q, ctx_lens, block_table, slots)
-        self.cu_q, self.ctx_lens, self.block_table, self.slots = cu_q, ctx_lens, block_table, slots
+        self._tensors, self._device = (cu_q, ctx_lens, block_table, slots), cu_q.device
+
+    cu_q = property(lambda self: self._tensors[0])
+    ctx_lens = property(lambda self: self._tensors[1])
+    block_table = property(lambda self: self._tensors[2])
+    slots = property(lambda self: self._tensors[3])
 
     def _struct(self, tokens, device):
-        if self.cu_q.device != device:
+        if self._device != device:
             raise W4A16Error("all tensors must be on the same GPU")
-        return _lib.PagedBatch(self.cu_q.data_ptr(), self.ctx_lens.data_ptr(), self.block_table.data_ptr(),
-                               self.slots.data_ptr(), tokens, self.ctx_lens.shape[0], self.block_table.shape[1])
+        q, c, t, s = self._tensors
+        return _lib.PagedBatch(q.data_ptr(), c.data_ptr(), t.data_ptr(), s.data_ptr(), tokens, c.shape[0], t.shape[1])
 
 
 class PagedKVCache:
@@ -243,35 +257,40 @@ class PagedKVCache:
         T = k.shape[0]
         if v.shape[0] != T:
             raise W4A16Error("k and v must have the same tokens")
-        qs = n_q = 0
         if rope is None:
             if q is not None or positions is not None:
                 raise W4A16Error("q and positions are only used with rope")
-        else:
-            if not isinstance(rope, torch.Tensor) or rope.dim() != 3:
-                raise W4A16Error("rope must be fp32 [rows, dim/2, 2] on the GPU")
-            _need(rope, torch.float32, (rope.shape[0], rope.shape[1], 2), "rope")
-            if rope.shape[0] < 1 or rope.shape[1] < 16 or rope.shape[1] % 16 or rope.shape[1] * 2 > self.d:
-                raise W4A16Error(f"rope must rotate a multiple of 32 channels, at most d={self.d}")
-            _need(positions, torch.int32, (T,), "positions")
-            _same_device(self.k, rope, positions)
-            if q is not None:
-                qs, n_q = _heads(q, None, self.d, "q", dev), q.shape[1]
-                if q.shape[0] != T:
-                    raise W4A16Error("q and k must have the same tokens")
-                q_out = torch.empty((T, n_q, self.d), dtype=torch.float16, device=dev) if q_out is None else q_out
-                _need(q_out, torch.float16, (T, n_q, self.d), "q_out")
-                _same_device(self.k, q_out)
-        if T == 0:
-            return q_out
-        with _on(dev):
-            check(lib().kv_paged_append(
-                byref(c), byref(batch._struct(T, dev)), k.data_ptr(), ks, v.data_ptr(), vs,
-                None if q is None else q.data_ptr(), qs, n_q, None if rope is None else rope.data_ptr(),
-                0 if rope is None else rope.shape[0], 0 if rope is None else rope.shape[1] * 2, int(bool(interleaved)),
-                None if rope is None else positions.data_ptr(), None if q is None else q_out.data_ptr(),
-                _stream(self.k)), "kv_paged_append")
+            if T:
+                self._call("kv_paged_append", byref(c), byref(batch._struct(T, dev)), k.data_ptr(), ks, v.data_ptr(), vs,
+                           None, 0, 0, None, 0, 0, 0, None, None)
+            return None
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 3:
+            raise W4A16Error("rope must be fp32 [rows, dim/2, 2] on the GPU")
+        rows, pairs, _ = rope.shape
+        _fits(rope, torch.float32, (rows, pairs, 2), dev, "rope")
+        if rows < 1 or pairs < 16 or pairs % 16 or pairs * 2 > self.d:
+            raise W4A16Error(f"rope must rotate a multiple of 32 channels, at most d={self.d}")
+        _fits(positions, torch.int32, (T,), dev, "positions")
+        qs = n_q = q_at = out_at = None
+        if q is not None:
+            qs, n_q = _heads(q, None, self.d, "q", dev), q.shape[1]
+            if q.shape[0] != T:
+                raise W4A16Error("q and k must have the same tokens")
+            if q_out is None:
+                q_out = q.new_empty((T, n_q, self.d))
+            else:
+                _fits(q_out, torch.float16, (T, n_q, self.d), dev, "q_out")
+            q_at, out_at = q.data_ptr(), q_out.data_ptr()
+        if T:
+            self._call("kv_paged_append", byref(c), byref(batch._struct(T, dev)), k.data_ptr(), ks, v.data_ptr(), vs,
+                       q_at, qs or 0, n_q or 0, rope.data_ptr(), rows, pairs * 2, 1 if interleaved else 0,
+                       positions.data_ptr(), out_at)
         return None if q is None else q_out
+
+    def _call(self, name, *args):
+        """A library call on torch's current stream of the cache's GPU, made the current one."""
+        with _on(self.k.device):
+            check(getattr(lib(), name)(*args, _stream(self.k)), name)
 
     def read(self, ids, k_out=None, v_out=None):
         """Pool pages ids (int32 [n]) as fp16 (K, V), each [n, n_kv, page, d] in the
@@ -280,17 +299,18 @@ class PagedKVCache:
         if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
             raise W4A16Error("ids must be int32 [n] on the GPU")
         n = ids.shape[0]
-        _need(ids, torch.int32, (n,), "ids")
+        _fits(ids, torch.int32, (n,), dev, "ids")
         shape = (n, self.n_kv, self.page, self.d)
-        k_out = torch.empty(shape, dtype=torch.float16, device=dev) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=torch.float16, device=dev) if v_out is None else v_out
-        _need(k_out, torch.float16, shape, "k_out")
-        _need(v_out, torch.float16, shape, "v_out")
-        _same_device(self.k, ids, k_out, v_out)
+        if k_out is None:
+            k_out = self.k_tail.new_empty(shape)
+        else:
+            _fits(k_out, torch.float16, shape, dev, "k_out")
+        if v_out is None:
+            v_out = self.k_tail.new_empty(shape)
+        else:
+            _fits(v_out, torch.float16, shape, dev, "v_out")
         if n:
-            with _on(dev):
-                check(lib().kv_paged_read(byref(c), ids.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
-                                          _stream(self.k)), "kv_paged_read")
+            self._call("kv_paged_read", byref(c), ids.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr())
         return k_out, v_out
 
     def attend(self, q, batch, scale=None, window=0, sinks=0, out=None, workspace=None):
@@ -309,19 +329,18 @@ class PagedKVCache:
         scale = self.d ** -0.5 if scale is None else float(scale)
         if not 0.0 < scale <= 1e6:
             raise W4A16Error(f"scale must be in (0, 1e6], got {scale}")
-        out = torch.empty((T, n_q, self.d), dtype=torch.float16, device=dev) if out is None else out
-        _need(out, torch.float16, (T, n_q, self.d), "out")
-        _same_device(self.k, out)
+        if out is None:
+            out = q.new_empty((T, n_q, self.d))
+        else:
+            _fits(out, torch.float16, (T, n_q, self.d), dev, "out")
         if T == 0:
             return out
         b = batch._struct(T, dev)
         need = lib().kv_paged_attention_workspace_size(T, b.batch, n_q, self.n_kv, self.d)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = self.k.new_empty(need)
         elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
             raise W4A16Error("workspace must be a contiguous tensor on the cache's GPU")
-        with _on(dev):
-            check(lib().kv_paged_attention(byref(c), byref(b), q.data_ptr(), qs, n_q, scale, window, sinks,
-                                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                           out.data_ptr(), _stream(self.k)), "kv_paged_attention")
+        self._call("kv_paged_attention", byref(c), byref(b), q.data_ptr(), qs, n_q, scale, window, sinks,
+                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr())
         return out
