@@ -6,7 +6,6 @@ cache (PagedKVCache): appending new tokens with rotation, and attention over it.
 Only argument marshalling happens here: tensors must already live on the GPU
 and the library does all of the arithmetic on torch's current stream.
 """
-import contextlib
 import operator
 from ctypes import byref
 
@@ -139,11 +138,6 @@ def _fits(t, dtype, shape, device, name):
         raise W4A16Error("all tensors must be on the same GPU")
 
 
-def _on(device):
-    """torch.cuda.device(device), or nothing where that is the current one."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
 def _heads(t, heads, d, name, device):
     """The row stride of fp16 t [T, heads, d] whose rows are whole (a view into
     a fused projection's output is)."""
@@ -180,6 +174,7 @@ class PagedBatch:
             _need(t, torch.int32, shape, name)
         _same_device(cu_q, ctx_lens, block_table, slots)
         self._tensors, self._device = (cu_q, ctx_lens, block_table, slots), cu_q.device
+        self._known = None
 
     cu_q = property(lambda self: self._tensors[0])
     ctx_lens = property(lambda self: self._tensors[1])
@@ -190,7 +185,11 @@ class PagedBatch:
         if self._device != device:
             raise W4A16Error("all tensors must be on the same GPU")
         q, c, t, s = self._tensors
-        return _lib.PagedBatch(q.data_ptr(), c.data_ptr(), t.data_ptr(), s.data_ptr(), tokens, c.shape[0], t.shape[1])
+        at = (q.data_ptr(), c.data_ptr(), t.data_ptr(), s.data_ptr(), tokens)
+        known = self._known
+        if known is None or known[0] != at:
+            known = self._known = at, _lib.PagedBatch(*at, c.shape[0], t.shape[1])
+        return known[1]
 
 
 class PagedKVCache:
@@ -230,10 +229,12 @@ class PagedKVCache:
 
     def _checked(self):
         """The six tensors as the library's struct, checked when one was replaced."""
-        now = (self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
-        at = [t.data_ptr() for t in now]
-        if self._known is not None and at == self._known[1] and all(map(operator.is_, now, self._known[0])):
-            return self._known[2]
+        k, v, ks, vs, kt, vt = now = self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail
+        at = (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kt.data_ptr(), vt.data_ptr(), self.n_kv, self.d,
+              self.page)
+        known = self._known
+        if known is not None and at == known[1] and all(map(operator.is_, now, known[0])):
+            return known[2]
         kshape, vshape = self._shapes()
         P, S = self.pool_pages, self.slots
         _need(self.k, torch.int8, (P, *kshape), "k")
@@ -243,8 +244,8 @@ class PagedKVCache:
         _need(self.k_tail, torch.float16, (S, 2, *kshape), "k_tail")
         _need(self.v_tail, torch.float16, (S, 2, *vshape), "v_tail")
         _same_device(self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
-        self._known = now, at, _lib.PagedCache(*at, P, S, self.n_kv, self.d, self.page)
-        return self._known[2]
+        known = self._known = now, at, _lib.PagedCache(*at[:6], P, S, *at[6:])
+        return known[2]
 
     def append(self, k, v, batch, q=None, rope=None, positions=None, interleaved=False, q_out=None):
         """Put fp16 k, v [T, n_kv, d] behind each sequence's ctx_lens tokens; with
@@ -289,8 +290,16 @@ class PagedKVCache:
 
     def _call(self, name, *args):
         """A library call on torch's current stream of the cache's GPU, made the current one."""
-        with _on(self.k.device):
-            check(getattr(lib(), name)(*args, _stream(self.k)), name)
+        at = self.k.device.index
+        fn = getattr(lib(), name)
+        stream = torch._C._cuda_getCurrentRawStream(at)
+        if torch._C._cuda_getDevice() == at:
+            rc = fn(*args, stream)
+        else:
+            with torch.cuda.device(at):
+                rc = fn(*args, stream)
+        if rc:
+            check(rc, name)
 
     def read(self, ids, k_out=None, v_out=None):
         """Pool pages ids (int32 [n]) as fp16 (K, V), each [n, n_kv, page, d] in the
