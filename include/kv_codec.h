@@ -110,7 +110,8 @@ int kv_flush_blocks(const uint16_t *k, const uint16_t *v, int64_t blocks, int32_
  *
  *  - page: 64, 128 or 256.  d: 64, 96, 128 or 256.  n_kv in [1, 1024], n_q a
  *    multiple of n_kv, at most 1024; query head i reads kv head
- *    i / (n_q / n_kv).
+ *    i / (n_q / n_kv).  batch: at most 65536, and batch * n_kv at most 2^21.
+ *    A sequence's tokens (table_cols * page) end before 2^30.
  *  - Alignment: k, v, k_tail, v_tail, q, k, v of new tokens and out 16 bytes,
  *    the rest 4 (the rotation table 16).
  */
@@ -181,7 +182,10 @@ int64_t kv_paged_attention_workspace_size(int64_t tokens, int32_t batch, int32_t
  * softmax_j(scale * q . k_j) v, with sums and statistics in binary32, rounded
  * once.  Pages whose block_table entry is outside [0, pages) are not visible
  * (pages that no row sees are not looked up at all); a row that sees nothing
- * gives zeros.  Rows of no sequence are left as they were.  `workspace`: device
+ * gives zeros.  Rows of no sequence are left as they were.  An infinity or NaN in
+ * the k or v of a token that is read from the ring gives NaN in the rows that see
+ * the token (with a weight above zero) and reaches no other; one that was
+ * quantized has spoiled its page.  `workspace`: device
  * memory of at least kv_paged_attention_workspace_size bytes, 16-byte aligned,
  * overwritten; calls sharing a workspace must not overlap.  Results are
  * deterministic for given inputs and sizes.

@@ -209,6 +209,45 @@ def test_every_way_the_attention_is_run(d, page, n_kv, n_q, held, n):
     w.attend(n, n_q, window=200, sinks=5)
 
 
+@pytest.mark.parametrize("d,page,n_q,n", [(64, 128, 1, 20), (128, 128, 2, 20), (64, 128, 2, 20), (128, 128, 8, 20),
+                                          (96, 256, 8, 20), (256, 128, 2, 20), (128, 128, 8, 1), (256, 256, 1, 1)])
+def test_infinities_and_nan_in_masked_places(d, page, n_q, n):
+    """In tokens outside the window and in tokens behind a row: the rows that do not
+    see them are right, those that do are NaN.  A value that must not count is 0 in
+    the definition's sequence."""
+    w = World(1, 1, d, page, seed=d + n)
+    L = page + 60 + n                                   # the last 60 + n tokens are in the ring
+    k, v = w.values(L, 1), w.values(L, 1)
+    bad = {L - n - 30: "v", L - n - 31: "k"}            # 30 tokens or more before the first row
+    if n > 1:
+        bad.update({L - 10: "v", L - 5: "k"})           # behind the first rows
+    clean = [k.copy(), v.copy()]
+    for j, which in bad.items():
+        x = v if which == "v" else k
+        x[j, 0, 5], x[j, 0, d - 1] = np.nan, -np.inf
+        clean["kv".index(which)][j] = 0
+    w.cache.append(to_dev(k), to_dev(v), w.batch([L]))
+    w.seqs[0].append(*clean)
+    x = w.values(n, n_q)
+    out = w.cache.attend(to_dev(x), w.batch([n], ctx=[L - n]), window=30)
+    torch.cuda.synchronize()
+    rows = n if n == 1 else n - 10                      # rows before the first bad token behind them
+    y = out.cpu().numpy().astype(np.float64)
+    o, size, most = ref.attend(w.seqs[0], x, d ** -0.5, 30)
+    ok = bool((np.abs(y - o)[:rows] <= ref.tolerance(o, size, most, L, d)[:rows]).all())
+    assert ok
+    # Row i stands at L - n + i.  A bad k makes every later row NaN; a bad v those
+    # whose weight for it fp16 can hold: certainly the ones above 2^-20.
+    for i in range(rows, n):
+        at = L - n + i
+        ks = w.seqs[0].values(0)[0][at - 29:at + 1]
+        for h in range(n_q):
+            e = np.exp2((ks @ x[i, h].astype(np.float64)) * d ** -0.5 / np.log(2))
+            weight = e[L - 10 - (at - 29)] / e.sum()
+            if at >= L - 5 or weight >= 2.0**-20:
+                assert np.isnan(y[i, h]).all(), (i, h, weight)
+
+
 def test_many_sequences_of_many_rows():
     """More than 64 sequences in the kernels that look them up."""
     rng = np.random.default_rng(2)

@@ -67,6 +67,7 @@ def test_cache_and_batch_are_checked(L, call):
         assert call(L, c=cache(**bad)) == code, bad
     for bad, code in BAD_BATCH:
         assert call(L, b=batch(**bad)) == code, bad
+    assert call(L, c=cache(n_kv=64), b=batch(batch=32769)) == Q4_ERR_SHAPE
 
 
 @pytest.mark.parametrize("bad,code", [

@@ -57,7 +57,7 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c)
 // Four channels of o = O / l to fp16; a row that saw nothing gives zeros.
 __device__ __forceinline__ void store_out(uint16_t *to, f32x4 o, float l)
 {
-    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+    const float f = l == 0.0f ? 0.0f : 1.0f / l;
     const f16x2 x = {(_Float16)(o[0] * f), (_Float16)(o[1] * f)}, y = {(_Float16)(o[2] * f), (_Float16)(o[3] * f)};
     *reinterpret_cast<u32x2 *>(to) = u32x2{bitcast<uint32_t>(x), bitcast<uint32_t>(y)};
 }
@@ -77,6 +77,24 @@ __device__ __forceinline__ float column_sum(float v)
     v = bitcast<float>(a[0]) + bitcast<float>(a[1]);
     const auto b = __builtin_amdgcn_permlane32_swap(bitcast<uint32_t>(v), bitcast<uint32_t>(v), false, false);
     return bitcast<float>(b[0]) + bitcast<float>(b[1]);
+}
+
+// Infinities and NaN among the ring's V.  In the matrix product a row would get NaN
+// from a token that it does not see (0 * NaN); so they are replaced by finite values
+// there, and the rows that do see such a token get NaN by their sum.  `trace` turns
+// to NaN at their places.
+__device__ __forceinline__ f16x8 finite(const u32x4 &x, f16x8 &trace)
+{
+    const f16x8 v = bitcast<f16x8>(x), zero = {}, most = {65504, 65504, 65504, 65504, 65504, 65504, 65504, 65504};
+    trace = __builtin_elementwise_fma(v, zero, trace);
+    return __builtin_elementwise_min(__builtin_elementwise_max(v, -most), most);
+}
+
+// Whether any of 16 weights, in the order of tokens, is of a token in the mask.
+__device__ __forceinline__ bool sees(const f16x8 p[2], const u32x4 bad[2])
+{
+    const u32x4 x = (bitcast<u32x4>(p[0]) & bad[0]) | (bitcast<u32x4>(p[1]) & bad[1]);
+    return (x[0] | x[1] | x[2] | x[3]) != 0u;
 }
 
 struct Args {
@@ -379,17 +397,30 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 keep[e >> 2][e & 3] = left >= 2 * e + 2 ? 0xFFFFFFFFu : left == 2 * e + 1 ? 0xFFFFu : 0u;
+            f16x8 trace[2] = {};                                       // NaN at tokens with an infinity or NaN
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const u32x4 lo = *reinterpret_cast<const u32x4 *>(vp + d * 256) & keep[0];
-                const u32x4 hi = *reinterpret_cast<const u32x4 *>(vp + d * 256 + 8) & keep[1];
+                const f16x8 lo = finite(*reinterpret_cast<const u32x4 *>(vp + d * 256) & keep[0], trace[0]);
+                const f16x8 hi = finite(*reinterpret_cast<const u32x4 *>(vp + d * 256 + 8) & keep[1], trace[1]);
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
-                    s.o[t][d] = mfma(bitcast<f16x8>(lo), ph[t][0], s.o[t][d]);
-                    s.o[t][d] = mfma(bitcast<f16x8>(hi), ph[t][1], s.o[t][d]);
-                    s.o[t][d] = mfma(bitcast<f16x8>(lo), pl[t][0], s.o[t][d]);
-                    s.o[t][d] = mfma(bitcast<f16x8>(hi), pl[t][1], s.o[t][d]);
+                    s.o[t][d] = mfma(lo, ph[t][0], s.o[t][d]);
+                    s.o[t][d] = mfma(hi, ph[t][1], s.o[t][d]);
+                    s.o[t][d] = mfma(lo, pl[t][0], s.o[t][d]);
+                    s.o[t][d] = mfma(hi, pl[t][1], s.o[t][d]);
                 }
+            }
+            u32x4 bad[2] = {bitcast<u32x4>(trace[0] != trace[0]), bitcast<u32x4>(trace[1] != trace[1])};
+            const u32x4 both = bad[0] | bad[1];
+            if (__ballot((both[0] | both[1] | both[2] | both[3]) != 0u)) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)                        // over the channels, the lanes of a group
+#pragma unroll
+                        for (int o = 1; o < 16; o <<= 1) bad[half][e] |= (uint32_t)__shfl_xor((int)bad[half][e], o);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) s.l[t] = sees(ph[t], bad) ? NAN : s.l[t];
             }
         }
     }
@@ -873,14 +904,18 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attend_rows_kernel(Args a, int 
         const int tile0 = tiles.at(base) * kTile;
         const int64_t at0 = (((int64_t)seq.slot * 2 + (tile0 >> a.page_shift & 1)) * n_kv + h) * head +
                             (tile0 & (page - 1)) * D;
+        __shared__ uint32_t bad_tokens[4][8];              // all ones for such tokens, by group of 16
         __syncthreads();                                   // the tile before has been read
+        if (tid < 32) bad_tokens[tid >> 3][tid & 7] = 0;
+        __syncthreads();
+        bool any = false;
         for (int unit = tid; unit < UNITS; unit += THREADS) {
             const u32x4 *kp = reinterpret_cast<const u32x4 *>(a.cache.k_tail + at0 + unit * 16);
             const u32x4 *vp = reinterpret_cast<const u32x4 *>(a.cache.v_tail + at0 + unit * 16);
             f16x8 *to = k_place(0, unit);
             to[0] = bitcast<f16x8>(kp[0]);
             to[64] = bitcast<f16x8>(kp[1]);
-            // places behind the last token hold anything: zero them, 0 * NaN is not 0
+            // places behind the last token hold anything: zero them
             const int left = seq.total() - tile0 - 16 * (unit / D);
             u32x4 lo = vp[0], hi = vp[1];
 #pragma unroll
@@ -888,13 +923,30 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attend_rows_kernel(Args a, int 
                 lo[e] &= left >= 2 * e + 2 ? 0xFFFFFFFFu : left == 2 * e + 1 ? 0xFFFFu : 0u;
                 hi[e] &= left >= 2 * e + 10 ? 0xFFFFFFFFu : left == 2 * e + 9 ? 0xFFFFu : 0u;
             }
+            f16x8 trace[2] = {};
             to = v_place(0, unit);
-            to[0] = bitcast<f16x8>(lo);
-            to[64] = bitcast<f16x8>(hi);
+            to[0] = finite(lo, trace[0]);
+            to[64] = finite(hi, trace[1]);
+            lo = bitcast<u32x4>(trace[0] != trace[0]);
+            hi = bitcast<u32x4>(trace[1] != trace[1]);
+            const u32x4 both = lo | hi;
+            if (both[0] | both[1] | both[2] | both[3]) {
+                any = true;
+                for (int e = 0; e < 4; ++e) {
+                    atomicOr(&bad_tokens[unit / D][e], lo[e]);
+                    atomicOr(&bad_tokens[unit / D][e + 4], hi[e]);
+                }
+            }
         }
-        __syncthreads();
+        const bool found = __syncthreads_or(any);
         matrix_work(0, false, true, [](int) {});
         vector_work(tile0, a.scale, 0.0f, 1.0f);
+        if (found) {
+            u32x4 bad[2];
+            for (int e = 0; e < 8; ++e) bad[e >> 2][e & 3] = bad_tokens[g][e];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) l[t] = sees(p[t], bad) ? NAN : l[t];
+        }
         matrix_work(1, true, false, [](int) {});           // its V is in buffer 0
     }
 

@@ -120,11 +120,12 @@ int check_paged_cache(const kv_paged_cache *c)
     return Q4_OK;
 }
 
-int check_paged_batch(const kv_paged_batch *b, int32_t page)
+int check_paged_batch(const kv_paged_batch *b, const kv_paged_cache *c)
 {
     if (!b || !b->cu_q || !b->ctx_lens || !b->block_table || !b->slots) return Q4_ERR_NULL;
     if (check_rows(b->tokens) || b->batch < 1 || b->batch > 65536) return Q4_ERR_SHAPE;
-    if (b->table_cols < 1 || b->table_cols > (1 << 30) / page) return Q4_ERR_SHAPE;
+    if ((int64_t)b->batch * c->n_kv > (1 << 21)) return Q4_ERR_SHAPE;      // 32-bit grids
+    if (b->table_cols < 1 || b->table_cols > (1 << 30) / c->page) return Q4_ERR_SHAPE;
     if (!aligned(b->cu_q, 4) || !aligned(b->ctx_lens, 4) || !aligned(b->block_table, 4) || !aligned(b->slots, 4))
         return Q4_ERR_ALIGN;
     return Q4_OK;
@@ -343,7 +344,7 @@ int kv_paged_append(const kv_paged_cache *cache, const kv_paged_batch *batch, co
                     const int32_t *positions, uint16_t *q_out, void *stream)
 {
     if (int rc = check_paged_cache(cache)) return rc;
-    if (int rc = check_paged_batch(batch, cache->page)) return rc;
+    if (int rc = check_paged_batch(batch, cache)) return rc;
     if (!k || !v || (rope && !positions) || (q && !q_out)) return Q4_ERR_NULL;
     const int64_t T = batch->tokens;
     const int64_t width = (int64_t)cache->n_kv * cache->d;
@@ -384,7 +385,7 @@ int kv_paged_attention(const kv_paged_cache *cache, const kv_paged_batch *batch,
                        int64_t workspace_bytes, uint16_t *out, void *stream)
 {
     if (int rc = check_paged_cache(cache)) return rc;
-    if (int rc = check_paged_batch(batch, cache->page)) return rc;
+    if (int rc = check_paged_batch(batch, cache)) return rc;
     if (!q || !workspace || !out) return Q4_ERR_NULL;
     if (check_heads(n_q, cache->n_kv) || !(scale > 0.0f && scale <= 1e6f)) return Q4_ERR_SHAPE;
     if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return Q4_ERR_SHAPE;
