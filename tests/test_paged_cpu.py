@@ -91,6 +91,15 @@ def test_attention_rejects(L, bad, code):
     assert attend(L, **bad) == code
 
 
+def test_workspace_stays_small(L):
+    """Parts of rows, not of all rows times sixteen: at most 2^18 of d + 2 floats."""
+    for T in (1, 17, 512, 1500, 2800, 5000, 20001, 100000, 1 << 20):
+        for B in (1, 2, 4, 64, 512):
+            for n_q, n_kv, d in ((8, 1, 256), (32, 32, 128), (64, 8, 128), (64, 8, 64), (24, 8, 96)):
+                size = L.kv_paged_attention_workspace_size(T, B, n_q, n_kv, d)
+                assert 0 < size <= (1 << 18) * (d + 2) * 4 + (1 << 20), (T, B, n_q, n_kv, d, size)
+
+
 def test_attention_needs_its_whole_workspace(L):
     for T, B, n_q, n_kv, d in ((3, 2, 64, 8, 128), (1, 1, 1, 1, 64), (5000, 3, 16, 8, 256), (300, 300, 8, 1, 96)):
         size = L.kv_paged_attention_workspace_size(T, B, n_q, n_kv, d)

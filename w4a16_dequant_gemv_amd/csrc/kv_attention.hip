@@ -1040,7 +1040,9 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
         return rounds * tiles * (p.waves == 4 && groups * cuts <= 256 ? 1.3 : 2.0) + (cuts > 1 ? 5.0 + (double)(tokens * n_q) * cuts * d * 8 / 4e6 : 0.0);
     };
     p.splits = 1;
-    for (int cuts = 2; cuts <= 16; ++cuts)
+    // No more than four rounds of them: the parts, at most 2^18 rows, stay small (16 cuts
+    // of 100000 rows of 64 heads would be 53 GB), and an uneven end among more rounds costs little.
+    for (int cuts = 2; cuts <= 16 && groups * cuts <= 4 * places; ++cuts)
         if (cost(cuts) < cost(p.splits)) p.splits = cuts;
     p.parts = p.splits > 1 ? tokens * n_q * p.splits : 0;
     return p;
