@@ -307,6 +307,24 @@ def test_a_replaced_tensor_is_used():
         c.attend(to_dev(x), w.batch([1], ctx=[199]))
 
 
+def test_a_resized_block_table_is_used():
+    """A table that the caller makes narrower or wider in place, where it is."""
+    w = World(2, 2, 64, 64, seed=31)
+    w.append([150, 90])
+    q = to_dev(w.values(2, 4))
+    pages = w.batch([1, 1]).block_table[:, :3]
+    table = torch.full((2, 16), -1, dtype=torch.int32, device="cuda")
+    batch = kv.PagedBatch(i32([0, 1, 2]), i32([149, 89]), table, i32(w.slots.tolist()))
+    want = w.cache.attend(q, w.batch([1, 1], ctx=[149, 89]))
+    for cols in (4, 16, 3):
+        table.resize_(2, cols).fill_(-1)
+        table[:, :3] = pages
+        assert np.array_equal(bits(w.cache.attend(q, batch)), bits(want)), cols
+    table.resize_(3, 4)
+    with pytest.raises(W4A16Error):
+        w.cache.attend(q, batch)
+
+
 def test_wrappers_refuse():
     c = kv.PagedKVCache(2, 2, 64, 1, torch.device("cuda"), page=64)
     b = kv.PagedBatch(i32([0, 3]), i32([0]), i32([[0]]), i32([0]))
