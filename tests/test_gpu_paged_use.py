@@ -187,10 +187,14 @@ def test_drafted_tokens():
 
 
 @pytest.mark.parametrize("d,page,n_kv,n_q,held,n", [
-    (64, 64, 8, 64, [1500], [1100]),                  # eight waves a workgroup
+    (64, 64, 8, 64, [1500], [1000]),                  # eight waves a workgroup, uncut
+    (128, 128, 8, 64, [1300], [1000]),
+    (96, 64, 8, 64, [1200, 1040], [508, 500]),
+    (128, 128, 4, 8, [4100], [2100]),                 # the same with tiles cut
+    (64, 64, 8, 64, [1500], [1100]),                  # four waves, uncut
     (128, 128, 8, 64, [1300], [1030]),
-    (128, 128, 4, 8, [4100], [2100]),                 # eight waves, more than 64 tiles
     (96, 64, 8, 64, [1200, 40], [1030, 20]),
+    (128, 64, 4, 8, [9000], [1100]),                  # eight waves, more than 64 tiles in a cut
     (256, 128, 2, 4, [900, 500], [600, 33]),
     (64, 128, 1, 8, [4500, 4700], [40, 30]),          # few row blocks: tiles cut and joined
     (256, 64, 1, 2, [4400], [20]),

@@ -432,6 +432,12 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
 // worker has whole is finished there; the others' parts go to the workspace: the
 // run's first row block to place 0, its last to place 1.  The worker that has a
 // shared row block's first tile leaves a note for the kernel that joins them.
+// Bound by HBM with many tokens (32 x 32k, 64 query heads on 8: 377 us, 5.7 TB/s; 64
+// ragged sequences of 4k on average: 67 us, 4.7 TB/s, where a fixed number of cuts for
+// each sequence took 89), by latency with few (1 x 500 tokens: 10.6 us with the join).
+// Pages go from memory to operand registers: no wave shares a tile with another, so
+// LDS would add a trip and a barrier.  P is used as two fp16 parts, whose second one
+// costs little here (5 rows of 8 sequences: 21.8 us, 20.0 without it).
 template <int D, int QT, int OCC>
 __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
 {
@@ -579,7 +585,8 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
 
 // Joins the parts of a row block that several workers shared: a workgroup per
 // row, D / 4 lanes side by side, the parts dealt out to its NW waves and to as
-// many places in a wave as there is room for.
+// many places in a wave as there is room for.  Bound by latency (a note, then the
+// parts, eight at a time): 3 to 5 us.
 template <int D, int QT, int NW>
 __global__ __launch_bounds__(64 * NW) void kv_join_kernel(Args a)
 {
@@ -1009,7 +1016,7 @@ constexpr int split_occupancy(int d, int qt) { return (d <= 64 && qt <= 2) || (d
 // `splits` runs of tiles.
 struct Plan {
     int qt, waves, splits, workers;
-    int64_t items, parts;        // row blocks of the rows kernel (an upper bound); rows of workspace
+    int64_t items, parts;        // row blocks of the rows kernel (an upper bound); rows of workspace, whatever the lengths
 };
 
 // Sequences have at most `most` tokens, and a row sees at most `span` of them.
@@ -1017,6 +1024,8 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
 {
     Plan p = {};
     const int64_t group = n_q / n_kv, rows = (tokens + batch - 1) / batch * group;
+    // the rows kernel with these would be half idle (8 x 5 rows of 8 query heads on 4000
+    // tokens: 40 us, 42 in the rows kernel; 3 rows 32 and 43; d = 64 with 20 rows on 8000 29 and 42)
     if (rows <= (d <= 128 ? 48 : 16)) {
         p.qt = (int)(rows + 15) / 16;
         const int groups = 256 * split_occupancy(d, p.qt);       // workgroups that the 256 CUs hold at once
@@ -1024,27 +1033,34 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
         p.parts = (int64_t)p.workers * n_kv * 2 * 16 * p.qt;
         return p;
     }
-    // 256 rows a workgroup while that gives every CU one, else 128
-    p.waves = d == 256 || (rows >= 256 && tokens * group / 256 * n_kv >= 256) ? 8 : 4;
-    const int64_t rb = (d == 256 ? 16 : 32) * p.waves;
-    p.items = tokens * group / rb + batch;
-    // Cuts of the tiles, by what they cost: rounds of workgroups on 256 CUs (two of
-    // four waves fit a CU, one of eight) at 2 us a tile, 1.3 where four waves have a CU
-    // to themselves, against a second launch and the parts' way out and back at 4 TB/s.
-    // (1 x 512 queries on 8k tokens: uncut 310 us, in two 159; 2 x 1500 in a window of
-    // 1024, d = 256: uncut 102 us, in two 120; 32 x 8 on 2k: uncut 52, in two 62.)
-    const int64_t groups = (tokens * group + rb - 1) / rb * n_kv, places = p.waves == 4 ? 512 : 256;
-    const double tiles = (double)std::min(most, span + rb / group + 2 * kTile) / kTile;
-    auto cost = [&](int cuts) {
-        const double rounds = (double)((groups * cuts + places - 1) / places) / cuts;
-        return rounds * tiles * (p.waves == 4 && groups * cuts <= 256 ? 1.3 : 2.0) + (cuts > 1 ? 5.0 + (double)(tokens * n_q) * cuts * d * 8 / 4e6 : 0.0);
-    };
-    p.splits = 1;
-    // No more than four rounds of them: the parts, at most 2^18 rows, stay small (16 cuts
-    // of 100000 rows of 64 heads would be 53 GB), and an uneven end among more rounds costs little.
-    for (int cuts = 2; cuts <= 16 && groups * cuts <= 4 * places; ++cuts)
-        if (cost(cuts) < cost(p.splits)) p.splits = cuts;
-    p.parts = p.splits > 1 ? tokens * n_q * p.splits : 0;
+    // Waves and cuts by what they cost: a workgroup takes 8 us and 2 a tile, one of four
+    // waves 2.3 where two share a CU and 1.3 alone; cuts cost a second launch and the
+    // parts' way out and back at 4 TB/s.  (64 query heads on 8, four against eight waves:
+    // 512 queries on 8k tokens 157 and 139 us, 2048 on 6144 467 and 410, 512 on none 20.7
+    // and 25.5, 32 x 40 on 2000 124 and 130.  Cuts: 512 on 8k uncut 310, in
+    // two 159; 2 x 1500 in a window of 1024, d = 256, 102 and 120; 32 x 8 on 2k 52 and 62.)
+    // No more than four rounds of cut ones: the parts, at most 2^18 rows, stay small (16
+    // cuts of 100000 rows of 64 heads would be 53 GB), and an uneven end among more
+    // rounds costs little.
+    double best = 0.0;
+    for (int waves = d == 256 ? 8 : 4; waves <= 8; waves += 4) {
+        const int64_t rb = (d == 256 ? 16 : 32) * waves, places = waves == 4 ? 512 : 256;
+        const int64_t groups = (rows + rb - 1) / rb * batch * n_kv;
+        const double tiles = (double)std::min(most, span + rb / group + 2 * kTile) / kTile;
+        for (int cuts = 1; cuts <= 16 && (cuts == 1 || groups * cuts <= 4 * places); ++cuts) {
+            const int64_t full = groups * cuts / places, rest = groups * cuts % places;
+            const double pair = waves == 4 ? 2.3 : 2.0, last = waves == 4 && rest <= 256 ? 1.3 : pair;
+            const double run = tiles / cuts, cost = (double)full * (8.0 + run * pair) + (rest ? 8.0 + run * last : 0.0) +
+                (cuts > 1 ? 5.0 + (double)(tokens * n_q) * cuts * d * 8 / 4e6 : 0.0);
+            if (p.waves == 0 || cost < best) {
+                best = cost;
+                p.waves = waves;
+                p.splits = cuts;
+            }
+            if (cuts > 1) p.parts = std::max(p.parts, tokens * n_q * cuts);
+        }
+    }
+    p.items = tokens * group / ((d == 256 ? 16 : 32) * p.waves) + batch;
     return p;
 }
 
@@ -1055,7 +1071,8 @@ hipError_t launch_split(const Args &a, hipStream_t stream)
     kv_attend_split_kernel<D, QT, split_occupancy(D, QT)><<<groups, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // with 16 parts a sequence or more, four waves join a row
+    // with 16 parts a sequence or more, four waves join a row (1 x 131k tokens, 64 heads on
+    // 8: 53 us, 59 with one wave; 32 x 4k: 55, 53 with one)
     if (a.workers >= 16 * a.batch.batch) kv_join_kernel<D, QT, 4><<<groups * 16 * QT, 256, 0, stream>>>(a);
     else kv_join_kernel<D, QT, 1><<<groups * 16 * QT, 64, 0, stream>>>(a);
     return hipGetLastError();
