@@ -203,6 +203,10 @@ def test_drafted_tokens():
     (64, 64, 2, 16, [300, 900, 65], [5, 6, 4]),
     (96, 256, 1, 8, [700, 513], [5, 5]),
     (64, 64, 600, 600, [70], [1]),                    # more kv heads than workgroups
+    (64, 64, 2, 16, [300, 200, 65], [5, 6, 4]),       # few tokens: a row block a worker, no joining
+    (128, 64, 2, 4, [300, 64, 130], [1, 40, 3]),
+    (96, 128, 1, 8, [300, 200], [3, 5]),
+    (256, 64, 2, 4, [100, 150], [2, 3]),
     (64, 64, 1, 1024, [130, 64], [1, 2]),             # a token's heads fill several row blocks
     (128, 64, 3, 21, [200, 77], [3, 20]),             # seven heads a kv head
 ])
@@ -262,6 +266,19 @@ def test_many_sequences_of_many_rows():
     w.check_storage()
     w.attend(n, 4, front=1, back=2)
     w.attend(n, 4, window=50, sinks=2)
+
+
+@pytest.mark.parametrize("most", [256, 4096])
+def test_many_sequences_of_few_rows(most):
+    """The same for the kernel of single and drafted tokens: with a short table a
+    row block a worker, with a long one equal runs."""
+    rng = np.random.default_rng(3)
+    held = rng.integers(0, 150, 140).tolist()
+    n = [min(h, int(k)) for h, k in zip(held, rng.integers(0, 4, 140))]
+    w = World(140, 2, 64, 64, seed=8, most=most)
+    w.append(held)
+    w.attend(n, 8, front=1, back=2)
+    w.attend(n, 8, window=50, sinks=2)
 
 
 def test_two_gib_of_queries_apart():

@@ -106,6 +106,7 @@ struct Args {
     float scale;                 // times log2(e)
     int window, sinks, page_shift;
     int workers;                 // per kv head, of the split kernel
+    bool whole;                  // a worker has a row block to itself
     double inv_workers;
     float *part, *stats;         // sums and (m, l) of unfinished row blocks
     int32_t *notes;              // [workers][4]: what the joining kernel has to do
@@ -154,7 +155,7 @@ struct Roster {
         s = {0, 0, 0, 0};
         if (b < a.batch.batch) {
             s = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
-            if (s.n) units = (int64_t)((s.n * a.group + RB - 1) / RB) * (visible_tiles(a, s).count + kStart);
+            if (s.n) units = (int64_t)((s.n * a.group + RB - 1) / RB) * (a.whole ? 1 : visible_tiles(a, s).count + kStart);
         }
         end = kv_wave_scan(units);
     }
@@ -427,14 +428,15 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
 }
 
 // One kv head's work is cut into equal runs of units, one for each worker (a
-// workgroup), whatever the sequences' lengths; a worker's four waves take its
+// workgroup), whatever the sequences' lengths (or, with few tokens, a worker takes a
+// row block as a whole: then the row blocks are the units); a worker's four waves take its
 // tiles in turn and join at the end of each row block.  A row block that one
 // worker has whole is finished there; the others' parts go to the workspace: the
 // run's first row block to place 0, its last to place 1.  The worker that has a
 // shared row block's first tile leaves a note for the kernel that joins them.
 // Bound by HBM with many tokens (32 x 32k, 64 query heads on 8: 377 us, 5.7 TB/s; 64
 // ragged sequences of 4k on average: 67 us, 4.7 TB/s, where a fixed number of cuts for
-// each sequence took 89), by latency with few (1 x 500 tokens: 10.6 us with the join).
+// each sequence took 89), by latency with few (1 x 500 tokens: 9.1 us, uncut).
 // Pages go from memory to operand registers: no wave shares a tile with another, so
 // LDS would add a trip and a barrier.  P is used as two fp16 parts, whose second one
 // costs little here (5 rows of 8 sequences: 21.8 us, 20.0 without it).
@@ -455,9 +457,12 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         roster.load(a, c);
         units += kv_lane(roster.end, 63);
     }
-    int64_t run = (int64_t)((double)units * a.inv_workers);
-    while (run * a.workers < units) ++run;
-    run = max(run, (int64_t)kWaves);
+    int64_t run = 1;
+    if (!a.whole) {
+        run = (int64_t)((double)units * a.inv_workers);
+        while (run * a.workers < units) ++run;
+        run = max(run, (int64_t)kWaves);
+    }
     int64_t u = run * worker;
     const int64_t end = min(u + run, units);
     int note_row = 0, note_rows = 0, note_parts = 0, note_place = 0;
@@ -487,9 +492,9 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         const KvSeq seq = roster.get(b & 63);
         const Tiles tiles = visible_tiles(a, seq);
         const int rows = seq.n * a.group;
-        const int per_block = tiles.count + kStart, rb = (int)(off / per_block), at = (int)(off - (int64_t)rb * per_block);
+        const int per_block = a.whole ? 1 : tiles.count + kStart, rb = (int)(off / per_block), at = (int)(off - (int64_t)rb * per_block);
         const int take = (int)min((int64_t)(per_block - at), end - u);
-        const int t0 = max(at - kStart, 0), count = max(at + take - kStart, 0) - t0;
+        const int t0 = max(at - kStart, 0), count = a.whole ? tiles.count : max(at + take - kStart, 0) - t0;
         const int64_t last = u - at + per_block - 1;         // the row block's last unit
         u += take;
         off += take;
@@ -574,7 +579,7 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         }
         place = 1;
     }
-    if (h == 0 && threadIdx.x == 0) {
+    if (!a.whole && h == 0 && threadIdx.x == 0) {
         int32_t *n = a.notes + worker * 4;
         n[0] = note_row;
         n[1] = note_rows;
@@ -1016,6 +1021,7 @@ constexpr int split_occupancy(int d, int qt) { return (d <= 64 && qt <= 2) || (d
 // `splits` runs of tiles.
 struct Plan {
     int qt, waves, splits, workers;
+    bool whole;                  // the split kernel with a worker for each row block
     int64_t items, parts;        // row blocks of the rows kernel (an upper bound); rows of workspace, whatever the lengths
 };
 
@@ -1031,6 +1037,20 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
         const int groups = 256 * split_occupancy(d, p.qt);       // workgroups that the 256 CUs hold at once
         p.workers = n_kv < groups ? (groups + n_kv - 1) / n_kv : 1;
         p.parts = (int64_t)p.workers * n_kv * 2 * 16 * p.qt;
+        // A worker for each row block, with no second launch, where that is 3.3 us and a tile
+        // 0.42 us of a worker (0.8 where it has a CU to itself): 32 heads, 500 tokens 9.1 us,
+        // 10.4 cut; 1000 tokens 12.4 and 10.6; 64 x 500 on average, 8 kv heads 16.4 and 25.8,
+        // 64 x 1000 22.4 and 28.6, 256 x 1000 107 and 101; d = 256, 500 tokens 14.8 and 14.2.
+        // Up to 32 tiles: the host sees only what the table holds, and one long sequence
+        // among short ones is then a worker's alone.
+        const int rb = 16 * p.qt;
+        const int64_t blocks = tokens * group / rb + batch;
+        const int64_t tiles = std::min(most, span + rb / group + 2 * kTile) / kTile;
+        const int64_t cut = std::max(tiles * ((rows + rb - 1) / rb * batch * n_kv) / groups, (int64_t)kWaves) + 4 * split_occupancy(d, p.qt);
+        if (tiles <= 32 && tiles <= cut) {
+            p.whole = true;
+            p.workers = (int)blocks;
+        }
         return p;
     }
     // Waves and cuts by what they cost: a workgroup takes 8 us and 2 a tile, one of four
@@ -1070,7 +1090,7 @@ hipError_t launch_split(const Args &a, hipStream_t stream)
     const unsigned groups = (unsigned)(a.workers * a.cache.n_kv);
     kv_attend_split_kernel<D, QT, split_occupancy(D, QT)><<<groups, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.whole) return e;
     // with 16 parts a sequence or more, four waves join a row (1 x 131k tokens, 64 heads on
     // 8: 53 us, 59 with one wave; 32 x 4k: 55, 53 with one)
     if (a.workers >= 16 * a.batch.batch) kv_join_kernel<D, QT, 4><<<groups * 16 * QT, 256, 0, stream>>>(a);
@@ -1126,7 +1146,7 @@ hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch
     float *part = (float *)workspace;
     float *stats = part + p.parts * cache.d;
     const Args a = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, window, sinks,
-                    __builtin_ctz(cache.page), p.workers, p.workers ? 1.0 / p.workers : 0.0, part, stats,
+                    __builtin_ctz(cache.page), p.workers, p.whole, p.workers ? 1.0 / p.workers : 0.0, part, stats,
                     reinterpret_cast<int32_t *>(stats + p.parts * 2), out};
     switch (cache.d) {
     case 64: return launch<64>(a, p, stream);
