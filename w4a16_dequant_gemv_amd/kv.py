@@ -174,7 +174,7 @@ class PagedBatch:
             _need(t, torch.int32, shape, name)
         _same_device(cu_q, ctx_lens, block_table, slots)
         self._tensors, self._device = (cu_q, ctx_lens, block_table, slots), cu_q.device
-        self._known, self._shapes = None, tuple(t.shape for t in self._tensors)
+        self._known, self._sizes = None, tuple(t.numel() for t in self._tensors)
 
     cu_q = property(lambda self: self._tensors[0])
     ctx_lens = property(lambda self: self._tensors[1])
@@ -185,7 +185,7 @@ class PagedBatch:
         if self._device != device:
             raise W4A16Error("all tensors must be on the same GPU")
         q, c, t, s = self._tensors
-        if (q.shape, c.shape, t.shape, s.shape) != self._shapes:       # resized in place: checked again
+        if (q.numel(), c.numel(), t.numel(), s.numel()) != self._sizes:        # resized in place: checked again
             self.__init__(q, c, t, s)
         at = (q.data_ptr(), c.data_ptr(), t.data_ptr(), s.data_ptr(), tokens)
         known = self._known
@@ -232,8 +232,8 @@ class PagedKVCache:
     def _checked(self):
         """The six tensors as the library's struct, checked when one was replaced."""
         k, v, ks, vs, kt, vt = now = self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail
-        at = (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kt.data_ptr(), vt.data_ptr(), k.shape[0],
-              kt.shape[0], self.n_kv, self.d, self.page)
+        at = (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kt.data_ptr(), vt.data_ptr(),
+              k.numel(), kt.numel(), self.n_kv, self.d, self.page)
         known = self._known
         if known is not None and at == known[1] and all(map(operator.is_, now, known[0])):
             return known[2]
@@ -246,7 +246,7 @@ class PagedKVCache:
         _need(self.k_tail, torch.float16, (S, 2, *kshape), "k_tail")
         _need(self.v_tail, torch.float16, (S, 2, *vshape), "v_tail")
         _same_device(self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
-        known = self._known = now, at, _lib.PagedCache(*at)
+        known = self._known = now, at, _lib.PagedCache(*at[:6], P, S, *at[8:])
         return known[2]
 
     def append(self, k, v, batch, q=None, rope=None, positions=None, interleaved=False, q_out=None):
