@@ -452,13 +452,13 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
 
     // how many units there are, and what a worker takes: no less than a tile for each wave
     Roster<RB> roster;
-    int64_t units = 0;
-    for (int c = 0; c * 64 < a.batch.batch; ++c) {
-        roster.load(a, c);
-        units += kv_lane(roster.end, 63);
-    }
-    int64_t run = 1;
+    int64_t run = 1, units = worker + 1;
     if (!a.whole) {
+        units = 0;
+        for (int c = 0; c * 64 < a.batch.batch; ++c) {
+            roster.load(a, c);
+            units += kv_lane(roster.end, 63);
+        }
         run = (int64_t)((double)units * a.inv_workers);
         while (run * a.workers < units) ++run;
         run = max(run, (int64_t)kWaves);
@@ -1045,14 +1045,16 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
         // A worker for each row block, with no second launch, where that is 3.3 us and a tile
         // 0.42 us of a worker (0.8 where it has a CU to itself): 32 heads, 500 tokens 9.1 us,
         // 10.4 cut; 1000 tokens 12.4 and 10.6; 64 x 500 on average, 8 kv heads 16.4 and 25.8,
-        // 64 x 1000 22.4 and 28.6, 256 x 1000 107 and 101; d = 256, 500 tokens 14.8 and 14.2.
-        // Up to 32 tiles: the host sees only what the table holds, and one long sequence
-        // among short ones is then a worker's alone.
+        // 64 x 1000 22.4 and 28.6; d = 256, 500 tokens 14.8 and 14.2.  Up to 32 tiles: the host
+        // sees only what the table holds, and one long sequence among short ones is then a
+        // worker's alone.  Up to four rounds of workers, since each begins and looks for its
+        // sequence anew: 256 x 250 47 and 50, 512 x 250 127 and 106.
         const int rb = 16 * p.qt;
         const int64_t blocks = tokens * group / rb + batch;
         const int64_t tiles = std::min(most, span + rb / group + 2 * kTile) / kTile;
-        const int64_t cut = std::max(tiles * ((rows + rb - 1) / rb * batch * n_kv) / groups, (int64_t)kWaves) + 4 * split_occupancy(d, p.qt);
-        if (tiles <= 32 && tiles <= cut) {
+        const int64_t all = (rows + rb - 1) / rb * batch * n_kv;
+        const int64_t cut = std::max(tiles * all / groups, (int64_t)kWaves) + 4 * split_occupancy(d, p.qt);
+        if (tiles <= 32 && tiles <= cut && all <= 4 * groups) {
             p.whole = true;
             p.workers = (int)blocks;
         }
