@@ -268,17 +268,23 @@ def test_many_sequences_of_many_rows():
     w.attend(n, 4, window=50, sinks=2)
 
 
-@pytest.mark.parametrize("most", [256, 4096])
-def test_many_sequences_of_few_rows(most):
-    """The same for the kernel of single and drafted tokens: with a short table a
-    row block a worker, with a long one equal runs."""
+@pytest.mark.parametrize("d,n_kv,n_q,most", [
+    (64, 2, 8, 4096),                                 # a long table: equal runs
+    (64, 2, 8, 256),                                  # a short one: a row block a workgroup
+    (64, 16, 64, 256),                                # and with many row blocks a wave
+    (96, 8, 96, 256),
+    (128, 8, 80, 256),
+    (256, 8, 8, 256),
+])
+def test_many_sequences_of_few_rows(d, n_kv, n_q, most):
+    """The same for the kernels of single and drafted tokens."""
     rng = np.random.default_rng(3)
     held = rng.integers(0, 150, 140).tolist()
     n = [min(h, int(k)) for h, k in zip(held, rng.integers(0, 4, 140))]
-    w = World(140, 2, 64, 64, seed=8, most=most)
+    w = World(140, n_kv, d, 64, seed=8, most=most)
     w.append(held)
-    w.attend(n, 8, front=1, back=2)
-    w.attend(n, 8, window=50, sinks=2)
+    w.attend(n, n_q, front=1, back=2)
+    w.attend(n, n_q, front=45, window=50, sinks=2)
 
 
 def test_two_gib_of_queries_apart():

@@ -264,8 +264,33 @@ struct PageScales {
     }
 };
 
-// Tiles t0, t0 + 4, ... < t1 of one row block, into the wave's state.
+// A row block's state before its first tile: row block rb of the sequence for kv head h.
 template <int D, int QT>
+__device__ __forceinline__ void begin(Wave<D, QT> &s, const Args &a, const KvSeq &seq, int h, int rb)
+{
+    constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 16 * QT;
+    const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int r = rb * RB + t * 16 + m16, tok = r / a.group;
+        s.at[t] = seq.ctx + tok;
+        s.m[t] = kNone;
+        s.l[t] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) s.o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const uint16_t *row = a.q + (int64_t)(seq.q0 + tok) * a.q_stride + (h * a.group + r - tok * a.group) * D;
+#pragma unroll
+        for (int e = 0; e < 2 * KS; ++e) {
+            const int ch = (e >> 1) * 64 + g * 16 + (e & 1) * 8;
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (r < seq.n * a.group && ch < D) v = *reinterpret_cast<const u32x4 *>(row + ch);
+            s.q[t][e] = bitcast<f16x8>(v);
+        }
+    }
+}
+
+// Tiles t0, t0 + STEP, ... < t1 of one row block, into the wave's state.
+template <int STEP, int D, int QT>
 __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, const KvSeq &seq, int b, int h,
                                              const Tiles &tiles, int t0, int t1, int at_min, int at_max)
 {
@@ -274,7 +299,7 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
     const int n_kv = a.cache.n_kv, page = 1 << a.page_shift, head = page * D;
     const int full = seq.total() >> a.page_shift << a.page_shift;      // tokens in finished pages
     const bool mine = 4 * (KS - 1) + g < DT;                           // the last K load's channels exist (D = 96)
-    int n = t1 > t0 ? (t1 - t0 + kWaves - 1) / kWaves : 0;
+    int n = t1 > t0 ? (t1 - t0 + STEP - 1) / STEP : 0;
 
     // byte offsets inside a tile's K and V
     const int k_lane = (g * 16 + m16) * 16, v_lane = (g * D + m16) * 16;
@@ -284,7 +309,7 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
         int tok0 = 0, id = -1;
         const int many = min(n - base, 64);
         if (lane < many) {
-            tok0 = tiles.at(t0 + (base + lane) * kWaves) * kTile;
+            tok0 = tiles.at(t0 + (base + lane) * STEP) * kTile;
             if (tok0 < full) id = a.batch.block_table[(int64_t)b * a.batch.table_cols + (tok0 >> a.page_shift)];
         }
         const bool there = id >= 0 && id < a.cache.pages;
@@ -443,7 +468,7 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
 template <int D, int QT, int OCC>
 __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
 {
-    constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 16 * QT;
+    constexpr int DT = D / 16, RB = 16 * QT;
     constexpr int PAD = D + 4;                       // floats a row of the joining buffer: four banks on per row
     __shared__ float joint[kWaves][16 * PAD], stat_m[kWaves][RB], stat_l[kWaves][RB];
     const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
@@ -501,26 +526,10 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         if (count == 0) continue;                            // only the beginning is this worker's
 
         Wave<D, QT> s;
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            const int r = rb * RB + t * 16 + m16, tok = r / a.group;
-            s.at[t] = seq.ctx + tok;
-            s.m[t] = kNone;
-            s.l[t] = 0.0f;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) s.o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const uint16_t *row = a.q + (int64_t)(seq.q0 + tok) * a.q_stride + (h * a.group + r - tok * a.group) * D;
-#pragma unroll
-            for (int e = 0; e < 2 * KS; ++e) {
-                const int ch = (e >> 1) * 64 + g * 16 + (e & 1) * 8;
-                u32x4 v = {0u, 0u, 0u, 0u};
-                if (r < rows && ch < D) v = *reinterpret_cast<const u32x4 *>(row + ch);
-                s.q[t][e] = bitcast<f16x8>(v);
-            }
-        }
+        begin(s, a, seq, h, rb);
         const int at_min = seq.ctx + rb * RB / a.group;
         const int at_max = seq.ctx + (min(rb * RB + RB, rows) - 1) / a.group;
-        attend_tiles<D, QT>(s, a, seq, b, h, tiles, t0 + wave, t0 + count, at_min, at_max);
+        attend_tiles<kWaves>(s, a, seq, b, h, tiles, t0 + wave, t0 + count, at_min, at_max);
 
         // join the waves
 #pragma unroll
@@ -585,6 +594,47 @@ __global__ __launch_bounds__(kThreads, OCC) void kv_attend_split_kernel(Args a)
         n[1] = note_rows;
         n[2] = note_parts;
         n[3] = note_place;
+    }
+}
+
+// Many row blocks with few tokens each: a wave takes one to itself, so nothing is
+// joined and no wave waits for another.  Row block `item` of a kv head is found without
+// a pass over the sequences: sequence b's numbers begin at rows_before(b) / RB + b, which
+// leaves each of them room enough.
+template <int D, int QT, int OCC>
+__global__ __launch_bounds__(64, OCC) void kv_attend_wave_kernel(Args a)
+{
+    constexpr int DT = D / 16, RB = 16 * QT;
+    const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
+    const int h = blockIdx.x % a.cache.n_kv, item = blockIdx.x / a.cache.n_kv;
+    auto number = [&](int b) {
+        const int before = min(max(a.batch.cu_q[b], 0), (int)a.batch.tokens);
+        return (int64_t)before * a.group / RB + b;
+    };
+    int b = 0;                                               // the last sequence that begins at or before `item`
+    for (int many = a.batch.batch; many > 0;) {
+        const int step = (many + 63) / 64, p = lane * step;
+        const int n = __popcll(__ballot(p < many && number(b + p) <= item));
+        if (n == 0) return;                                  // before the first one: padding
+        b += (n - 1) * step;
+        many = step > 1 ? min(step, many - (n - 1) * step) : 0;
+    }
+    const KvSeq seq = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
+    const int rows = seq.n * a.group, rb = item - (int)number(b);
+    if (rb < 0 || rb * RB >= rows) return;
+    const Tiles tiles = visible_tiles(a, seq);
+    Wave<D, QT> s;
+    begin(s, a, seq, h, rb);
+    attend_tiles<1>(s, a, seq, b, h, tiles, 0, tiles.count, seq.ctx + rb * RB / a.group,
+                    seq.ctx + (min(rb * RB + RB, rows) - 1) / a.group);
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int r = rb * RB + t * 16 + m16, tok = r / a.group;
+        const float l = column_sum(s.l[t]);
+        if (r >= rows) continue;
+        uint16_t *to = a.out + ((int64_t)(seq.q0 + tok) * a.n_q + h * a.group + r - tok * a.group) * D + g * 4;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) store_out(to + d * 16, s.o[t][d], l);
     }
 }
 
@@ -1026,11 +1076,11 @@ constexpr int split_occupancy(int d, int qt) { return (d <= 64 && qt <= 2) || (d
 // `splits` runs of tiles.
 struct Plan {
     int qt, waves, splits, workers;
-    bool whole;                  // the split kernel with a worker for each row block
+    int alone;                   // waves that have a row block to themselves, 0: none, workers' runs share them
     int64_t items, parts;        // row blocks of the rows kernel (an upper bound); rows of workspace, whatever the lengths
 };
 
-// Sequences have at most `most` tokens, and a row sees at most `span` of them.
+// Sequences have about `most` tokens at most, and a row sees at most `span` of them.
 Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most, int64_t span)
 {
     Plan p = {};
@@ -1042,21 +1092,23 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
         const int groups = 256 * split_occupancy(d, p.qt);       // workgroups that the 256 CUs hold at once
         p.workers = n_kv < groups ? (groups + n_kv - 1) / n_kv : 1;
         p.parts = (int64_t)p.workers * n_kv * 2 * 16 * p.qt;
-        // A worker for each row block, with no second launch, where that is 3.3 us and a tile
-        // 0.42 us of a worker (0.8 where it has a CU to itself): 32 heads, 500 tokens 9.1 us,
-        // 10.4 cut; 1000 tokens 12.4 and 10.6; 64 x 500 on average, 8 kv heads 16.4 and 25.8,
-        // 64 x 1000 22.4 and 28.6; d = 256, 500 tokens 14.8 and 14.2.  Up to 32 tiles: the host
-        // sees only what the table holds, and one long sequence among short ones is then a
-        // worker's alone.  Up to four rounds of workers, since each begins and looks for its
-        // sequence anew: 256 x 250 47 and 50, 512 x 250 127 and 106.
+        // Where rows see few tokens, a row block is left whole, which saves the second launch:
+        // a workgroup for each or, with many, a wave.  By what each costs (us; a round is what
+        // the CUs hold): 32 heads and 500 tokens, cut, a workgroup, a wave: 10.4, 9.1, 15.7;
+        // 1000 tokens 10.6, 12.4; 64 x 250 tokens on average, 8 kv heads 21.3, 11.6, 13.6;
+        // 256 x 250 49.6, 47.5, 26.7; 1024 x 250 216, 335, 122; 128 x 1000 46, 42, 48.
+        // Only up to 32 tiles: the host sees no more than what the table holds, and one long
+        // sequence among short ones would keep its wave busy alone.
         const int rb = 16 * p.qt;
-        const int64_t blocks = tokens * group / rb + batch;
-        const int64_t tiles = std::min(most, span + rb / group + 2 * kTile) / kTile;
-        const int64_t all = (rows + rb - 1) / rb * batch * n_kv;
-        const int64_t cut = std::max(tiles * all / groups, (int64_t)kWaves) + 4 * split_occupancy(d, p.qt);
-        if (tiles <= 32 && tiles <= cut && all <= 4 * groups) {
-            p.whole = true;
-            p.workers = (int)blocks;
+        const double all = (double)((rows + rb - 1) / rb * batch * n_kv) / groups;           // in rounds
+        const double tiles = (double)std::min(most, span + rb / group + 2 * kTile) / kTile;
+        const double tile = split_occupancy(d, p.qt) == 2 ? 0.45 : 0.8;
+        const double cut = 9.5 + tile * std::max((tiles + kStart) * all, (double)kWaves);
+        const double group4 = std::max(all, 1.0) * (6.0 + tile * tiles);
+        const double one = std::max(all / 4, 1.0) * (6.0 + 4 * tile * tiles);
+        if (tiles <= 32 && std::min(group4, one) < cut) {
+            p.alone = one < group4 ? 1 : kWaves;
+            p.workers = (int)(tokens * group / rb + batch);
         }
         return p;
     }
@@ -1092,9 +1144,13 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
 }
 
 template <int D, int QT>
-hipError_t launch_split(const Args &a, hipStream_t stream)
+hipError_t launch_split(const Args &a, const Plan &p, hipStream_t stream)
 {
     const unsigned groups = (unsigned)(a.workers * a.cache.n_kv);
+    if (p.alone == 1) {
+        kv_attend_wave_kernel<D, QT, split_occupancy(D, QT)><<<groups, 64, 0, stream>>>(a);
+        return hipGetLastError();
+    }
     kv_attend_split_kernel<D, QT, split_occupancy(D, QT)><<<groups, kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.whole) return e;
@@ -1125,12 +1181,12 @@ hipError_t launch_rows(const Args &a, const Plan &p, hipStream_t stream)
 template <int D>
 hipError_t launch(const Args &a, const Plan &p, hipStream_t stream)
 {
-    if (p.qt == 1) return launch_split<D, 1>(a, stream);
+    if (p.qt == 1) return launch_split<D, 1>(a, p, stream);
     if constexpr (D == 256) {
         return launch_rows<D, 8, 1>(a, p, stream);
     } else {
-        if (p.qt == 2) return launch_split<D, 2>(a, stream);
-        if (p.qt == 3) return launch_split<D, 3>(a, stream);
+        if (p.qt == 2) return launch_split<D, 2>(a, p, stream);
+        if (p.qt == 3) return launch_split<D, 3>(a, p, stream);
         return p.waves == 8 ? launch_rows<D, 8, 2>(a, p, stream) : launch_rows<D, 4, 2>(a, p, stream);
     }
 }
@@ -1147,13 +1203,13 @@ hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch
                                int64_t q_stride, int n_q, float scale, int window, int sinks, void *workspace,
                                uint16_t *out, hipStream_t stream)
 {
-    const int64_t most = (int64_t)(batch.table_cols + 1) * cache.page;
+    const int64_t most = (int64_t)batch.table_cols * cache.page;
     const Plan p = plan_for(batch.tokens, batch.batch, n_q, cache.n_kv, cache.d, most,
                             window > 0 ? (int64_t)window + sinks : most);
     float *part = (float *)workspace;
     float *stats = part + p.parts * cache.d;
     const Args a = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, window, sinks,
-                    __builtin_ctz(cache.page), p.workers, p.whole, p.workers ? 1.0 / p.workers : 0.0, part, stats,
+                    __builtin_ctz(cache.page), p.workers, p.alone == kWaves, p.workers ? 1.0 / p.workers : 0.0, part, stats,
                     reinterpret_cast<int32_t *>(stats + p.parts * 2), out};
     switch (cache.d) {
     case 64: return launch<64>(a, p, stream);
