@@ -185,8 +185,9 @@ int64_t kv_paged_attention_workspace_size(int64_t tokens, int32_t batch, int32_t
  * gives zeros.  Rows of no sequence are left as they were.  An infinity or NaN in
  * the k or v of a token that is read from the ring gives NaN in the rows that see
  * the token (with a weight above zero) and reaches no other; one that was
- * quantized has spoiled its page.  `workspace`: device
- * memory of at least kv_paged_attention_workspace_size bytes, 16-byte aligned,
+ * quantized has spoiled its page for its kv head: NaN in the rows that see any of the
+ * page's tokens, and in no other.  A page with scales of 0 (nobody filled it) counts as
+ * zeros.  `workspace`: device memory of at least kv_paged_attention_workspace_size bytes, 16-byte aligned,
  * overwritten; calls sharing a workspace must not overlap.  Results are
  * deterministic for given inputs and sizes.
  */

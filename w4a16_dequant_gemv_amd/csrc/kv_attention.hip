@@ -8,7 +8,9 @@
 //   O = sum P_j c_j,  l = sum P_j / vs,  o = O / l,
 // so the second product also takes plain integer codes, and pages of very
 // different scales cannot overflow P.  The unfinished page is read from the
-// fp16 ring with ks = vs = 1.
+// fp16 ring with ks = vs = 1.  Scores are scaled first and hidden tokens set to -inf
+// after that, so whatever a page's scales are (infinite or NaN where an infinity or
+// NaN was quantized), a row that sees none of its tokens gets weights of 0 from it.
 //
 // Layout.  A wave takes tiles of 64 tokens.  S^T = K Q^T with
 // v_mfma_f32_16x16x32_f16: a lane holds scores of one query (column lane % 16)
@@ -176,7 +178,7 @@ struct Wave {
     int at[QT];                  // the row's index in its sequence
 };
 
-// Scores x[a][i] of one query (row index `at`): those of tokens that it does not
+// Exponents x[a][i] of one query (row index `at`): those of tokens that it does not
 // see become -inf.
 __device__ __forceinline__ void hide(f32x4 x[4], const Args &a, int at, int tile0)
 {
@@ -191,9 +193,18 @@ __device__ __forceinline__ void hide(f32x4 x[4], const Args &a, int at, int tile
         }
 }
 
-// Scores to weights.  First the running maximum, which follows the scores only
-// in steps (each step costs a pass over O); returns the factor for what was
-// summed before, 1 nearly always.  c1 = scale log2(e) ks > 0, w = log2(vs).
+// Scores to exponents: c1 = scale log2(e) ks > 0, w = log2(vs).
+__device__ __forceinline__ void scale_scores(f32x4 x[4], float c1, float w)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = __builtin_fmaf(x[i][j], c1, w);
+}
+
+// Scores to weights.  First the running maximum of their exponents x c1 + w, which
+// follows them only in steps (each step costs a pass over O); returns the factor for
+// what was summed before, 1 nearly always.
 __device__ __forceinline__ float weigh_max(const f32x4 x[4], float c1, float w, float &m_run)
 {
     float top = -INFINITY;
@@ -234,11 +245,12 @@ template <int D, int QT>
 __device__ __forceinline__ void weigh(Wave<D, QT> &s, int t, f32x4 x[4], const Args &a, bool masked, int tile0, float c1,
                                       float w, float inv, f16x8 hi[2], f16x8 lo[2])
 {
+    scale_scores(x, c1, w);
     if (masked) hide(x, a, s.at[t], tile0);
-    const float keep = weigh_max(x, c1, w, s.m[t]);
+    const float keep = weigh_max(x, 1.0f, 0.0f, s.m[t]);
     float sum = 0.0f;
-    weigh_exp(x, 0, c1, w - s.m[t] + kLift, hi, sum, lo);
-    weigh_exp(x, 1, c1, w - s.m[t] + kLift, hi, sum, lo);
+    weigh_exp(x, 0, 1.0f, kLift - s.m[t], hi, sum, lo);
+    weigh_exp(x, 1, 1.0f, kLift - s.m[t], hi, sum, lo);
     s.l[t] = s.l[t] * keep + sum * inv;
     if (__ballot(keep != 1.0f)) {
 #pragma unroll
@@ -251,14 +263,18 @@ __device__ __forceinline__ float lane_value(float v, int i)
     return bitcast<float>(__builtin_amdgcn_readlane(bitcast<int>(v), i));
 }
 
-// What a tile's page contributes to the scores: c1 is kept positive so that a
-// masked score stays -inf, and a page that is not there has weight 2^-inf.
+// What a tile's page contributes to the scores.  A page that is not there has weight
+// 2^-inf.  Scales that are not finite give NaN to every token of the page (and nothing
+// to rows that see none: w and inv stay finite).  A page that nobody filled has scales
+// of 0 and counts as zeros: for V, 2^-100 stands for 0 and vanishes in every output.
 struct PageScales {
     float c1, w, inv;
     __device__ PageScales() : c1(1.0f), w(-INFINITY), inv(0.0f) {}
     __device__ void set(float scale, float ks, float vs)
     {
-        c1 = fmaxf(scale * ks, 1e-30f);
+        const bool finite = ks < INFINITY && vs < INFINITY;
+        vs = finite ? fmaxf(vs, 0x1p-100f) : 1.0f;
+        c1 = finite ? scale * ks : NAN;
         w = __builtin_amdgcn_logf(vs);
         inv = 1.0f / vs;
     }
@@ -863,7 +879,12 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attend_rows_kernel(Args a, int 
     auto vector_work = [&](int tile0, float c1, float w, float inv) {
         if (tile0 + kTile - 1 > at_min || (a.window > 0 && at_max - tile0 >= a.window && tile0 + kTile > a.sinks)) {
 #pragma unroll
-            for (int t = 0; t < QT; ++t) hide(x[t], a, at[t], tile0);
+            for (int t = 0; t < QT; ++t) {
+                scale_scores(x[t], c1, w);
+                hide(x[t], a, at[t], tile0);
+            }
+            c1 = 1.0f;                                     // all other tiles are scaled on the way to exp2 (425 us
+            w = 0.0f;                                      // on 2048 queries over 8192 tokens, 449 in a step apart)
         }
         float keep[QT];
         bool moved = false;
