@@ -93,7 +93,8 @@ int kv_flush_blocks(const uint16_t *k, const uint16_t *v, int64_t blocks, int32_
  * consecutive tokens of one sequence for one kv head, as int8 codes with one
  * fp32 scale for K and one for V (scale and codes by the map above, taken over
  * all page * d values: scale = max|x| / 127 floored at 1e-8, codes =
- * clamp(rint(x / scale), -128, 127), each step one binary32 operation).  A
+ * clamp(rint(x / scale), -128, 127), each step one binary32 operation; with a NaN
+ * among the values the scale is NaN, with an infinity infinite, whatever the codes).  A
  * page's scale needs all of its tokens, so the newest tokens stay in fp16: a
  * slot per sequence holds its last two pages (the ring; page p of the sequence
  * in half p % 2), a page that becomes full is quantized into the pool as well,

@@ -109,3 +109,75 @@ def test_a_page_with_zero_scales(way, most):
     s.k[p * page:(p + 1) * page] = 0
     s.v[p * page:(p + 1) * page] = 0
     w.attend([n] + [1] * others, n_q, window=window)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("d,page,steps,at", [
+    (64, 64, [30, 40], 10),              # in the ring when the page fills
+    (64, 64, [30, 40], 50),              # in the call that fills it
+    (128, 128, [300], 200),              # in a page of new tokens only
+    (96, 128, [127, 1], 127),            # the token that fills it
+    (256, 64, [60, 70], 63),
+    (128, 256, [256], 0),
+])
+def test_a_bad_value_in_a_page_that_becomes_full(d, page, steps, at, which, bad):
+    """The page's scale says so, and every row that sees the page is NaN; the other
+    head, K or V, and the other pages are what they are without it."""
+    n_kv, total = 2, sum(steps)
+    w = World(1, n_kv, d, page, seed=d + at)
+    k, v = w.values(total, n_kv), w.values(total, n_kv)
+    x = k if which == "k" else v
+    x[at, 1, d // 2] = bad
+    done = 0
+    for n in steps:
+        w.cache.append(to_dev(k[done:done + n]), to_dev(v[done:done + n]), w.batch([n], ctx=[done]))
+        done += n
+    torch.cuda.synchronize()
+    ks, vs = w.cache.k_scale.cpu().numpy(), w.cache.v_scale.cpu().numpy()
+    for p in range(total // page):
+        for name, y, scale in (("k", k, ks), ("v", v, vs)):
+            for h in range(n_kv):
+                with np.errstate(invalid="ignore"):
+                    got, want = scale[w.table[0, p], h], ref.quantize(y[p * page:(p + 1) * page, h])[1]
+                if name == which and h == 1 and p == at // page:
+                    assert np.isnan(got) if np.isnan(bad) else np.isinf(got)
+                else:
+                    assert got == want, (p, name, h)
+    pages = w.cache.read(to_dev(w.table[0, :1].copy()))["kv".index(which)]
+    if at < page and np.isnan(bad):
+        assert torch.isnan(pages[0, 1]).all()
+    assert torch.isfinite(pages[0, 0]).all()
+    w.seqs[0].append(*(np.where(np.isfinite(y), y, 0).astype(np.float16) for y in (k, v)))
+    q = w.values(1, 4)
+    y = w.cache.attend(to_dev(q), w.batch([1], ctx=[total - 1])).cpu().numpy()
+    o, size, most = ref.attend(w.seqs[0], q, d ** -0.5)
+    assert np.isnan(y[:, 2:]).all()
+    assert bool((np.abs(y - o) <= ref.tolerance(o, size, most, total, d))[:, :2].all())
+    # windows that have left the page
+    left = total - (at // page + 1) * page
+    if left > 1:
+        y = w.cache.attend(to_dev(q), w.batch([1], ctx=[total - 1]), window=left).cpu().numpy()
+        o, size, most = ref.attend(w.seqs[0], q, d ** -0.5, left)
+        assert bool((np.abs(y - o) <= ref.tolerance(o, size, most, total, d)).all())
+
+
+def test_positions_outside_the_table_stay_nan():
+    """A key that was rotated to a position outside the table is NaN in the ring, and
+    so is what sees it there; once its page is full, all that see the page."""
+    d, page = 64, 64
+    w = World(1, 1, d, page, seed=3)
+    table = ref.rope_table(40, d)
+    x = w.values(70, 2)
+    positions = (np.arange(70) % 40).astype(np.int32)
+    positions[33] = 40
+    k, v = (np.ascontiguousarray(x[:, i:i + 1]) for i in range(2))
+    for lo, hi in ((0, 50), (50, 70)):
+        w.cache.append(to_dev(k[lo:hi]), to_dev(v[lo:hi]), w.batch([hi - lo], ctx=[lo]), rope=to_dev(table),
+                       positions=to_dev(positions[lo:hi].copy()))
+        q = to_dev(w.values(hi - lo, 2))
+        y = w.cache.attend(q, w.batch([hi - lo], ctx=[lo]))
+        sees = torch.arange(lo, hi, device="cuda") >= (33 if lo == 0 else 0)
+        assert torch.isnan(y[sees]).all() and torch.isfinite(y[~sees]).all()
+        y = w.cache.attend(q[-1:], w.batch([1], ctx=[hi - 1]), window=6)
+        assert torch.isfinite(y).all()

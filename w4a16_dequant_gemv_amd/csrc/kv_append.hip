@@ -140,15 +140,28 @@ __device__ __forceinline__ Chunk rotated_unit(const uint16_t *x, int64_t row, in
     return u.turned ? turn(r, load_angles(rope, row, pc), rope.interleaved) : r;
 }
 
-// Largest of a value over the workgroup; `red` holds one float per wave.
-__device__ __forceinline__ float block_max(float a, float *red)
+// The largest magnitude, of two values each in x, joined to `top`.  Magnitudes are
+// compared as bit patterns, in whose order NaN stands above infinity: a page with a
+// NaN gets NaN for its scale.
+using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ u16x2 join_max(u16x2 top, const u32x4 &x)
 {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) a = fmaxf(a, __shfl_xor(a, o));
+    for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, bitcast<u16x2>(x[i] & 0x7FFF7FFFu));
+    return top;
+}
+
+// The same over the workgroup, as a value; `red` holds one pattern per wave.
+__device__ __forceinline__ float block_max(u16x2 top, uint32_t *red)
+{
+    uint32_t a = max((uint32_t)top[0], (uint32_t)top[1]);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, o));
     __syncthreads();                                   // earlier readers of red are done
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = a;
     __syncthreads();
-    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    return half_bits_to_float((uint16_t)max(max(red[0], red[1]), max(red[2], red[3])));
 }
 
 // Page `page_no` of sequence s, all of its tokens at hand: the first
@@ -156,7 +169,7 @@ __device__ __forceinline__ float block_max(float a, float *red)
 // (src, `stride` apart).
 template <int D, int T>
 __device__ void quantize_k_page(const uint16_t *src, int64_t stride, const KvSeq &s, const Rope &rope, int page_no,
-                                const uint16_t *ring, int8_t *codes, float *scale_out, float *red)
+                                const uint16_t *ring, int8_t *codes, float *scale_out, uint32_t *red)
 {
     constexpr int DC = D / 16, KU = T * DC, KN = (KU + kThreads - 1) / kThreads;
     const int tid = threadIdx.x;
@@ -164,7 +177,7 @@ __device__ void quantize_k_page(const uint16_t *src, int64_t stride, const KvSeq
     const int64_t row0 = (int64_t)s.q0 + page_no * T - s.ctx;  // row of the page's token 0
     auto place = [](int tok, int c) { return kv_k_index(tok, c >> 4, DC) + (c & 15); };
     Chunk x[KN];
-    float amax = 0.0f;
+    u16x2 top = {0, 0};
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
         // four tokens, whose codes lie side by side, in neighbouring threads
@@ -176,11 +189,10 @@ __device__ void quantize_k_page(const uint16_t *src, int64_t stride, const KvSeq
                         *reinterpret_cast<const u32x4 *>(ring + place(tok, unit.c1))};
             else
                 x[i] = rotated_unit(src + (row0 + tok) * stride, row0 + tok, pc, unit, rope);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(half_at(x[i], e)));
+            top = join_max(join_max(top, x[i].lo), x[i].hi);
         }
     }
-    const float scale = kv_scale(block_max(amax, red), 127.0f), r = __builtin_amdgcn_rcpf(scale);
+    const float scale = kv_scale(block_max(top, red), 127.0f), r = __builtin_amdgcn_rcpf(scale);
     if (tid == 0) *scale_out = scale;
 #pragma unroll
     for (int i = 0; i < KN; ++i) {
@@ -217,7 +229,7 @@ __device__ __forceinline__ void gather_v(Chunk x[4], const uint16_t *src, int64_
 
 template <int D, int T>
 __device__ void quantize_v_page(const uint16_t *src, int64_t stride, const KvSeq &s, int page_no, const uint16_t *ring,
-                                int8_t *codes, float *scale_out, float *red)
+                                int8_t *codes, float *scale_out, uint32_t *red)
 {
     constexpr int VU = T / 16 * (D / 4), VN = (VU + kThreads - 1) / kThreads;
     const int tid = threadIdx.x;
@@ -225,7 +237,7 @@ __device__ void quantize_v_page(const uint16_t *src, int64_t stride, const KvSeq
     const int64_t row0 = (int64_t)s.q0 + page_no * T - s.ctx;
     // 16 tokens of four channels: x[i][channel] holds the tokens in order
     Chunk x[VN][4];
-    float amax = 0.0f;
+    u16x2 top = {0, 0};
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
         const int u = tid + i * kThreads, ch = u % (D / 4) * 4, t0 = u / (D / 4) * 16;
@@ -237,11 +249,9 @@ __device__ void quantize_v_page(const uint16_t *src, int64_t stride, const KvSeq
         }
         gather_v(x[i], src + (row0 + t0) * stride + ch, stride, old - t0, 16);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(half_at(x[i][e], j)));
+        for (int e = 0; e < 4; ++e) top = join_max(join_max(top, x[i][e].lo), x[i][e].hi);
     }
-    const float scale = kv_scale(block_max(amax, red), 127.0f), r = __builtin_amdgcn_rcpf(scale);
+    const float scale = kv_scale(block_max(top, red), 127.0f), r = __builtin_amdgcn_rcpf(scale);
     if (tid == 0) *scale_out = scale;
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
@@ -337,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(kv_paged_cache cach
 {
     constexpr int PC = D / 16, SHIFT = T == 64 ? 6 : T == 128 ? 7 : 8;
     constexpr int PAGE = D * T;
-    __shared__ float red[4];
+    __shared__ uint32_t red[4];
     const int n_kv = cache.n_kv;
     int g = blockIdx.x - edge_groups;                          // behind the edges, pages and q mixed: every
     int page_item = -1;                                        // `mix`-th workgroup is a page's while there are any
