@@ -4,7 +4,7 @@
 //   o = sum_j p_j vs c_j / sum_j p_j,   p_j = 2^(x_j),  x_j = log2(e) scale ks q . a_j.
 // The products q . a_j use the fp16 query and the exact integer codes; the
 // scales are applied to the fp32 sums.  vs goes into the exponent: with
-// e_j = x_j + log2(vs) and a running maximum m of the e_j, P_j = 2^(e_j - m),
+// e_j = x_j + log2(vs) and m a little below the running maximum of the e_j, P_j = 2^(e_j - m),
 //   O = sum P_j c_j,  l = sum P_j / vs,  o = O / l,
 // so the second product also takes plain integer codes, and pages of very
 // different scales cannot overflow P.  The unfinished page is read from the
@@ -29,9 +29,11 @@ namespace {
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kTile = 64;                  // tokens
 constexpr int kStart = 4;                  // what a row block's beginning costs, in tiles
-constexpr float kNone = -1e30f;            // running maximum before any token: below every score
-constexpr float kSlack = 5.0f;             // a query's maximum is raised only by more than this many powers of two,
-constexpr float kLift = 10.0f;             // so P is at most 2^15 and fp16 keeps weights down to 2^-24 of that at least
+constexpr float kNone = -1e30f;            // m before any token: below every score
+constexpr float kLift = 10.0f;             // m is put this many powers of two below the maximum, and raised only when the
+constexpr float kSlack = 5.0f;             // maximum is this many more above it: P is at most 2^15, and fp16 keeps weights
+                                           // down to 2^-34 of the largest
+constexpr float kFar = 0x1p18f;            // m beyond this: an exponent and m are both rounded before they meet
 
 // 16 codes of a lane as two operands, channel or token order kept.  The byte
 // c + 128 under the exponent of 1024 is the fp16 value 1152 + c, exactly.
@@ -202,9 +204,10 @@ __device__ __forceinline__ void scale_scores(f32x4 x[4], float c1, float w)
         for (int j = 0; j < 4; ++j) x[i][j] = __builtin_fmaf(x[i][j], c1, w);
 }
 
-// Scores to weights.  First the running maximum of their exponents x c1 + w, which
-// follows them only in steps (each step costs a pass over O); returns the factor for
-// what was summed before, 1 nearly always.
+// Scores to weights.  First m, which follows the maximum of the exponents x c1 + w only
+// in steps (each step costs a pass over O); returns the factor for what was summed before,
+// 1 nearly always.  Where m's own units are large, kLift below the maximum may come out
+// as more than kLift: then m is the maximum.
 __device__ __forceinline__ float weigh_max(const f32x4 x[4], float c1, float w, float &m_run)
 {
     float top = -INFINITY;
@@ -212,15 +215,17 @@ __device__ __forceinline__ float weigh_max(const f32x4 x[4], float c1, float w, 
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) top = fmaxf(top, x[i][j]);
-    const float now = column_max(top) * c1 + w, m = now > m_run + kSlack ? now : m_run;
+    const float now = __builtin_fmaf(column_max(top), c1, w), low = now - kLift;
+    const float m = now - m_run > kLift + kSlack ? now - low > kLift + 1.0f ? now : low : m_run;
     const float keep = __builtin_amdgcn_exp2f(m_run - m);
     m_run = m;
     return keep;
 }
 
 // Then P in fp16, and where `lo` is given the rest of P there, for the tokens of
-// the second product's step `half`; sum gets this lane's sum of P.  add = w - m +
-// kLift.
+// the second product's step `half`; sum gets this lane's sum of P.  add = w - m: its
+// rounding moves a tile's weights together by up to half a unit of m, so where that counts
+// (beyond kFar) the scores have been scaled before, c1 is 1, and e - m is exact for the largest.
 __device__ __forceinline__ void weigh_exp(const f32x4 x[4], int half, float c1, float add, f16x8 hi[2], float &sum,
                                           f16x8 *lo = nullptr)
 {
@@ -228,8 +233,8 @@ __device__ __forceinline__ void weigh_exp(const f32x4 x[4], int half, float c1, 
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(x[2 * half + i][j] * c1 + add);
-            const float p1 = __builtin_amdgcn_exp2f(x[2 * half + i][j + 1] * c1 + add);
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * half + i][j], c1, add));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * half + i][j + 1], c1, add));
             sum += p0 + p1;
             const f16x2 h = {(_Float16)p0, (_Float16)p1};
             hi[half][i * 4 + j] = h[0];
@@ -249,8 +254,8 @@ __device__ __forceinline__ void weigh(Wave<D, QT> &s, int t, f32x4 x[4], const A
     if (masked) hide(x, a, s.at[t], tile0);
     const float keep = weigh_max(x, 1.0f, 0.0f, s.m[t]);
     float sum = 0.0f;
-    weigh_exp(x, 0, 1.0f, kLift - s.m[t], hi, sum, lo);
-    weigh_exp(x, 1, 1.0f, kLift - s.m[t], hi, sum, lo);
+    weigh_exp(x, 0, 1.0f, -s.m[t], hi, sum, lo);
+    weigh_exp(x, 1, 1.0f, -s.m[t], hi, sum, lo);
     s.l[t] = s.l[t] * keep + sum * inv;
     if (__ballot(keep != 1.0f)) {
 #pragma unroll
@@ -876,6 +881,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attend_rows_kernel(Args a, int 
         __builtin_amdgcn_s_setprio(0);
     };
     // x to p
+    bool far = false;                                      // m of some row is beyond kFar
     auto vector_work = [&](int tile0, float c1, float w, float inv) {
         if (tile0 + kTile - 1 > at_min || (a.window > 0 && at_max - tile0 >= a.window && tile0 + kTile > a.sinks)) {
 #pragma unroll
@@ -891,18 +897,31 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attend_rows_kernel(Args a, int 
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             keep[t] = weigh_max(x[t], c1, w, m[t]);
-            const float add = w - m[t] + kLift;
-            float sum = 0.0f;
-            weigh_exp(x[t], 0, c1, add, p[t], sum);
-            weigh_exp(x[t], 1, c1, add, p[t], sum);
-            l[t] = l[t] * keep[t] + sum * inv;
             moved |= keep[t] != 1.0f;
         }
         if (__ballot(moved)) {
+            bool out = false;
 #pragma unroll
-            for (int t = 0; t < QT; ++t)
+            for (int t = 0; t < QT; ++t) {
+                l[t] *= keep[t];
+                out |= fabsf(m[t]) >= kFar && m[t] != kNone;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[t][d] *= keep[t];
+            }
+            far = __ballot(out) != 0;
+        }
+        if (far) {
+#pragma unroll
+            for (int t = 0; t < QT; ++t) scale_scores(x[t], c1, w);
+            c1 = 1.0f;
+            w = 0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            float sum = 0.0f;
+            weigh_exp(x[t], 0, c1, w - m[t], p[t], sum);
+            weigh_exp(x[t], 1, c1, w - m[t], p[t], sum);
+            l[t] += sum * inv;
         }
     };
 
