@@ -96,12 +96,17 @@ int kv_flush_blocks(const uint16_t *k, const uint16_t *v, int64_t blocks, int32_
  * clamp(rint(x / scale), -128, 127), each step one binary32 operation; with a NaN
  * among the values the scale is NaN, with an infinity infinite, whatever the codes).  A
  * page's scale needs all of its tokens, so the newest tokens stay in fp16: a
- * slot per sequence holds its last two pages (the ring; page p of the sequence
- * in half p % 2), a page that becomes full is quantized into the pool as well,
- * and readers take the unfinished page from the ring.  Since the ring keeps
- * two pages, a sequence can be shortened (drafted tokens taken back) by calling
- * again with a smaller ctx_lens, as far back as the first token of the page
- * before that of its last token.
+ * slot per sequence holds the two highest pages that it has reached (the ring;
+ * page p of the sequence in half p % 2), a page that becomes full is quantized
+ * into the pool as well, and readers take the unfinished page from the ring.
+ *
+ * A sequence can be shortened (drafted tokens taken back) by calling again with a
+ * smaller ctx_lens, no further than to the first token of the page before the
+ * highest one that it has reached, in however many steps: the ring gave page p's
+ * place to page p + 2 and does not get it back.  Beyond that only to a multiple of
+ * `page` (0 among them), where no page is unfinished, and from then on no further
+ * back than there.  The library cannot tell: a sequence that is shortened further
+ * reads a later page's tokens from the ring.
  *
  * Both pools have the order in which the attention kernels read them: inside
  * a page of one head, K is [page / 64][4][d / 16][16][16] -- token

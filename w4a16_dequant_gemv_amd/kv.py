@@ -197,8 +197,9 @@ class PagedBatch:
 class PagedKVCache:
     """One layer's paged INT8 cache (kv_paged_* in kv_codec.h): pages of `page`
     tokens with one scale per (page, kv head) for K and one for V, and a ring of
-    each sequence's last two pages in fp16, from which the unfinished page is
-    read.  Pages and rings are in the order of kv_codec.h; `read` gives pages in
+    the two highest pages that each sequence has reached in fp16, from which the
+    unfinished page is read.  Tokens can be taken back to the first one of those
+    pages, and beyond that only to a multiple of `page`.  Pages and rings are in the order of kv_codec.h; `read` gives pages in
     the order of tokens.  Block tables, lengths and slots are the caller's
     (PagedBatch), shared by a model's layers."""
 
