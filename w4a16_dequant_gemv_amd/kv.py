@@ -6,7 +6,6 @@ cache (PagedKVCache): appending new tokens with rotation, and attention over it.
 Only argument marshalling happens here: tensors must already live on the GPU
 and the library does all of the arithmetic on torch's current stream.
 """
-import operator
 from ctypes import byref
 
 import torch
@@ -203,13 +202,14 @@ class PagedKVCache:
     the order of tokens.  Block tables, lengths and slots are the caller's
     (PagedBatch), shared by a model's layers."""
 
+    _known = None                    # (addresses and sizes, the library's struct) of the last check
+
     def __init__(self, pool_pages, n_kv, d, slots, device, page=128):
         if page not in (64, 128, 256) or d not in (64, 96, 128, 256):
             raise W4A16Error(f"page must be 64, 128 or 256 and d 64, 96, 128 or 256, got {page} and {d}")
         if pool_pages < 1 or slots < 1 or not 1 <= n_kv <= 1024:
             raise W4A16Error("pool_pages and slots must be positive, n_kv in [1, 1024]")
         self.n_kv, self.d, self.page = n_kv, d, page
-        self._known = None
         kshape, vshape = self._shapes()
         self.k = torch.zeros((pool_pages, *kshape), dtype=torch.int8, device=device)
         self.v = torch.zeros((pool_pages, *vshape), dtype=torch.int8, device=device)
@@ -217,6 +217,11 @@ class PagedKVCache:
         self.v_scale = torch.zeros((pool_pages, n_kv), dtype=torch.float32, device=device)
         self.k_tail = torch.zeros((slots, 2, *kshape), dtype=torch.float16, device=device)
         self.v_tail = torch.zeros((slots, 2, *vshape), dtype=torch.float16, device=device)
+
+    def __setattr__(self, name, value):
+        """A replaced tensor is checked by the next call, and let go at once."""
+        object.__setattr__(self, "_known", None)
+        object.__setattr__(self, name, value)
 
     def _shapes(self):
         h, d, t = self.n_kv, self.d, self.page
@@ -232,12 +237,12 @@ class PagedKVCache:
 
     def _checked(self):
         """The six tensors as the library's struct, checked when one was replaced."""
-        k, v, ks, vs, kt, vt = now = self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail
+        k, v, ks, vs, kt, vt = self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail
         at = (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kt.data_ptr(), vt.data_ptr(),
-              k.numel(), kt.numel(), self.n_kv, self.d, self.page)
+              k.numel(), kt.numel())
         known = self._known
-        if known is not None and at == known[1] and all(map(operator.is_, now, known[0])):
-            return known[2]
+        if known is not None and known[0] == at:
+            return known[1]
         kshape, vshape = self._shapes()
         P, S = self.pool_pages, self.slots
         _need(self.k, torch.int8, (P, *kshape), "k")
@@ -247,8 +252,8 @@ class PagedKVCache:
         _need(self.k_tail, torch.float16, (S, 2, *kshape), "k_tail")
         _need(self.v_tail, torch.float16, (S, 2, *vshape), "v_tail")
         _same_device(self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
-        known = self._known = now, at, _lib.PagedCache(*at[:6], P, S, *at[8:])
-        return known[2]
+        known = self._known = at, _lib.PagedCache(*at[:6], P, S, self.n_kv, self.d, self.page)
+        return known[1]
 
     def append(self, k, v, batch, q=None, rope=None, positions=None, interleaved=False, q_out=None):
         """Put fp16 k, v [T, n_kv, d] behind each sequence's ctx_lens tokens; with
