@@ -48,3 +48,44 @@ def test_changed_sizes_are_checked():
         c.attend(q, b)
     c.page = 64
     assert np.array_equal(bits(c.attend(q, b)), bits(want))
+
+
+@pytest.mark.parametrize("name", TENSORS)
+def test_a_tensor_made_smaller_in_place_is_refused(name):
+    c, q, b, want = used()
+    t = getattr(c, name)
+    shape = t.shape
+    t.resize_(shape[0] - 1, *shape[1:])                  # its memory stays where it is
+    with pytest.raises(W4A16Error):
+        c.attend(q, b)
+    t.resize_(shape)
+    assert np.array_equal(bits(c.attend(q, b)), bits(want))
+
+
+def test_a_pool_made_smaller_in_place_is_used_as_such():
+    """All of its tensors: the pages that are gone are not visible any more."""
+    w = World(1, 1, 64, 64, seed=1)
+    w.append([200])
+    at = int(w.table[0, 1])
+    for name in ("k", "v", "k_scale", "v_scale"):
+        t = getattr(w.cache, name)
+        t.resize_(at, *t.shape[1:])
+    hidden = [p for p in range(3) if w.table[0, p] >= at]
+    w.attend([1], 4, hidden=hidden)
+
+
+def test_a_block_table_of_another_shape_in_place():
+    """The same number of entries in another shape, and a table turned in place."""
+    c, q, b, want = used()
+    table = b.block_table
+    rows, cols = table.shape
+    table.resize_(rows * cols // 2, 2)
+    with pytest.raises(W4A16Error):
+        c.attend(q, b)
+    table.resize_(rows, cols)
+    assert np.array_equal(bits(c.attend(q, b)), bits(want))
+    square = torch.full((2, 2), -1, dtype=torch.int32, device="cuda")
+    batch = kv.PagedBatch(b.cu_q, b.ctx_lens, square, b.slots)
+    square.t_()
+    with pytest.raises(W4A16Error, match="contiguous"):
+        c.attend(q, batch)

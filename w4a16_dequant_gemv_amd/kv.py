@@ -173,7 +173,7 @@ class PagedBatch:
             _need(t, torch.int32, shape, name)
         _same_device(cu_q, ctx_lens, block_table, slots)
         self._tensors, self._device = (cu_q, ctx_lens, block_table, slots), cu_q.device
-        self._known, self._sizes = None, tuple(t.numel() for t in self._tensors)
+        self._known, self._sizes = None, (*(t.numel() for t in self._tensors), block_table.shape[1])
 
     cu_q = property(lambda self: self._tensors[0])
     ctx_lens = property(lambda self: self._tensors[1])
@@ -184,8 +184,8 @@ class PagedBatch:
         if self._device != device:
             raise W4A16Error("all tensors must be on the same GPU")
         q, c, t, s = self._tensors
-        if (q.numel(), c.numel(), t.numel(), s.numel()) != self._sizes:        # resized in place: checked again
-            self.__init__(q, c, t, s)
+        if (q.numel(), c.numel(), t.numel(), s.numel(), t.shape[-1]) != self._sizes or not t.is_contiguous():
+            self.__init__(q, c, t, s)                          # changed in place: checked again
         at = (q.data_ptr(), c.data_ptr(), t.data_ptr(), s.data_ptr(), tokens)
         known = self._known
         if known is None or known[0] != at:
@@ -239,7 +239,7 @@ class PagedKVCache:
         """The six tensors as the library's struct, checked when one was replaced."""
         k, v, ks, vs, kt, vt = self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail
         at = (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kt.data_ptr(), vt.data_ptr(),
-              k.numel(), kt.numel())
+              k.numel(), v.numel(), ks.numel(), vs.numel(), kt.numel(), vt.numel())
         known = self._known
         if known is not None and known[0] == at:
             return known[1]
