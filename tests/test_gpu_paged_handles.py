@@ -1,6 +1,9 @@
 """PagedKVCache and PagedBatch as objects that a program keeps: tensors replaced,
 changed in place, copied and stored."""
+import copy
 import gc
+import io
+import pickle
 import weakref
 
 import numpy as np
@@ -89,3 +92,24 @@ def test_a_block_table_of_another_shape_in_place():
     square.t_()
     with pytest.raises(W4A16Error, match="contiguous"):
         c.attend(q, batch)
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle", "save"])
+def test_copies_of_a_used_cache(how):
+    """Copied or stored after calls, as before them; a deep copy goes its own way."""
+    c, q, b, want = used()
+    if how == "save":
+        f = io.BytesIO()
+        torch.save((c, b), f)
+        f.seek(0)
+        c2, b2 = torch.load(f, weights_only=False)
+    elif how == "pickle":
+        c2, b2 = pickle.loads(pickle.dumps((c, b)))
+    else:
+        c2, b2 = getattr(copy, how)(c), getattr(copy, how)(b)
+    assert np.array_equal(bits(c2.attend(q, b2)), bits(want))
+    if how != "copy":
+        c2.k_tail.zero_()
+        b2.ctx_lens.fill_(1)
+        assert not np.array_equal(bits(c2.attend(q, b2)), bits(want))
+    assert np.array_equal(bits(c.attend(q, b)), bits(want))

@@ -154,7 +154,16 @@ def _heads(t, heads, d, name, device):
     return row if shape[0] > 1 else shape[1] * d
 
 
-class PagedBatch:
+class _Kept:
+    """Copies and pickles go without the library's struct, whose addresses are not theirs."""
+
+    _known = None                    # what the last check found, and the struct for it
+
+    def __getstate__(self):
+        return {**self.__dict__, "_known": None}
+
+
+class PagedBatch(_Kept):
     """The sequences of one call (kv_paged_batch in kv_codec.h), int32 GPU
     tensors: rows cu_q[b] .. cu_q[b+1]-1 of the call belong to sequence b, which
     holds ctx_lens[b] tokens before them; its page p is pool page
@@ -193,16 +202,15 @@ class PagedBatch:
         return known[1]
 
 
-class PagedKVCache:
+class PagedKVCache(_Kept):
     """One layer's paged INT8 cache (kv_paged_* in kv_codec.h): pages of `page`
     tokens with one scale per (page, kv head) for K and one for V, and a ring of
     the two highest pages that each sequence has reached in fp16, from which the
     unfinished page is read.  Tokens can be taken back to the first one of those
-    pages, and beyond that only to a multiple of `page`.  Pages and rings are in the order of kv_codec.h; `read` gives pages in
-    the order of tokens.  Block tables, lengths and slots are the caller's
-    (PagedBatch), shared by a model's layers."""
-
-    _known = None                    # (addresses and sizes, the library's struct) of the last check
+    pages, and beyond that only to a multiple of `page`.  Pages and rings are in
+    the order of kv_codec.h; `read` gives pages in the order of tokens.  Block
+    tables, lengths and slots are the caller's (PagedBatch), shared by a model's
+    layers."""
 
     def __init__(self, pool_pages, n_kv, d, slots, device, page=128):
         if page not in (64, 128, 256) or d not in (64, 96, 128, 256):
