@@ -38,9 +38,19 @@ class QuantizedWeight:
         return (self.qweight.numel() * 4 + self.scales.numel() * 2 + self.zeros.numel() * 2)
 
 
+def _stream_of_object(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# Handle of torch's current HIP stream on the GPU with this index.  Without a Stream object
+# in between a call is 1.3 us shorter on the host (of 13, one token's GEMV); where torch does
+# not have that function, with one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of_object)
+
+
 def _stream(t):
     """Handle of torch's current HIP stream on t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return _raw_stream(t.device.index)
 
 
 def _need(t, dtype, shape, name):

@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from ._lib import W4A16Error, check, lib
-from .api import _need, _same_device, _stream
+from .api import _need, _raw_stream, _same_device, _stream
 
 
 def _dev_tensor(t, dtype, name):
@@ -308,8 +308,8 @@ class PagedKVCache(_Kept):
         """A library call on torch's current stream of the cache's GPU, made the current one."""
         at = self.k.device.index
         fn = getattr(lib(), name)
-        stream = torch._C._cuda_getCurrentRawStream(at)
-        if torch._C._cuda_getDevice() == at:
+        stream = _raw_stream(at)
+        if torch.cuda.current_device() == at:
             rc = fn(*args, stream)
         else:
             with torch.cuda.device(at):
