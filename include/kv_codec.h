@@ -185,17 +185,21 @@ int64_t kv_paged_attention_workspace_size(int64_t tokens, int32_t batch, int32_t
  * sequence stands at index ctx_lens[b] + i and sees the tokens j <= that
  * index, with window > 0 only those with index - j < window and the first
  * `sinks` tokens.  out fp16 [tokens][n_q][d], contiguous:
- * softmax_j(scale * q . k_j) v, with sums and statistics in binary32, rounded
- * once.  Pages whose block_table entry is outside [0, pages) are not visible
- * (pages that no row sees are not looked up at all); a row that sees nothing
- * gives zeros.  Rows of no sequence are left as they were.  An infinity or NaN in
- * the k or v of a token that is read from the ring gives NaN in the rows that see
- * the token (with a weight above zero) and reaches no other; one that was
- * quantized has spoiled its page for its kv head: NaN in the rows that see any of the
- * page's tokens, and in no other.  A page with scales of 0 (nobody filled it) counts as
- * zeros.  `workspace`: device memory of at least kv_paged_attention_workspace_size bytes, 16-byte aligned,
- * overwritten; calls sharing a workspace must not overlap.  Results are
- * deterministic for given inputs and sizes.
+ * softmax_j(scale * q . k_j) v, with scores, sums and statistics in binary32 and
+ * the output rounded once; in calls of many rows a sequence each weight of the
+ * second product is rounded to fp16 too (2^-11; in others to two fp16 parts, 2^-22).
+ * Pages whose block_table entry is outside [0, pages) are not visible (pages that
+ * no row sees are not looked up at all); a row that sees nothing gives zeros.  Rows
+ * of no sequence are left as they were.  An infinity or NaN in the k or v of a
+ * token that is read from the ring gives NaN in the rows that see the token (with a
+ * weight above zero) and reaches no other; one that was quantized has spoiled its
+ * page for its kv head: NaN in the rows that see any of the page's tokens, and in
+ * no other.  A page with scales of 0 (nobody filled it) counts as zeros.
+ * `workspace`: device memory of at least kv_paged_attention_workspace_size bytes,
+ * 16-byte aligned, overwritten; calls sharing a workspace must not overlap.
+ * Results are deterministic for given inputs and sizes; a row's last bits depend on
+ * the sizes of its call (tokens, batch, table_cols, window), which choose how it is
+ * run.
  */
 int kv_paged_attention(const kv_paged_cache *cache, const kv_paged_batch *batch, const uint16_t *q, int64_t q_stride,
                        int32_t n_q, float scale, int32_t window, int32_t sinks, void *workspace,

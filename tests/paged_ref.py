@@ -112,10 +112,33 @@ def attend(seq, q, scale, window=0, sinks=0, hidden=(), quant=None):
     return out, size, most
 
 
-def tolerance(o, size, most, tokens, d):
+def tolerance(o, size, most, tokens, d, weights=2.0**-11):
     """How far the kernel may be off, by its roundings: o to fp16 (2^-11), each
-    weight to fp16 (2^-11 of sum p|v|), scores in binary32 (d products and a few
+    weight to fp16 (2^-11 of sum p|v|; WEIGHTS_IN_TWO where it is two parts), scores in
+    binary32 (d products and a few
     steps, each 2^-24 of the largest score's terms, counted for numerator and
     denominator), sums over the tokens and the hardware exponential (2^-20)."""
-    rel = 2.0**-11 + 2 * (d + 8) * 2.0**-24 * most + 2 * (tokens + 64) * 2.0**-24 + 2.0**-20
+    rel = weights + 2 * (d + 8) * 2.0**-24 * most + 2 * (tokens + 64) * 2.0**-24 + 2.0**-20
     return 2.0**-11 * np.abs(o) + rel * size + 2.0**-25
+
+
+# A weight as two fp16 parts: what the second leaves is half a step of its own, 2^-11 of
+# at most 2^-11 of the weight, or 2^-25 where it is below fp16's normal numbers, of a
+# largest weight of 2^10 or more: 2^-35 for each of up to 2^13 tokens.
+WEIGHTS_IN_TWO = 2.0**-22 + 2.0**-22
+
+
+def balanced(n_kv, d, tokens):
+    """K, V [tokens, n_kv, d], a query [1, n_kv, d] and a scale, for which half of the
+    tokens nearly cancel the other half, so that an output shows how exact the weights
+    are: its own rounding is small beside them.  K holds whole numbers with a scale of 1
+    and the query does not see its largest channel, so scores are exact."""
+    k = np.zeros((tokens, n_kv, d))
+    k[::16, :, 0] = 127
+    k[1::2, :, 1] = 16
+    q = np.zeros((1, n_kv, d))
+    q[0, :, 1] = 1 + np.arange(n_kv)
+    scale = 1 / 64
+    ratio = np.exp(-q[0, :, 1] * 16 * scale)[:, None]            # weight of an even token over an odd one's
+    v = np.where(np.arange(tokens)[:, None, None] % 2 == 0, np.ones((n_kv, d)), -ratio)
+    return k.astype(np.float16), v.astype(np.float16), q.astype(np.float16), scale

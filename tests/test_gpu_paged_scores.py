@@ -64,3 +64,32 @@ def test_the_best_token_takes_all(d, page, n_kv, n_q, held, n, window, scale, ti
             assert bool((np.abs(y[at:at + m, h] - o[:, h]) <= tol[:, h])[sure].all()), h
         at += m
     assert clear >= sum(n) * n_q * 3 // 4
+
+
+@pytest.mark.parametrize("d,page,tokens,others,most", [
+    (64, 64, 330, 0, 512),                   # a row block a workgroup
+    (128, 128, 330, 0, 512),
+    (96, 64, 200, 0, 512),
+    (256, 64, 200, 0, 512),
+    (64, 64, 330, 0, 16384),                 # runs shared by workgroups
+    (128, 128, 330, 1, 16384),
+    (96, 128, 300, 2, 16384),
+    (256, 128, 300, 0, 16384),
+    (64, 64, 200, 300, 256),                 # a wave each
+])
+def test_few_rows_have_their_weights_in_full(d, page, tokens, others, most):
+    """With few rows a sequence a weight is two fp16 parts: far below one part's rounding."""
+    n_kv = 8
+    w = World(1 + others, n_kv, d, page, seed=d, most=most)
+    k, v, q, scale = ref.balanced(n_kv, d, tokens)
+    T = tokens + 3 * others
+    extra = w.values(T - tokens, n_kv), w.values(T - tokens, n_kv)
+    w.cache.append(to_dev(np.concatenate([k, extra[0]])), to_dev(np.concatenate([v, extra[1]])), w.batch([tokens] + [3] * others))
+    w.seqs[0].append(k, v)
+    x = np.concatenate([q, w.values(others, n_kv)])
+    y = w.cache.attend(to_dev(x), w.batch([1] * (1 + others), ctx=[tokens - 1] + [2] * others), scale=scale)
+    torch.cuda.synchronize()
+    o, size, top = ref.attend(w.seqs[0], q, scale)
+    tol = ref.tolerance(o, size, top, tokens, 0, ref.WEIGHTS_IN_TWO)
+    err = np.abs(y[:1].cpu().numpy().astype(np.float64) - o)
+    assert bool((err <= tol).all()), float((err / tol).max())
