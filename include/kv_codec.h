@@ -205,6 +205,17 @@ int kv_paged_attention(const kv_paged_cache *cache, const kv_paged_batch *batch,
                        int32_t n_q, float scale, int32_t window, int32_t sinks, void *workspace,
                        int64_t workspace_bytes, uint16_t *out, void *stream);
 
+/*
+ * Kernel selection report, for tests and profiling: writes to `name` the kernels
+ * that kv_paged_attention launches for these sizes, in the form in which profilers
+ * print their names ("kv_attend_split_kernel<128, 1, 2>, kv_join_kernel<128, 1, 1>"),
+ * NUL-terminated and truncated to name_len bytes.  Nothing is launched and no HIP
+ * call is made.  Returns the status that kv_paged_attention would return for these
+ * sizes (Q4_ERR_NULL without a name, Q4_ERR_SHAPE for name_len < 1).
+ */
+int kv_paged_attention_config(int64_t tokens, int32_t batch, int32_t table_cols, int32_t page, int32_t n_q, int32_t n_kv,
+                              int32_t d, int32_t window, int32_t sinks, char *name, int64_t name_len);
+
 #ifdef __cplusplus
 }
 #endif

@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define Q4_ABI_VERSION 5
+#define Q4_ABI_VERSION 6
 
 enum {
     Q4_OK = 0,

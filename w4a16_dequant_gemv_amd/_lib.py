@@ -9,7 +9,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("W4A16_LIB") or os.path.join(PKG, "libw4a16.so")
 
 Q4_OK, Q4_ERR_NULL, Q4_ERR_SHAPE, Q4_ERR_GROUP, Q4_ERR_ALIGN, Q4_ERR_HIP, Q4_ERR_CAPACITY = range(7)
-ABI_VERSION = 5
+ABI_VERSION = 6
 
 # Every symbol the public header declares, with its ctypes signature.
 _p = ctypes.c_void_p
@@ -54,6 +54,8 @@ SIGNATURES = {
     "kv_paged_read": (ctypes.c_int, [_cache, _p, _i64, _p, _p, _p]),
     "kv_paged_attention_workspace_size": (_i64, [_i64, _i32, _i32, _i32, _i32]),
     "kv_paged_attention": (ctypes.c_int, [_cache, _batch, _p, _i64, _i32, ctypes.c_float, _i32, _i32, _p, _i64, _p, _p]),
+    "kv_paged_attention_config": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_char_p,
+                                                 _i64]),
     "sq_absmax_update_f16": (ctypes.c_int, [_p, _i64, _i32, _p, _p]),
     "sq_absmax_update_f32": (ctypes.c_int, [_p, _i64, _i32, _p, _p]),
     "sq_smooth_factors": (ctypes.c_int, [_p, _p, _i32, ctypes.c_float, _p, _p]),

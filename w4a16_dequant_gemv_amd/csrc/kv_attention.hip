@@ -19,6 +19,8 @@
 // 16 g .. 16 g + 15 at a time: its own registers, since K rows are stored in the
 // order that puts them there (kv_k_index).  P never leaves the lane, and K and
 // V pages are read straight into operand registers in contiguous 16-byte loads.
+#include <stdio.h>
+
 #include <algorithm>
 
 #include "kv_device.h"
@@ -1188,27 +1190,54 @@ Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most,
     return p;
 }
 
-template <int D, int QT>
-hipError_t launch_split(const Args &a, const Plan &p, hipStream_t stream)
-{
-    const unsigned groups = (unsigned)(a.workers * a.cache.n_kv);
-    if (p.alone == 1) {
-        kv_attend_wave_kernel<D, QT, split_occupancy(D, QT)><<<groups, 64, 0, stream>>>(a);
-        return hipGetLastError();
+// Where a call goes: to a stream, or with `name` nowhere, and the kernels that would have
+// been launched are written there.
+struct Target {
+    hipStream_t stream;
+    char *name;
+    int64_t name_len;
+    template <typename... V>
+    hipError_t report(const char *format, V... values) const
+    {
+        snprintf(name, (size_t)name_len, format, values...);
+        return hipSuccess;
     }
-    kv_attend_split_kernel<D, QT, split_occupancy(D, QT)><<<groups, kThreads, 0, stream>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.whole) return e;
+};
+
+template <int D, int QT>
+hipError_t launch_split(const Args &a, const Plan &p, const Target &to)
+{
+    const hipStream_t stream = to.stream;
+    const unsigned groups = (unsigned)(a.workers * a.cache.n_kv);
+    constexpr int OCC = split_occupancy(D, QT);
     // with 16 parts a sequence or more, four waves join a row (1 x 131k tokens, 64 heads on
     // 8: 53 us, 59 with one wave; 32 x 4k: 55, 53 with one)
-    if (a.workers >= 16 * a.batch.batch) kv_join_kernel<D, QT, 4><<<groups * 16 * QT, 256, 0, stream>>>(a);
+    const int join = a.workers >= 16 * a.batch.batch ? 4 : 1;
+    if (to.name) {
+        if (p.alone == 1) return to.report("kv_attend_wave_kernel<%d, %d, %d>", D, QT, OCC);
+        if (a.whole) return to.report("kv_attend_split_kernel<%d, %d, %d>, whole row blocks", D, QT, OCC);
+        return to.report("kv_attend_split_kernel<%d, %d, %d>, kv_join_kernel<%d, %d, %d>", D, QT, OCC, D, QT, join);
+    }
+    if (p.alone == 1) {
+        kv_attend_wave_kernel<D, QT, OCC><<<groups, 64, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    kv_attend_split_kernel<D, QT, OCC><<<groups, kThreads, 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.whole) return e;
+    if (join == 4) kv_join_kernel<D, QT, 4><<<groups * 16 * QT, 256, 0, stream>>>(a);
     else kv_join_kernel<D, QT, 1><<<groups * 16 * QT, 64, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <int D, int NW, int QT>
-hipError_t launch_rows(const Args &a, const Plan &p, hipStream_t stream)
+hipError_t launch_rows(const Args &a, const Plan &p, const Target &to)
 {
+    const hipStream_t stream = to.stream;
+    if (to.name) {
+        if (p.splits == 1) return to.report("kv_attend_rows_kernel<%d, %d, %d>", D, NW, QT);
+        return to.report("kv_attend_rows_kernel<%d, %d, %d>, kv_join_rows_kernel<%d>, %d cuts", D, NW, QT, D, p.splits);
+    }
     constexpr int LDS = 2 * (8 * ((D + 63) / 64) + D / 8) * 1024;
     if (LDS > 65536) {
         hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kv_attend_rows_kernel<D, NW, QT>),
@@ -1224,15 +1253,15 @@ hipError_t launch_rows(const Args &a, const Plan &p, hipStream_t stream)
 }
 
 template <int D>
-hipError_t launch(const Args &a, const Plan &p, hipStream_t stream)
+hipError_t launch(const Args &a, const Plan &p, const Target &to)
 {
-    if (p.qt == 1) return launch_split<D, 1>(a, p, stream);
+    if (p.qt == 1) return launch_split<D, 1>(a, p, to);
     if constexpr (D == 256) {
-        return launch_rows<D, 8, 1>(a, p, stream);
+        return launch_rows<D, 8, 1>(a, p, to);
     } else {
-        if (p.qt == 2) return launch_split<D, 2>(a, p, stream);
-        if (p.qt == 3) return launch_split<D, 3>(a, p, stream);
-        return p.waves == 8 ? launch_rows<D, 8, 2>(a, p, stream) : launch_rows<D, 4, 2>(a, p, stream);
+        if (p.qt == 2) return launch_split<D, 2>(a, p, to);
+        if (p.qt == 3) return launch_split<D, 3>(a, p, to);
+        return p.waves == 8 ? launch_rows<D, 8, 2>(a, p, to) : launch_rows<D, 4, 2>(a, p, to);
     }
 }
 
@@ -1246,7 +1275,7 @@ int64_t kv_attention_workspace(int64_t tokens, int batch, int n_q, int n_kv, int
 
 hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch &batch, const uint16_t *q,
                                int64_t q_stride, int n_q, float scale, int window, int sinks, void *workspace,
-                               uint16_t *out, hipStream_t stream)
+                               uint16_t *out, hipStream_t stream, char *name, int64_t name_len)
 {
     const int64_t most = (int64_t)batch.table_cols * cache.page;
     const Plan p = plan_for(batch.tokens, batch.batch, n_q, cache.n_kv, cache.d, most,
@@ -1256,11 +1285,12 @@ hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch
     const Args a = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, window, sinks,
                     __builtin_ctz(cache.page), p.workers, p.alone == kWaves, p.workers ? 1.0 / p.workers : 0.0, part, stats,
                     reinterpret_cast<int32_t *>(stats + p.parts * 2), out};
+    const Target to = {stream, name, name_len};
     switch (cache.d) {
-    case 64: return launch<64>(a, p, stream);
-    case 96: return launch<96>(a, p, stream);
-    case 128: return launch<128>(a, p, stream);
-    case 256: return launch<256>(a, p, stream);
+    case 64: return launch<64>(a, p, to);
+    case 96: return launch<96>(a, p, to);
+    case 128: return launch<128>(a, p, to);
+    case 256: return launch<256>(a, p, to);
     default: return hipErrorInvalidValue;
     }
 }

@@ -398,6 +398,27 @@ int kv_paged_attention(const kv_paged_cache *cache, const kv_paged_batch *batch,
                                       (hipStream_t)stream));
 }
 
+int kv_paged_attention_config(int64_t tokens, int32_t batch, int32_t table_cols, int32_t page, int32_t n_q, int32_t n_kv,
+                              int32_t d, int32_t window, int32_t sinks, char *name, int64_t name_len)
+{
+    // only the sizes are read: the pointers stand for the arrays
+    static const uint32_t any[4] __attribute__((aligned(16))) = {};
+    int8_t *b = (int8_t *)any;
+    float *f = (float *)any;
+    uint16_t *h = (uint16_t *)any;
+    const int32_t *i = (const int32_t *)any;
+    const kv_paged_cache cache = {b, b, f, f, h, h, 1, 1, n_kv, d, page};
+    const kv_paged_batch call = {i, i, i, i, tokens, batch, table_cols};
+    if (!name) return Q4_ERR_NULL;
+    if (name_len < 1) return Q4_ERR_SHAPE;
+    if (int rc = check_paged_cache(&cache)) return rc;
+    if (int rc = check_paged_batch(&call, &cache)) return rc;
+    if (check_heads(n_q, n_kv) || tokens * n_q * d > kMaxElems) return Q4_ERR_SHAPE;
+    if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return Q4_ERR_SHAPE;
+    return finish(kv_launch_attention(cache, call, h, (int64_t)n_q * d, n_q, 1.0f, window, sinks, f, h, nullptr, name,
+                                      name_len));
+}
+
 int sq_absmax_update_f16(const uint16_t *x, int64_t rows, int32_t cols, float *amax, void *stream)
 {
     if (!x || !amax) return Q4_ERR_NULL;

@@ -51,9 +51,10 @@ hipError_t kv_launch_append(const kv_paged_cache &cache, const kv_paged_batch &b
 hipError_t kv_launch_read(const kv_paged_cache &cache, const int32_t *ids, int64_t n, uint16_t *k_out, uint16_t *v_out,
                           hipStream_t stream);
 int64_t kv_attention_workspace(int64_t tokens, int batch, int n_q, int n_kv, int d);
+// With `name` nothing is launched: the kernels that would be are written there.
 hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch &batch, const uint16_t *q,
                                int64_t q_stride, int n_q, float scale, int window, int sinks, void *workspace,
-                               uint16_t *out, hipStream_t stream);
+                               uint16_t *out, hipStream_t stream, char *name = nullptr, int64_t name_len = 0);
 
 // W8A8 with SmoothQuant (w8a8.hip); cols % 8 == 0, k % 32 == 0, k <= 32768.
 hipError_t w8a8_launch_col_absmax(const void *src, bool f32, int64_t rows, int cols, float *out,

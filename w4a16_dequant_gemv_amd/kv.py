@@ -6,7 +6,7 @@ cache (PagedKVCache): appending new tokens with rotation, and attention over it.
 Only argument marshalling happens here: tensors must already live on the GPU
 and the library does all of the arithmetic on torch's current stream.
 """
-from ctypes import byref
+from ctypes import byref, create_string_buffer
 
 import torch
 
@@ -152,6 +152,16 @@ def _heads(t, heads, d, name, device):
     if one != 1 or (head != d and shape[1] > 1):
         raise W4A16Error(f"{name}: a token's heads must lie side by side")
     return row if shape[0] > 1 else shape[1] * d
+
+
+def attention_config(tokens, batch, table_cols, n_q, n_kv, d, page=128, window=0, sinks=0):
+    """Names of the kernels that PagedKVCache.attend launches for `tokens` queries of
+    `batch` sequences with block tables of `table_cols` pages, as profilers print them.
+    Nothing is launched; works without a GPU."""
+    name = create_string_buffer(160)
+    check(lib().kv_paged_attention_config(tokens, batch, table_cols, page, n_q, n_kv, d, window, sinks, name, len(name)),
+          "kv_paged_attention_config")
+    return name.value.decode()
 
 
 class _Kept:
