@@ -854,7 +854,9 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_attend_rows_kernel(Args a, int 
     // an accumulator comes up again after one or three others.  `between` is run twice, after two
     // pieces of the scores.
     auto matrix_work = [&](int i, bool second, bool first, auto between) {
-        constexpr int VP = DT / 2, NP = VP + 2 * KS, AHEAD = 2;
+        // two pieces ahead; one for d = 96 in four waves, whose registers two pieces overflow
+        // (8 x 300 queries on 2000 tokens 136 us, 140 with two; 512 on 2000 72 and 73)
+        constexpr int VP = DT / 2, NP = VP + 2 * KS, AHEAD = D % 64 != 0 && NW == 4 ? 1 : 2;
         f16x8 f[AHEAD + 1][4];
         auto fetch = [&](int n) {
             if (n < VP) { if (second) read_v(i - 1, n, f[n % (AHEAD + 1)]); }
