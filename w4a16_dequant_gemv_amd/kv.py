@@ -7,6 +7,7 @@ Only argument marshalling happens here: tensors must already live on the GPU
 and the library does all of the arithmetic on torch's current stream.
 """
 from ctypes import byref, create_string_buffer
+from functools import lru_cache
 
 import torch
 
@@ -154,6 +155,12 @@ def _heads(t, heads, d, name, device):
     return row if shape[0] > 1 else shape[1] * d
 
 
+@lru_cache(maxsize=4096)
+def _workspace_size(tokens, batch, n_q, n_kv, d):
+    """By these sizes alone, so asked once for each (0.7 us of a call on the host)."""
+    return lib().kv_paged_attention_workspace_size(tokens, batch, n_q, n_kv, d)
+
+
 def attention_config(tokens, batch, table_cols, n_q, n_kv, d, page=128, window=0, sinks=0):
     """Names of the kernels that PagedKVCache.attend launches for `tokens` queries of
     `batch` sequences with block tables of `table_cols` pages, as profilers print them.
@@ -200,6 +207,7 @@ class PagedBatch(_Kept):
     slots = property(lambda self: self._tensors[3])
 
     def _struct(self, tokens, device):
+        """The library's struct for a call of so many tokens, and the number of sequences."""
         if self._device != device:
             raise W4A16Error("all tensors must be on the same GPU")
         q, c, t, s = self._tensors
@@ -208,7 +216,8 @@ class PagedBatch(_Kept):
         at = (q.data_ptr(), c.data_ptr(), t.data_ptr(), s.data_ptr(), tokens)
         known = self._known
         if known is None or known[0] != at:
-            known = self._known = at, _lib.PagedBatch(*at, c.shape[0], t.shape[1])
+            B = c.shape[0]
+            known = self._known = at, (byref(_lib.PagedBatch(*at, B, t.shape[1])), B)
         return known[1]
 
 
@@ -254,7 +263,8 @@ class PagedKVCache(_Kept):
         return self.k_tail.shape[0]
 
     def _checked(self):
-        """The six tensors as the library's struct, checked when one was replaced."""
+        """The six tensors as the library's struct, checked when one was replaced, the
+        GPU they are on and its index."""
         k, v, ks, vs, kt, vt = self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail
         at = (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kt.data_ptr(), vt.data_ptr(),
               k.numel(), v.numel(), ks.numel(), vs.numel(), kt.numel(), vt.numel())
@@ -270,7 +280,8 @@ class PagedKVCache(_Kept):
         _need(self.k_tail, torch.float16, (S, 2, *kshape), "k_tail")
         _need(self.v_tail, torch.float16, (S, 2, *vshape), "v_tail")
         _same_device(self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail)
-        known = self._known = at, _lib.PagedCache(*at[:6], P, S, self.n_kv, self.d, self.page)
+        dev = k.device
+        known = self._known = at, (byref(_lib.PagedCache(*at[:6], P, S, self.n_kv, self.d, self.page)), dev, dev.index)
         return known[1]
 
     def append(self, k, v, batch, q=None, rope=None, positions=None, interleaved=False, q_out=None):
@@ -279,7 +290,7 @@ class PagedKVCache(_Kept):
         is rotated first, and q [T, n_q, d] into the result [T, n_q, d] (None
         without q).  ctx_lens is not changed: advance it once every layer has
         appended and attended."""
-        c, dev = self._checked(), self.k.device
+        c, dev, gpu = self._checked()
         ks, vs = _heads(k, self.n_kv, self.d, "k", dev), _heads(v, self.n_kv, self.d, "v", dev)
         T = k.shape[0]
         if v.shape[0] != T:
@@ -288,7 +299,7 @@ class PagedKVCache(_Kept):
             if q is not None or positions is not None:
                 raise W4A16Error("q and positions are only used with rope")
             if T:
-                self._call("kv_paged_append", byref(c), byref(batch._struct(T, dev)), k.data_ptr(), ks, v.data_ptr(), vs,
+                self._call("kv_paged_append", gpu, c, batch._struct(T, dev)[0], k.data_ptr(), ks, v.data_ptr(), vs,
                            None, 0, 0, None, 0, 0, 0, None, None)
             return None
         if not isinstance(rope, torch.Tensor) or rope.dim() != 3:
@@ -309,20 +320,20 @@ class PagedKVCache(_Kept):
                 _fits(q_out, torch.float16, (T, n_q, self.d), dev, "q_out")
             q_at, out_at = q.data_ptr(), q_out.data_ptr()
         if T:
-            self._call("kv_paged_append", byref(c), byref(batch._struct(T, dev)), k.data_ptr(), ks, v.data_ptr(), vs,
+            self._call("kv_paged_append", gpu, c, batch._struct(T, dev)[0], k.data_ptr(), ks, v.data_ptr(), vs,
                        q_at, qs or 0, n_q or 0, rope.data_ptr(), rows, pairs * 2, 1 if interleaved else 0,
                        positions.data_ptr(), out_at)
         return None if q is None else q_out
 
-    def _call(self, name, *args):
-        """A library call on torch's current stream of the cache's GPU, made the current one."""
-        at = self.k.device.index
+    @staticmethod
+    def _call(name, gpu, *args):
+        """A library call on torch's current stream of that GPU, made the current one."""
         fn = getattr(lib(), name)
-        stream = _raw_stream(at)
-        if torch.cuda.current_device() == at:
+        stream = _raw_stream(gpu)
+        if torch.cuda.current_device() == gpu:
             rc = fn(*args, stream)
         else:
-            with torch.cuda.device(at):
+            with torch.cuda.device(gpu):
                 rc = fn(*args, stream)
         if rc:
             check(rc, name)
@@ -330,7 +341,7 @@ class PagedKVCache(_Kept):
     def read(self, ids, k_out=None, v_out=None):
         """Pool pages ids (int32 [n]) as fp16 (K, V), each [n, n_kv, page, d] in the
         order of tokens; ids outside the pool are skipped."""
-        c, dev = self._checked(), self.k.device
+        c, dev, gpu = self._checked()
         if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
             raise W4A16Error("ids must be int32 [n] on the GPU")
         n = ids.shape[0]
@@ -345,7 +356,7 @@ class PagedKVCache(_Kept):
         else:
             _fits(v_out, torch.float16, shape, dev, "v_out")
         if n:
-            self._call("kv_paged_read", byref(c), ids.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr())
+            self._call("kv_paged_read", gpu, c, ids.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr())
         return k_out, v_out
 
     def attend(self, q, batch, scale=None, window=0, sinks=0, out=None, workspace=None):
@@ -354,7 +365,7 @@ class PagedKVCache(_Kept):
         a sequence sees the tokens up to its own, with window > 0 the last
         `window` of them and the sequence's first `sinks`.  scale defaults to
         d^-1/2.  Rows of no sequence are left as they were."""
-        c, dev = self._checked(), self.k.device
+        c, dev, gpu = self._checked()
         qs = _heads(q, None, self.d, "q", dev)
         T, n_q = q.shape[:2]
         if n_q == 0 or n_q % self.n_kv or n_q > 1024:
@@ -370,12 +381,12 @@ class PagedKVCache(_Kept):
             _fits(out, torch.float16, (T, n_q, self.d), dev, "out")
         if T == 0:
             return out
-        b = batch._struct(T, dev)
-        need = lib().kv_paged_attention_workspace_size(T, b.batch, n_q, self.n_kv, self.d)
+        b, B = batch._struct(T, dev)
+        need = _workspace_size(T, B, n_q, self.n_kv, self.d)
         if workspace is None:
             workspace = self.k.new_empty(need)
         elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
             raise W4A16Error("workspace must be a contiguous tensor on the cache's GPU")
-        self._call("kv_paged_attention", byref(c), byref(b), q.data_ptr(), qs, n_q, scale, window, sinks,
+        self._call("kv_paged_attention", gpu, c, b, q.data_ptr(), qs, n_q, scale, window, sinks,
                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr())
         return out
