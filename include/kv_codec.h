@@ -134,7 +134,9 @@ typedef struct kv_paged_cache {
  * (or queries) belong to sequence b, which holds ctx_lens[b] tokens before
  * them; its page p is pool page block_table[b][p] and its ring is slots[b].
  * Rows before cu_q[0] and from cu_q[batch] on (padding) belong to none.  All
- * four arrays are int32 device arrays, read when the kernels run.  A sequence
+ * four arrays are int32 device arrays, read when the kernels run; how attention is
+ * run goes by the sizes below, table_cols standing for the length of the sequences
+ * (a narrower table for short ones is faster).  A sequence
  * with ctx_lens[b] < 0, slots[b] outside [0, cache.slots) or more than
  * table_cols full pages is skipped as if it had no rows.  cu_q must not
  * decrease (a decreasing one gives unspecified, memory-safe results); two
