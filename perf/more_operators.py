@@ -5,7 +5,8 @@ share a long prefix, as cases that can be timed.
 MXFP4: 32 consecutive values of a row share a scale 2^(s - 127), s a byte (255 is NaN);
 a value is a code of 4 bits, sign, two exponent bits and one of mantissa, which stands
 for 0, 0.5, 1, 1.5, 2, 3, 4 or 6 times the scale.  s = floor(log2(largest |x|)) - 2 + 127.
-Codes lie two in a byte, the even one in its low half.
+Codes lie two in a byte, the even one in its low half; block b's scale of a row is at
+[b // 8][row][b % 8], zeros behind the last.
 
 Paged cache: a page holds `page` tokens of one sequence, for every kv head, as int8 codes
 with one fp32 scale per (page, head) for K and one for V.  The last two pages of a
@@ -156,7 +157,7 @@ def _packed(w):
 
 
 def _values(codes, scales):
-    """[rows, k/2] codes and [rows, k/32] scales as fp32 [rows, k]."""
+    """Codes [rows, k/2] and scales [rows, k/32] as fp32 [rows, k]."""
     table = torch.tensor(STEPS + tuple(-x for x in STEPS), device=codes.device)
     c = torch.stack((codes & 15, codes >> 4), -1).view(*scales.shape, 32)
     return torch.ldexp(table[c.int()], scales[..., None].int() - 127).view(codes.shape[0], -1)
@@ -177,7 +178,11 @@ def prepare(case, seed):
         x = torch.randn((m, k), generator=g, device=dev)
         x *= torch.where(torch.rand(k, generator=g, device=dev) < 0.01, 20.0, 1.0)
         codes, scales = _packed(torch.randn((n, k), generator=g, device=dev) * 0.02)
-        return dict(case=dict(case), x=x.to(getattr(torch, case["type"])), codes=codes, scales=scales)
+        st = dict(case=dict(case), x=x.to(getattr(torch, case["type"])), codes=codes, scales=scales)
+        if own:
+            from w4a16_dequant_gemv_amd import mxfp4
+            st["weight"] = mxfp4.MXTensor.from_blocks(codes, scales)
+        return st
 
     cuts, pages, ctx, new = _lens(case)
     B, n_q, n_kv, d, t = case["batch"], case["n_q"], case["n_kv"], case["d"], case["page"]
@@ -303,11 +308,12 @@ def run(st):
             q = mxfp4.quantize(x)
             return dict(values=mxfp4.dequantize(q, dtype=x.dtype), scales=q.scales)
         v, s = _rounded(x)
+        s = torch.nn.functional.pad(s, (0, -s.shape[1] % 8)).view(s.shape[0], -1, 8).transpose(0, 1).contiguous()
         return dict(values=v.to(x.dtype), scales=s)
     if op == "linear":
         if own:
             from w4a16_dequant_gemv_amd import mxfp4
-            return mxfp4.linear(st["x"], mxfp4.MXTensor(st["codes"], st["scales"]))
+            return mxfp4.linear(st["x"], st["weight"])
         x, _ = _rounded(st["x"])
         return torch.matmul(x, _values(st["codes"], st["scales"]).t()).to(st["x"].dtype)
     if own:
