@@ -52,7 +52,7 @@
 extern "C" {
 #endif
 
-#define Q4_ABI_VERSION 6
+#define Q4_ABI_VERSION 7
 
 enum {
     Q4_OK = 0,

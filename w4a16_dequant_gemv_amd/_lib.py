@@ -9,7 +9,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("W4A16_LIB") or os.path.join(PKG, "libw4a16.so")
 
 Q4_OK, Q4_ERR_NULL, Q4_ERR_SHAPE, Q4_ERR_GROUP, Q4_ERR_ALIGN, Q4_ERR_HIP, Q4_ERR_CAPACITY = range(7)
-ABI_VERSION = 6
+ABI_VERSION = 7
 
 # Every symbol the public header declares, with its ctypes signature.
 _p = ctypes.c_void_p
@@ -73,6 +73,15 @@ SIGNATURES = {
                                     _p, _p, _p]),
 }
 
+# Those of mxfp4.h.
+MX4_SIGNATURES = {
+    "mx4_quantize": (ctypes.c_int, [_p, _i32, _i64, _i64, _i64, _p, _p, _p]),
+    "mx4_dequantize": (ctypes.c_int, [_p, _p, _i64, _i64, _i32, _p, _p]),
+    "mx4_matmul": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p]),
+    "mx4_linear_workspace_size": (_i64, [_i64, _i64]),
+    "mx4_linear": (ctypes.c_int, [_p, _i32, _i64, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _p]),
+}
+
 
 class W4A16Error(RuntimeError):
     """A non-zero status from the library, or the library is unavailable."""
@@ -91,7 +100,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise W4A16Error(f"{LIB_PATH} is not built; run `python -m w4a16_dequant_gemv_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in (*SIGNATURES.items(), *MX4_SIGNATURES.items()):
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args

@@ -3,6 +3,7 @@
 #include "w4a16.h"
 #include "kv_codec.h"
 #include "w8a8.h"
+#include "mxfp4.h"
 #include "producers.h"
 
 #include "q4_launch.h"
@@ -473,6 +474,77 @@ int w8a8_gemm(const int8_t *qx, const float *sx, const int8_t *qw, const float *
     if (!aligned(qx, 16) || !aligned(qw, 16) || !aligned(sx, 4) || !aligned(sw, 4) || !aligned(y, 2))
         return Q4_ERR_ALIGN;
     return finish(w8a8_launch_gemm(qx, sx, qw, sw, m, n_out, k, y, (hipStream_t)stream));
+}
+
+namespace {
+
+int check_mx4_shape(int64_t rows, int64_t k)
+{
+    if (check_rows(rows) || k < 32 || k > kMaxIn || k % 32 != 0 || rows * k > kMaxElems) return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+
+// Rows of x, `stride` elements apart.
+int check_mx4_rows(const void *x, int32_t type, int64_t rows, int64_t k, int64_t stride)
+{
+    const int64_t unit = type == MX4_F32 ? 4 : 8;
+    if (stride < k || stride % unit != 0 || stride > kMaxElems || rows * stride > 4 * kMaxElems) return Q4_ERR_SHAPE;
+    return aligned(x, 16) ? Q4_OK : Q4_ERR_ALIGN;
+}
+
+// Bytes of codes and of scales, each a multiple of 16.
+int64_t mx4_code_bytes(int64_t rows, int64_t k) { return rows * (k / 2); }
+int64_t mx4_scale_bytes(int64_t rows, int64_t k) { return ((k + 255) / 256 * rows * 8 + 15) / 16 * 16; }
+
+}  // namespace
+
+int mx4_quantize(const void *x, int32_t type, int64_t rows, int64_t k, int64_t stride, uint8_t *codes,
+                 uint8_t *scales, void *stream)
+{
+    if (!x || !codes || !scales) return Q4_ERR_NULL;
+    if (check_mx4_shape(rows, k) || type < MX4_F16 || type > MX4_F32) return Q4_ERR_SHAPE;
+    if (int rc = check_mx4_rows(x, type, rows, k, stride)) return rc;
+    if (!aligned(codes, 16) || !aligned(scales, 8)) return Q4_ERR_ALIGN;
+    return finish(mx4_launch_quantize(x, type, rows, k, stride, codes, scales, (hipStream_t)stream));
+}
+
+int mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, int32_t type, void *out,
+                   void *stream)
+{
+    if (!codes || !scales || !out) return Q4_ERR_NULL;
+    if (check_mx4_shape(rows, k) || type < MX4_F16 || type > MX4_F32) return Q4_ERR_SHAPE;
+    if (!aligned(codes, 16) || !aligned(scales, 8) || !aligned(out, 16)) return Q4_ERR_ALIGN;
+    return finish(mx4_launch_dequantize(codes, scales, rows, k, type, out, (hipStream_t)stream));
+}
+
+int mx4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes, const uint8_t *w_scales,
+               int64_t m, int64_t n_out, int64_t k, int32_t type, void *y, void *stream)
+{
+    if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return Q4_ERR_NULL;
+    if (check_mx4_shape(m, k) || check_mx4_shape(n_out, k) || m * n_out > kMaxElems || type < MX4_F16 || type > MX4_BF16)
+        return Q4_ERR_SHAPE;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 8) || !aligned(w_codes, 16) || !aligned(w_scales, 8) || !aligned(y, 2))
+        return Q4_ERR_ALIGN;
+    return finish(mx4_launch_matmul(x_codes, x_scales, w_codes, w_scales, m, n_out, k, type, y, (hipStream_t)stream));
+}
+
+int64_t mx4_linear_workspace_size(int64_t m, int64_t k)
+{
+    return check_mx4_shape(m, k) ? 0 : mx4_code_bytes(m, k) + mx4_scale_bytes(m, k);
+}
+
+int mx4_linear(const void *x, int32_t type, int64_t stride, const uint8_t *w_codes, const uint8_t *w_scales, int64_t m,
+               int64_t n_out, int64_t k, void *workspace, int64_t workspace_bytes, void *y, void *stream)
+{
+    if (!x || !w_codes || !w_scales || !workspace || !y) return Q4_ERR_NULL;
+    if (check_mx4_shape(m, k) || check_mx4_shape(n_out, k) || m * n_out > kMaxElems || type < MX4_F16 || type > MX4_BF16)
+        return Q4_ERR_SHAPE;
+    if (int rc = check_mx4_rows(x, type, m, k, stride)) return rc;
+    if (!aligned(w_codes, 16) || !aligned(w_scales, 8) || !aligned(workspace, 16) || !aligned(y, 2)) return Q4_ERR_ALIGN;
+    if (workspace_bytes < mx4_linear_workspace_size(m, k)) return Q4_ERR_SHAPE;
+    uint8_t *codes = (uint8_t *)workspace, *scales = codes + mx4_code_bytes(m, k);
+    if (hipError_t e = mx4_launch_quantize(x, type, m, k, stride, codes, scales, (hipStream_t)stream)) return finish(e);
+    return finish(mx4_launch_matmul(codes, scales, w_codes, w_scales, m, n_out, k, type, y, (hipStream_t)stream));
 }
 
 int64_t gptq_factor_workspace_size(int64_t n) { return n > 0 ? gptq_factor_workspace(n) : 0; }

@@ -68,6 +68,14 @@ hipError_t w8a8_launch_quant_act(const uint16_t *x, const float *s, int64_t m, i
 hipError_t w8a8_launch_gemm(const int8_t *qx, const float *sx, const int8_t *qw, const float *sw, int64_t m,
                             int64_t n_out, int64_t k, uint16_t *y, hipStream_t stream);
 
+// MXFP4 (mx4_quantize.hip, mx4_matmul.hip); k % 32 == 0, types as in mxfp4.h.
+hipError_t mx4_launch_quantize(const void *x, int type, int64_t rows, int64_t k, int64_t stride, uint8_t *codes,
+                               uint8_t *scales, hipStream_t stream);
+hipError_t mx4_launch_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, int type,
+                                 void *out, hipStream_t stream);
+hipError_t mx4_launch_matmul(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int64_t m,
+                             int64_t n_out, int64_t k, int type, void *y, hipStream_t stream);
+
 // GPTQ and AWQ (producers.hip).  Workspace sizes in bytes.
 int64_t gptq_factor_workspace(int64_t n);
 int64_t gptq_loop_workspace(int64_t n_out, int64_t n);
