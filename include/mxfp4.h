@@ -73,6 +73,13 @@ int64_t mx4_linear_workspace_size(int64_t m, int64_t k);
 int mx4_linear(const void *x, int32_t type, int64_t stride, const uint8_t *w_codes, const uint8_t *w_scales, int64_t m,
                int64_t n_out, int64_t k, void *workspace, int64_t workspace_bytes, void *y, void *stream);
 
+/*
+ * Kernel selection report, for tests and profiling: writes to `name` the kernels that mx4_linear or, with
+ * `linear` 0, mx4_matmul launches for these sizes, in the form in which profilers print their names,
+ * NUL-terminated and truncated to name_len bytes.  Nothing is launched and no HIP call is made.
+ */
+int mx4_linear_config(int64_t m, int64_t n_out, int64_t k, int32_t type, int32_t linear, char *name, int64_t name_len);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,9 +18,10 @@ constexpr int kSgValu = 0x002, kSgMfma = 0x008, kSgVmemRead = 0x020, kSgDsRead =
 
 // Tile of workgroup `bid`.  Workgroup ids are dealt round-robin to the eight
 // XCDs, so ids are remapped to give each XCD a contiguous range of tiles
-// (XCDs 0..extra-1 own one more); tiles are numbered in bands of kGroupM row
+// (XCDs 0..extra-1 own one more); tiles are numbered in bands of GROUP_M row
 // tiles, walked column by column inside a band, so an XCD's range covers few
 // row tiles of x and its L2 shares them.
+template <int GROUP_M = kGroupM>
 __device__ __forceinline__ void xcd_tile(int bid, int tiles_m, int tiles_n, int &tile_m, int &tile_n)
 {
     const int tiles = tiles_m * tiles_n;
@@ -28,11 +29,11 @@ __device__ __forceinline__ void xcd_tile(int bid, int tiles_m, int tiles_n, int 
     const int per_xcd = tiles / kXcds, extra = tiles % kXcds;
     const int t = xcd < extra ? xcd * (per_xcd + 1) + local
                               : extra * (per_xcd + 1) + (xcd - extra) * per_xcd + local;
-    const int band = t / (kGroupM * tiles_n);
-    const int band_m = min(kGroupM, tiles_m - band * kGroupM);
-    const int in_band = t - band * kGroupM * tiles_n;
+    const int band = t / (GROUP_M * tiles_n);
+    const int band_m = min(GROUP_M, tiles_m - band * GROUP_M);
+    const int in_band = t - band * GROUP_M * tiles_n;
     tile_n = in_band / band_m;
-    tile_m = band * kGroupM + in_band % band_m;
+    tile_m = band * GROUP_M + in_band % band_m;
 }
 
 // Chunk permutation of LDS row r, a function of r & 15.  Its low two bits

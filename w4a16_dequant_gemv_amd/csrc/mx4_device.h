@@ -85,3 +85,13 @@ __device__ __forceinline__ f32x4 mx4_mfma16(u32x4 a, u32x4 b, f32x4 c, uint32_t 
     const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, OA, (int)sa, OB, (int)sb);
 }
+
+// 32 rows x 32 columns += 64 products each: lane l has a block of row l % 32 and of column
+// l % 32, and gets rows 8 (i / 4) + 4 (l / 32) + i % 4 of column l % 32.
+template <int OA, int OB>
+__device__ __forceinline__ f32x16 mx4_mfma32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa, uint32_t sb)
+{
+    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, OA, (int)sa, OB, (int)sb);
+}

@@ -15,10 +15,10 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(const typename M
                                                                 uint32_t per_row, int64_t rows, int64_t stride,
                                                                 uint32_t *__restrict__ codes, uint8_t *__restrict__ scales)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;          // eight elements
-    const int64_t row = i / per_row;
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;                  // eight elements: at most 2^31 of them
+    const uint32_t at = i / per_row, c = i - at * per_row;
+    const int64_t row = at;
     if (row >= rows) return;
-    const uint32_t c = (uint32_t)(i - row * per_row);
     float v[8];
     mx4_load8<TYPE>(x + row * stride + c * 8, v);
     uint32_t top = mx4_top8(v);
@@ -40,10 +40,11 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint32_t
                                                                   const uint8_t *__restrict__ scales, uint32_t per_row,
                                                                   int64_t rows, typename Mx4Type<TYPE>::T *__restrict__ out)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t row = i / per_row;
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t at = i / per_row, c = i - at * per_row;
+    const int64_t row = at;
     if (row >= rows) return;
-    const uint32_t c = (uint32_t)(i - row * per_row), w = codes[i];
+    const uint32_t w = codes[i];
     const int s = scales[((int64_t)(c / 32) * rows + row) * 8 + c / 4 % 8];
     float v[8];
     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -53,7 +54,7 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint32_t
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = s == 255 ? __builtin_nanf("") : ldexpf(v[j], s - 127);
     if constexpr (TYPE == MX4_F32) {
-        f32x4 *to = reinterpret_cast<f32x4 *>(out + i * 8);
+        f32x4 *to = reinterpret_cast<f32x4 *>(out + (int64_t)i * 8);
         to[0] = f32x4{v[0], v[1], v[2], v[3]};
         to[1] = f32x4{v[4], v[5], v[6], v[7]};
     } else {
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint32_t
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             p[j] = (uint32_t)Mx4Type<TYPE>::store(v[2 * j]) | (uint32_t)Mx4Type<TYPE>::store(v[2 * j + 1]) << 16;
-        *reinterpret_cast<u32x4 *>(out + i * 8) = p;
+        *reinterpret_cast<u32x4 *>(out + (int64_t)i * 8) = p;
     }
 }
 

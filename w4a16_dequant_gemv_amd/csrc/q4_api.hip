@@ -543,8 +543,17 @@ int mx4_linear(const void *x, int32_t type, int64_t stride, const uint8_t *w_cod
     if (!aligned(w_codes, 16) || !aligned(w_scales, 8) || !aligned(workspace, 16) || !aligned(y, 2)) return Q4_ERR_ALIGN;
     if (workspace_bytes < mx4_linear_workspace_size(m, k)) return Q4_ERR_SHAPE;
     uint8_t *codes = (uint8_t *)workspace, *scales = codes + mx4_code_bytes(m, k);
-    if (hipError_t e = mx4_launch_quantize(x, type, m, k, stride, codes, scales, (hipStream_t)stream)) return finish(e);
-    return finish(mx4_launch_matmul(codes, scales, w_codes, w_scales, m, n_out, k, type, y, (hipStream_t)stream));
+    return finish(mx4_launch_linear(x, type, stride, w_codes, w_scales, m, n_out, k, codes, scales, y, (hipStream_t)stream));
+}
+
+int mx4_linear_config(int64_t m, int64_t n_out, int64_t k, int32_t type, int32_t linear, char *name, int64_t name_len)
+{
+    if (!name) return Q4_ERR_NULL;
+    if (name_len < 1 || check_mx4_shape(m, k) || check_mx4_shape(n_out, k) || m * n_out > kMaxElems || type < MX4_F16 ||
+        type > MX4_BF16)
+        return Q4_ERR_SHAPE;
+    mx4_linear_name(m, n_out, k, type, linear != 0, name, name_len);
+    return Q4_OK;
 }
 
 int64_t gptq_factor_workspace_size(int64_t n) { return n > 0 ? gptq_factor_workspace(n) : 0; }

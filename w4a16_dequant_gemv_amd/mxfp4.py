@@ -9,6 +9,7 @@ cores that take them as they are.
 Only argument marshalling happens here: tensors must already live on the GPU
 and the library does all of the arithmetic on torch's current stream.
 """
+from ctypes import create_string_buffer
 from dataclasses import dataclass
 
 import torch
@@ -181,6 +182,16 @@ def linear(x, w, out=None, workspace=None):
     _call("mx4_linear", x.device, x.data_ptr(), _TYPES[x.dtype], stride, w.codes.data_ptr(), w.scales.data_ptr(), m,
           w.rows, k, workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr())
     return out
+
+
+def kernel_config(m, n_out, k, dtype=torch.float16, linear=True):
+    """Names of the kernels that `linear` (or `matmul`) launches for these sizes, as
+    profilers print them.  Nothing is launched; works without a GPU."""
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise W4A16Error(f"dtype must be float16 or bfloat16, got {dtype}")
+    name = create_string_buffer(128)
+    check(lib().mx4_linear_config(m, n_out, k, _TYPES[dtype], 1 if linear else 0, name, len(name)), "mx4_linear_config")
+    return name.value.decode()
 
 
 def workspace_size(m, k):
