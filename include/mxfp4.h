@@ -61,14 +61,15 @@ int mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, in
 int mx4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes, const uint8_t *w_scales,
                int64_t m, int64_t n_out, int64_t k, int32_t type, void *y, void *stream);
 
-/* Workspace bytes of mx4_linear; no HIP call is made. */
-int64_t mx4_linear_workspace_size(int64_t m, int64_t k);
+/* Workspace bytes of mx4_linear, 0 where few rows of x are quantized without one; no HIP
+ * call is made. */
+int64_t mx4_linear_workspace_size(int64_t m, int64_t n_out, int64_t k);
 
 /*
  * The linear layer y = Q(x) W^T: x (MX4_F16 or MX4_BF16) [m][k] is quantized as
  * mx4_quantize does, then multiplied as by mx4_matmul; y has x's type.
- * `workspace`: device memory of at least mx4_linear_workspace_size bytes, overwritten;
- * calls sharing one must not overlap.
+ * `workspace`: device memory of at least mx4_linear_workspace_size bytes (may be NULL where that
+ * is 0), overwritten; calls sharing one must not overlap.
  */
 int mx4_linear(const void *x, int32_t type, int64_t stride, const uint8_t *w_codes, const uint8_t *w_scales, int64_t m,
                int64_t n_out, int64_t k, void *workspace, int64_t workspace_bytes, void *y, void *stream);

@@ -142,6 +142,17 @@ def test_linear(m, n, k):
         codes, scales = ref.quantize(exact(x))
         check_product(y, ref.values(codes, scales), w)
         assert torch.equal(y, mxfp4.matmul(mxfp4.quantize(x), qw, dtype)), "linear is quantize and matmul"
-        ws = torch.empty(mxfp4.workspace_size(m, k) + 16, dtype=torch.uint8, device="cuda")
+        ws = torch.empty(mxfp4.workspace_size(m, n, k) + 16, dtype=torch.uint8, device="cuda")
         out = torch.empty_like(y)
         assert mxfp4.linear(x, qw, out=out, workspace=ws) is out and torch.equal(out, y)
+
+
+@pytest.mark.parametrize("m,n,k", ref.KERNELS)
+def test_every_kernel(m, n, k):
+    qw, w = operand(n, k, m + n)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    for dtype in (torch.float16, torch.bfloat16):
+        x = torch.randn((m, k), generator=g, device="cuda").to(dtype)
+        y = mxfp4.linear(x, qw)
+        check_product(y, ref.values(*ref.quantize(exact(x))), w, mxfp4.kernel_config(m, n, k, dtype))
+        assert torch.equal(y, mxfp4.matmul(mxfp4.quantize(x), qw, dtype))

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import mx4_ref as ref
+from mx4_ref import KERNELS
 from w4a16_dequant_gemv_amd import _lib, mxfp4
 from w4a16_dequant_gemv_amd._lib import Q4_ERR_ALIGN, Q4_ERR_NULL, Q4_ERR_SHAPE, W4A16Error
 
@@ -47,7 +48,7 @@ def matmul(L, **kw):
 
 
 def linear(L, **kw):
-    a = dict(x=P, type=0, stride=64, wc=P, ws=P, m=3, n=5, k=64, space=P, size=1 << 20, y=P)
+    a = dict(x=P, type=0, stride=4096, wc=P, ws=P, m=40, n=5, k=4096, space=P, size=1 << 20, y=P)
     a.update(kw)
     return L.mx4_linear(a["x"], a["type"], a["stride"], a["wc"], a["ws"], a["m"], a["n"], a["k"], a["space"], a["size"],
                         a["y"], None)
@@ -73,8 +74,8 @@ def linear(L, **kw):
     (matmul, dict(y=P + 1), Q4_ERR_ALIGN),
     (linear, dict(x=None), Q4_ERR_NULL), (linear, dict(wc=None), Q4_ERR_NULL), (linear, dict(ws=None), Q4_ERR_NULL),
     (linear, dict(space=None), Q4_ERR_NULL), (linear, dict(y=None), Q4_ERR_NULL), (linear, dict(type=2), Q4_ERR_SHAPE),
-    (linear, dict(m=0), Q4_ERR_SHAPE), (linear, dict(k=16, stride=16), Q4_ERR_SHAPE), (linear, dict(stride=32), Q4_ERR_SHAPE),
-    (linear, dict(stride=68), Q4_ERR_SHAPE), (linear, dict(size=16), Q4_ERR_SHAPE), (linear, dict(size=-1), Q4_ERR_SHAPE),
+    (linear, dict(m=0), Q4_ERR_SHAPE), (linear, dict(k=16, stride=16), Q4_ERR_SHAPE), (linear, dict(stride=4064), Q4_ERR_SHAPE),
+    (linear, dict(stride=4100), Q4_ERR_SHAPE), (linear, dict(size=16), Q4_ERR_SHAPE), (linear, dict(size=-1), Q4_ERR_SHAPE),
     (linear, dict(x=P + 2), Q4_ERR_ALIGN), (linear, dict(wc=P + 8), Q4_ERR_ALIGN), (linear, dict(ws=P + 4), Q4_ERR_ALIGN),
     (linear, dict(space=P + 8), Q4_ERR_ALIGN), (linear, dict(y=P + 1), Q4_ERR_ALIGN)])
 def test_refusals(L, call, bad, code):
@@ -82,11 +83,30 @@ def test_refusals(L, call, bad, code):
 
 
 def test_workspace_size(L):
-    for bad in ((0, 64), (3, 0), (3, 48), (-1, 64), (1 << 25, 64)):
+    for bad in ((0, 5, 64), (3, 0, 64), (3, 5, 0), (3, 5, 48), (-1, 5, 64), (1 << 25, 5, 64)):
         assert L.mx4_linear_workspace_size(*bad) == 0
-    for m, k in ((1, 32), (3, 288), (2048, 4096)):
-        assert L.mx4_linear_workspace_size(m, k) >= m * k // 2 + -(-k // 256) * 8 * m
-        assert linear(L, m=m, k=k, stride=k, size=mxfp4.workspace_size(m, k) - 1) == Q4_ERR_SHAPE
+    for m, n, k in ((17, 100, 4096), (33, 5, 288), (2048, 11008, 4096)):
+        size = mxfp4.workspace_size(m, n, k)
+        assert size >= m * k // 2 + -(-k // 256) * 8 * m
+        assert linear(L, m=m, n=n, k=k, stride=k, size=size - 1) == Q4_ERR_SHAPE
+        assert linear(L, m=m, n=n, k=k, stride=k, space=None) == Q4_ERR_NULL
+    assert mxfp4.workspace_size(1, 4096, 4096) == 0          # quantized on the way
+
+
+def test_config_reports_every_kernel(L):
+    """Each kernel that the rules can choose, at sizes that the GPU tests run."""
+    names = {mxfp4.kernel_config(m, n, k, linear=linear) for m, n, k in KERNELS for linear in (True, False)}
+    for want in ("mx4_rows_kernel<0, 1, 0>", "mx4_quantize_kernel<0>, mx4_rows_kernel<0, 1, -1>", "mx4_rows_kernel<0, 2, -1>",
+                 "mx4_rows_kernel<0, 2, 0>", "mx4_tile_kernel<0, 1, 1, 4>", "mx4_tile_kernel<0, 2, 1, 3>", "mx4_tile_kernel<0, 2, 2, 3>",
+                 "mx4_tile_kernel<0, 2, 2, 2>", "mx4_tile_kernel<0, 3, 4, 2>", "mx4_tile_kernel<0, 4, 4, 2>"):
+        assert want in names, want
+    assert mxfp4.kernel_config(1, 64, 64, torch.bfloat16) == "mx4_rows_kernel<1, 1, 1>"
+    buf = __import__("ctypes").create_string_buffer(8)
+    assert L.mx4_linear_config(1, 64, 64, 0, 1, None, 8) == Q4_ERR_NULL
+    for bad in ((0, 64, 64, 0), (1, 64, 48, 0), (1, 64, 64, 2), (1, 1 << 25, 64, 0)):
+        assert L.mx4_linear_config(*bad, 1, buf, 8) == Q4_ERR_SHAPE
+    assert L.mx4_linear_config(1, 64, 64, 0, 1, buf, 0) == Q4_ERR_SHAPE
+    assert L.mx4_linear_config(1, 64, 64, 0, 1, buf, 8) == 0 and buf.value == b"mx4_row"
 
 
 def test_python_refuses():

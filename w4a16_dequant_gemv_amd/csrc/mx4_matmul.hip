@@ -509,6 +509,8 @@ hipError_t mx4_launch_linear(const void *x, int type, int64_t stride, const uint
     return f(x, stride, wc, ws, (int)m, (int)n_out, (int)k, codes, scales, (uint16_t *)y, stream);
 }
 
+bool mx4_linear_needs_room(int64_t m, int64_t n_out, int64_t k) { return !quantizes_itself(plan_for(m, n_out, k), m, k); }
+
 void mx4_linear_name(int64_t m, int64_t n_out, int64_t k, int type, bool linear, char *name, int64_t name_len)
 {
     const Plan p = plan_for(m, n_out, k);

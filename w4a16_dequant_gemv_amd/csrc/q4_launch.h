@@ -75,7 +75,8 @@ hipError_t mx4_launch_dequantize(const uint8_t *codes, const uint8_t *scales, in
                                  void *out, hipStream_t stream);
 hipError_t mx4_launch_matmul(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int64_t m,
                              int64_t n_out, int64_t k, int type, void *y, hipStream_t stream);
-// codes, scales: room for the quantized x.
+// Whether mx4_launch_linear needs room for the quantized x: `codes` and `scales`.
+bool mx4_linear_needs_room(int64_t m, int64_t n_out, int64_t k);
 hipError_t mx4_launch_linear(const void *x, int type, int64_t stride, const uint8_t *wc, const uint8_t *ws, int64_t m,
                              int64_t n_out, int64_t k, uint8_t *codes, uint8_t *scales, void *y, hipStream_t stream);
 // The kernels of mx4_launch_matmul or, if `linear`, mx4_launch_linear.

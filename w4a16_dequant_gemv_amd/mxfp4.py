@@ -11,14 +11,16 @@ and the library does all of the arithmetic on torch's current stream.
 """
 from ctypes import create_string_buffer
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
 from ._lib import W4A16Error, check, lib
-from .api import _need, _raw_stream, _same_device
+from .api import _need, _raw_stream
 
 BLOCK = 32                              # elements that share a scale
-_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_HALVES = {torch.float16: 0, torch.bfloat16: 1}
+_TYPES = {**_HALVES, torch.float32: 2}
 
 
 @dataclass
@@ -60,43 +62,56 @@ class MXTensor:
         return cls(codes.contiguous(), s.view(rows, -1, 8).transpose(0, 1).contiguous())
 
 
-def _scale_shape(rows, k):
-    return -(-k // 256), rows, 8
-
-
-def _check(q, name):
-    """Raise unless q is an MXTensor whose tensors fit each other, and are on one GPU."""
+def _parts(q, name):
+    """Codes, scales, rows and k of an MXTensor whose tensors fit each other and are on one GPU."""
     if not isinstance(q, MXTensor):
         raise W4A16Error(f"{name} must be an MXTensor")
     c, s = q.codes, q.scales
-    if not (isinstance(c, torch.Tensor) and c.is_cuda and c.dtype is torch.uint8 and c.dim() == 2 and c.is_contiguous()
-            and c.shape[1] and not c.shape[1] % (BLOCK // 2)):
-        raise W4A16Error(f"{name}.codes must be a contiguous uint8 GPU tensor [rows, k // 2], k a multiple of {BLOCK}")
-    shape = _scale_shape(c.shape[0], c.shape[1] * 2)
+    if not (isinstance(c, torch.Tensor) and c.is_cuda and c.dtype is torch.uint8 and c.dim() == 2 and c.is_contiguous()):
+        raise W4A16Error(f"{name}.codes must be a contiguous uint8 GPU tensor [rows, k // 2]")
+    rows, half = c.shape
+    if not half or half % (BLOCK // 2):
+        raise W4A16Error(f"{name}.codes must be [rows, k // 2], k a multiple of {BLOCK}, got {tuple(c.shape)}")
+    shape = (half + 127) // 128, rows, 8
     if not (isinstance(s, torch.Tensor) and s.dtype is torch.uint8 and s.shape == shape and s.device == c.device
             and s.is_contiguous()):
         _need(s, torch.uint8, shape, f"{name}.scales")
         raise W4A16Error("all tensors must be on the same GPU")
+    return c, s, rows, half * 2
 
 
 def _rows_of(x, types):
-    """The row stride of x [rows, k], whose rows may be further apart than k."""
+    """Rows, k, row stride (they may be further apart than k) and type of x [rows, k]."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise W4A16Error("x must be a GPU tensor (there is no CPU implementation)")
-    if x.dtype not in types:
+    kind = types.get(x.dtype)
+    if kind is None:
         raise W4A16Error(f"x must be one of {', '.join(str(t) for t in types)}, got {x.dtype}")
-    if x.dim() != 2 or x.shape[1] % BLOCK or not x.shape[1]:
+    if x.dim() != 2:
+        raise W4A16Error(f"x must be [rows, k], got {tuple(x.shape)}")
+    rows, k = x.shape
+    if not k or k % BLOCK:
         raise W4A16Error(f"x must be [rows, k], k a multiple of {BLOCK}, got {tuple(x.shape)}")
     row, one = x.stride()
     if one != 1:
         raise W4A16Error("the elements of a row of x must lie side by side")
-    return row if x.shape[0] > 1 else x.shape[1]
+    return rows, k, row if rows > 1 else k, kind
 
 
-def _call(name, device, *args):
+def _output(out, like, shape, dtype):
+    """`out` if it is one of these, or a new one on like's GPU."""
+    if out is None:
+        return like.new_empty(shape, dtype=dtype)
+    if not (isinstance(out, torch.Tensor) and out.dtype is dtype and out.shape == shape and out.device == like.device
+            and out.is_contiguous()):
+        _need(out, dtype, shape, "out")
+        raise W4A16Error("all tensors must be on the same GPU")
+    return out
+
+
+def _call(name, gpu, *args):
     """A library call on torch's current stream of that GPU, made the current one."""
     fn = getattr(lib(), name)
-    gpu = device.index
     stream = _raw_stream(gpu)
     if torch.cuda.current_device() == gpu:
         rc = fn(*args, stream)
@@ -107,93 +122,92 @@ def _call(name, device, *args):
         check(rc, name)
 
 
-def _output(out, shape, dtype, like):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _need(out, dtype, shape, "out")
-    _same_device(like, out)
-    return out
-
-
 def quantize(x, out=None):
     """fp16, bf16 or fp32 x [rows, k] -> MXTensor, bit-exact.  Rows may be further
     apart than k (a view into a fused projection's output), a multiple of 16 bytes."""
-    stride = _rows_of(x, _TYPES)
-    rows, k = x.shape
+    rows, k, stride, kind = _rows_of(x, _TYPES)
     if out is None:
-        out = MXTensor(torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device),
-                       torch.empty(_scale_shape(rows, k), dtype=torch.uint8, device=x.device))
+        codes = x.new_empty((rows, k // 2), dtype=torch.uint8)
+        scales = x.new_empty((-(-k // 256), rows, 8), dtype=torch.uint8)
+        out = MXTensor(codes, scales)
     else:
-        _check(out, "out")
-        _need(out.codes, torch.uint8, (rows, k // 2), "out.codes")
-        _same_device(x, out.codes)
+        codes, scales, *size = _parts(out, "out")
+        if size != [rows, k] or codes.device != x.device:
+            raise W4A16Error(f"out must be [{rows}, {k}] on x's GPU, got {size}")
     if rows:
-        _call("mx4_quantize", x.device, x.data_ptr(), _TYPES[x.dtype], rows, k, stride, out.codes.data_ptr(),
-              out.scales.data_ptr())
+        _call("mx4_quantize", x.get_device(), x.data_ptr(), kind, rows, k, stride, codes.data_ptr(), scales.data_ptr())
     return out
 
 
 def dequantize(q, dtype=torch.float32, out=None):
     """MXTensor -> its values [rows, k] in fp32, fp16 or bf16, rounded once where the
     type does not hold them."""
-    _check(q, "q")
+    codes, scales, rows, k = _parts(q, "q")
     if dtype not in _TYPES:
         raise W4A16Error(f"dtype must be float32, float16 or bfloat16, got {dtype}")
-    out = _output(out, (q.rows, q.k), dtype, q.codes)
-    if q.rows:
-        _call("mx4_dequantize", out.device, q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.k, _TYPES[dtype],
+    out = _output(out, codes, (rows, k), dtype)
+    if rows:
+        _call("mx4_dequantize", codes.get_device(), codes.data_ptr(), scales.data_ptr(), rows, k, _TYPES[dtype],
               out.data_ptr())
     return out
 
 
 def matmul(x, w, dtype=torch.float16, out=None):
     """y = x W^T of MXTensors x [m, k] and w [n_out, k], fp16 or bf16 [m, n_out]."""
-    _check(x, "x")
-    _check(w, "w")
-    if x.k != w.k:
-        raise W4A16Error(f"x has rows of {x.k} elements, w of {w.k}")
-    _same_device(x.codes, w.codes)
-    if dtype not in (torch.float16, torch.bfloat16):
+    xc, xs, m, k = _parts(x, "x")
+    wc, ws, n, wk = _parts(w, "w")
+    if k != wk:
+        raise W4A16Error(f"x has rows of {k} elements, w of {wk}")
+    if xc.device != wc.device:
+        raise W4A16Error("all tensors must be on the same GPU")
+    if dtype not in _HALVES:
         raise W4A16Error(f"dtype must be float16 or bfloat16, got {dtype}")
-    out = _output(out, (x.rows, w.rows), dtype, x.codes)
-    if x.rows and w.rows:
-        _call("mx4_matmul", out.device, x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-              x.rows, w.rows, x.k, _TYPES[dtype], out.data_ptr())
+    out = _output(out, xc, (m, n), dtype)
+    if m and n:
+        _call("mx4_matmul", xc.get_device(), xc.data_ptr(), xs.data_ptr(), wc.data_ptr(), ws.data_ptr(), m, n, k,
+              _HALVES[dtype], out.data_ptr())
     return out
 
 
 def linear(x, w, out=None, workspace=None):
     """y = Q(x) W^T: fp16 or bf16 x [m, k] quantized to MXFP4 by rows of 32, times the
     MXTensor w [n_out, k]; y [m, n_out] has x's type.  workspace: at least
-    workspace_size(m, k) bytes on the GPU, 16-byte aligned, for programs that keep one."""
-    stride = _rows_of(x, (torch.float16, torch.bfloat16))
-    _check(w, "w")
-    m, k = x.shape
-    if k != w.k:
-        raise W4A16Error(f"x has rows of {k} elements, w of {w.k}")
-    _same_device(x, w.codes)
-    out = _output(out, (m, w.rows), x.dtype, x)
-    if m == 0 or w.rows == 0:
+    workspace_size(m, n_out, k) bytes on the GPU, 16-byte aligned, for programs that keep
+    one; calls that share it must not overlap."""
+    wc, ws, n, wk = _parts(w, "w")
+    m, k, stride, kind = _rows_of(x, _HALVES)
+    if k != wk:
+        raise W4A16Error(f"x has rows of {k} elements, w of {wk}")
+    if x.device != wc.device:
+        raise W4A16Error("all tensors must be on the same GPU")
+    out = _output(out, x, (m, n), x.dtype)
+    if m == 0 or n == 0:
         return out
-    if workspace is None:
-        workspace = torch.empty(workspace_size(m, k), dtype=torch.uint8, device=x.device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != x.device or not workspace.is_contiguous():
-        raise W4A16Error("workspace must be a contiguous tensor on x's GPU")
-    _call("mx4_linear", x.device, x.data_ptr(), _TYPES[x.dtype], stride, w.codes.data_ptr(), w.scales.data_ptr(), m,
-          w.rows, k, workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr())
+    need, at = workspace_size(m, n, k), None
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != x.device or not workspace.is_contiguous():
+            raise W4A16Error("workspace must be a contiguous tensor on x's GPU")
+        need, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    elif need:
+        workspace = wc.new_empty(need)
+        at = workspace.data_ptr()
+    _call("mx4_linear", x.get_device(), x.data_ptr(), kind, stride, wc.data_ptr(), ws.data_ptr(), m, n, k, at, need,
+          out.data_ptr())
     return out
 
 
 def kernel_config(m, n_out, k, dtype=torch.float16, linear=True):
     """Names of the kernels that `linear` (or `matmul`) launches for these sizes, as
     profilers print them.  Nothing is launched; works without a GPU."""
-    if dtype not in (torch.float16, torch.bfloat16):
+    if dtype not in _HALVES:
         raise W4A16Error(f"dtype must be float16 or bfloat16, got {dtype}")
     name = create_string_buffer(128)
     check(lib().mx4_linear_config(m, n_out, k, _TYPES[dtype], 1 if linear else 0, name, len(name)), "mx4_linear_config")
     return name.value.decode()
 
 
-def workspace_size(m, k):
-    """Bytes of `linear`'s workspace for x [m, k]."""
-    return lib().mx4_linear_workspace_size(m, k)
+@lru_cache(maxsize=4096)
+def workspace_size(m, n_out, k):
+    """Bytes of `linear`'s workspace for x [m, k] and w [n_out, k]: room for the quantized
+    x, none where the product quantizes it itself."""
+    return lib().mx4_linear_workspace_size(m, n_out, k)
