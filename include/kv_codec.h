@@ -218,6 +218,39 @@ int kv_paged_attention(const kv_paged_cache *cache, const kv_paged_batch *batch,
 int kv_paged_attention_config(int64_t tokens, int32_t batch, int32_t table_cols, int32_t page, int32_t n_q, int32_t n_kv,
                               int32_t d, int32_t window, int32_t sinks, char *name, int64_t name_len);
 
+/*
+ * Groups of a batch's sequences that begin with the same tokens (a system prompt, a
+ * document): sequences cu_seqs[g] .. cu_seqs[g + 1] - 1 have the same pool pages in the
+ * first pages[g] columns of their block tables.  Both are int32 device arrays, read when
+ * the kernels run.  A sequence that no group names shares nothing.  cu_seqs must not
+ * decrease (a decreasing one gives unspecified, memory-safe results).
+ */
+typedef struct kv_shared_prefix {
+    const int32_t *cu_seqs;      /* [groups + 1] */
+    const int32_t *pages;        /* [groups] */
+    int32_t groups, max_pages;   /* 1 .. 65536 groups; no group shares more than max_pages (at least 1) */
+} kv_shared_prefix;
+
+/* Workspace bytes of kv_paged_attention_shared; no HIP call is made. */
+int64_t kv_paged_attention_shared_workspace_size(int64_t tokens, int32_t batch, int32_t groups, int32_t max_pages,
+                                                 int32_t page, int32_t n_q, int32_t n_kv, int32_t d);
+
+/*
+ * kv_paged_attention without a window, with the shared pages read and scored once for each
+ * group, all of its rows at a time: the same result but for the order of sums.  Of a group's
+ * shared pages, as many as pages[g], max_pages and every one of its sequences' finished
+ * pages (ctx_lens[b] / page, of those that have rows) allow are taken together; they are
+ * read from the block table of the group's first sequence that has rows.  max_pages
+ * also chooses how the shared pages are worked through, table_cols - max_pages how the rest is.
+ */
+int kv_paged_attention_shared(const kv_paged_cache *cache, const kv_paged_batch *batch, const kv_shared_prefix *prefix,
+                              const uint16_t *q, int64_t q_stride, int32_t n_q, float scale, void *workspace,
+                              int64_t workspace_bytes, uint16_t *out, void *stream);
+
+/* Kernel selection report of kv_paged_attention_shared, as kv_paged_attention_config. */
+int kv_paged_attention_shared_config(int64_t tokens, int32_t batch, int32_t table_cols, int32_t page, int32_t groups,
+                                     int32_t max_pages, int32_t n_q, int32_t n_kv, int32_t d, char *name, int64_t name_len);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,13 @@ class PagedBatch(ctypes.Structure):
                 + [("tokens", _i64), ("batch", _i32), ("table_cols", _i32)])
 
 
+class SharedPrefix(ctypes.Structure):
+    """kv_shared_prefix of kv_codec.h."""
+    _fields_ = [(n, _p) for n in ("cu_seqs", "pages")] + [("groups", _i32), ("max_pages", _i32)]
+
+
 _cache = ctypes.POINTER(PagedCache)
+_prefix = ctypes.POINTER(SharedPrefix)
 _batch = ctypes.POINTER(PagedBatch)
 SIGNATURES = {
     "q4_abi_version": (ctypes.c_int, []),
@@ -56,6 +62,9 @@ SIGNATURES = {
     "kv_paged_attention": (ctypes.c_int, [_cache, _batch, _p, _i64, _i32, ctypes.c_float, _i32, _i32, _p, _i64, _p, _p]),
     "kv_paged_attention_config": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_char_p,
                                                  _i64]),
+    "kv_paged_attention_shared_workspace_size": (_i64, [_i64] + [_i32] * 7),
+    "kv_paged_attention_shared": (ctypes.c_int, [_cache, _batch, _prefix, _p, _i64, _i32, ctypes.c_float, _p, _i64, _p, _p]),
+    "kv_paged_attention_shared_config": (ctypes.c_int, [_i64] + [_i32] * 8 + [ctypes.c_char_p, _i64]),
     "sq_absmax_update_f16": (ctypes.c_int, [_p, _i64, _i32, _p, _p]),
     "sq_absmax_update_f32": (ctypes.c_int, [_p, _i64, _i32, _p, _p]),
     "sq_smooth_factors": (ctypes.c_int, [_p, _p, _i32, ctypes.c_float, _p, _p]),

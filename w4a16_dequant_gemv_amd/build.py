@@ -34,7 +34,7 @@ PER_FILE = {
     "producers.hip": EXACT_FP32,
 }
 SOURCES = ["q4_api.hip", "q4_quantize.hip", "q4_gemv.hip", "q4_gemm.hip", "kv_codec.hip", "kv_append.hip",
-           "kv_attention.hip", "w8a8.hip", "producers.hip", "mx4_quantize.hip", "mx4_matmul.hip"]
+           "kv_attention.hip", "kv_shared.hip", "w8a8.hip", "producers.hip", "mx4_quantize.hip", "mx4_matmul.hip"]
 
 
 # Host-side AddressSanitizer + UndefinedBehaviorSanitizer (argument checking,

@@ -107,11 +107,13 @@ int check_heads(int64_t n_q, int64_t n_kv)
 
 int check_paged_d(int32_t d) { return d == 64 || d == 96 || d == 128 || d == 256 ? Q4_OK : Q4_ERR_SHAPE; }
 
+int check_page(int32_t page) { return page == 64 || page == 128 || page == 256 ? Q4_OK : Q4_ERR_SHAPE; }
+
 int check_paged_cache(const kv_paged_cache *c)
 {
     if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->k_tail || !c->v_tail) return Q4_ERR_NULL;
     if (check_heads(c->n_kv, c->n_kv) || check_paged_d(c->d)) return Q4_ERR_SHAPE;
-    if (c->page != 64 && c->page != 128 && c->page != 256) return Q4_ERR_SHAPE;
+    if (check_page(c->page)) return Q4_ERR_SHAPE;
     const int64_t head = (int64_t)c->page * c->d, most = kMaxPool / (head * c->n_kv);
     if (c->pages < 1 || c->pages > most || c->slots < 1 || c->slots > most / 2) return Q4_ERR_SHAPE;
     if (c->pages > INT32_MAX || c->slots > INT32_MAX) return Q4_ERR_SHAPE;
@@ -418,6 +420,64 @@ int kv_paged_attention_config(int64_t tokens, int32_t batch, int32_t table_cols,
     if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return Q4_ERR_SHAPE;
     return finish(kv_launch_attention(cache, call, h, (int64_t)n_q * d, n_q, 1.0f, window, sinks, f, h, nullptr, name,
                                       name_len));
+}
+
+namespace {
+
+int check_shared(const kv_shared_prefix *p)
+{
+    if (!p || !p->cu_seqs || !p->pages) return Q4_ERR_NULL;
+    if (p->groups < 1 || p->groups > 65536 || p->max_pages < 1 || p->max_pages > (1 << 24)) return Q4_ERR_SHAPE;
+    return aligned(p->cu_seqs, 4) && aligned(p->pages, 4) ? Q4_OK : Q4_ERR_ALIGN;
+}
+
+}  // namespace
+
+int64_t kv_paged_attention_shared_workspace_size(int64_t tokens, int32_t batch, int32_t groups, int32_t max_pages,
+                                                 int32_t page, int32_t n_q, int32_t n_kv, int32_t d)
+{
+    if (check_rows(tokens) || batch < 1 || batch > 65536 || check_heads(n_q, n_kv) || check_paged_d(d)) return 0;
+    if (groups < 1 || groups > 65536 || max_pages < 1 || max_pages > (1 << 24) || check_page(page)) return 0;
+    return kv_shared_workspace(tokens, batch, groups, max_pages, page, n_q, n_kv, d);
+}
+
+int kv_paged_attention_shared(const kv_paged_cache *cache, const kv_paged_batch *batch, const kv_shared_prefix *prefix,
+                              const uint16_t *q, int64_t q_stride, int32_t n_q, float scale, void *workspace,
+                              int64_t workspace_bytes, uint16_t *out, void *stream)
+{
+    if (int rc = check_paged_cache(cache)) return rc;
+    if (int rc = check_paged_batch(batch, cache)) return rc;
+    if (int rc = check_shared(prefix)) return rc;
+    if (!q || !workspace || !out) return Q4_ERR_NULL;
+    if (check_heads(n_q, cache->n_kv) || !(scale > 0.0f && scale <= 1e6f)) return Q4_ERR_SHAPE;
+    if (batch->tokens * n_q * cache->d > kMaxElems || (int64_t)prefix->groups * cache->n_kv > int64_t(1) << 21) return Q4_ERR_SHAPE;
+    if (int rc = check_paged_rows(q, q_stride, (int64_t)n_q * cache->d, batch->tokens)) return rc;
+    if (!aligned(workspace, 16) || !aligned(out, 16)) return Q4_ERR_ALIGN;
+    if (workspace_bytes < kv_shared_workspace(batch->tokens, batch->batch, prefix->groups, prefix->max_pages, cache->page,
+                                              n_q, cache->n_kv, cache->d))
+        return Q4_ERR_SHAPE;
+    return finish(kv_launch_shared(*cache, *batch, *prefix, q, q_stride, n_q, scale, workspace, out, (hipStream_t)stream));
+}
+
+int kv_paged_attention_shared_config(int64_t tokens, int32_t batch, int32_t table_cols, int32_t page, int32_t groups,
+                                     int32_t max_pages, int32_t n_q, int32_t n_kv, int32_t d, char *name, int64_t name_len)
+{
+    // only the sizes are read: the pointers stand for the arrays
+    static const uint32_t any[4] __attribute__((aligned(16))) = {};
+    int8_t *b = (int8_t *)any;
+    float *f = (float *)any;
+    uint16_t *h = (uint16_t *)any;
+    const int32_t *i = (const int32_t *)any;
+    const kv_paged_cache cache = {b, b, f, f, h, h, 1, 1, n_kv, d, page};
+    const kv_paged_batch call = {i, i, i, i, tokens, batch, table_cols};
+    const kv_shared_prefix prefix = {i, i, groups, max_pages};
+    if (!name) return Q4_ERR_NULL;
+    if (name_len < 1) return Q4_ERR_SHAPE;
+    if (int rc = check_paged_cache(&cache)) return rc;
+    if (int rc = check_paged_batch(&call, &cache)) return rc;
+    if (int rc = check_shared(&prefix)) return rc;
+    if (check_heads(n_q, n_kv) || tokens * n_q * d > kMaxElems || (int64_t)groups * n_kv > int64_t(1) << 21) return Q4_ERR_SHAPE;
+    return finish(kv_launch_shared(cache, call, prefix, h, (int64_t)n_q * d, n_q, 1.0f, f, h, nullptr, name, name_len));
 }
 
 int sq_absmax_update_f16(const uint16_t *x, int64_t rows, int32_t cols, float *amax, void *stream)

@@ -161,11 +161,23 @@ def _workspace_size(tokens, batch, n_q, n_kv, d):
     return lib().kv_paged_attention_workspace_size(tokens, batch, n_q, n_kv, d)
 
 
-def attention_config(tokens, batch, table_cols, n_q, n_kv, d, page=128, window=0, sinks=0):
+@lru_cache(maxsize=4096)
+def _shared_workspace_size(tokens, batch, groups, max_pages, page, n_q, n_kv, d):
+    return lib().kv_paged_attention_shared_workspace_size(tokens, batch, groups, max_pages, page, n_q, n_kv, d)
+
+
+def attention_config(tokens, batch, table_cols, n_q, n_kv, d, page=128, window=0, sinks=0, groups=0, max_pages=0):
     """Names of the kernels that PagedKVCache.attend launches for `tokens` queries of
-    `batch` sequences with block tables of `table_cols` pages, as profilers print them.
-    Nothing is launched; works without a GPU."""
-    name = create_string_buffer(160)
+    `batch` sequences with block tables of `table_cols` pages (with `groups` and
+    `max_pages` of a SharedPrefix), as profilers print them.  Nothing is launched; works
+    without a GPU."""
+    name = create_string_buffer(256)
+    if groups:
+        if window or sinks:
+            raise W4A16Error("a shared prefix takes no window")
+        check(lib().kv_paged_attention_shared_config(tokens, batch, table_cols, page, groups, max_pages, n_q, n_kv, d,
+                                                     name, len(name)), "kv_paged_attention_shared_config")
+        return name.value.decode()
     check(lib().kv_paged_attention_config(tokens, batch, table_cols, page, n_q, n_kv, d, window, sinks, name, len(name)),
           "kv_paged_attention_config")
     return name.value.decode()
@@ -218,6 +230,43 @@ class PagedBatch(_Kept):
         if known is None or known[0] != at:
             B = c.shape[0]
             known = self._known = at, (byref(_lib.PagedBatch(*at, B, t.shape[1])), B)
+        return known[1]
+
+
+class SharedPrefix(_Kept):
+    """Groups of a batch's sequences that begin with the same tokens (kv_shared_prefix in
+    kv_codec.h), int32 GPU tensors: sequences cu_seqs[g] .. cu_seqs[g+1]-1 have the same pool
+    pages in the first pages[g] columns of their block tables.  max_pages: no group
+    shares more (of a group that does, the first max_pages are taken together).  The tensors
+    are read when the kernels run, as a PagedBatch's are."""
+
+    def __init__(self, cu_seqs, pages, max_pages):
+        if not isinstance(pages, torch.Tensor) or pages.dim() != 1 or not 1 <= pages.shape[0] <= 65536:
+            raise W4A16Error("pages must be an int32 GPU tensor [groups] of 1 to 65536 groups")
+        G = pages.shape[0]
+        _need(cu_seqs, torch.int32, (G + 1,), "cu_seqs")
+        _need(pages, torch.int32, (G,), "pages")
+        _same_device(cu_seqs, pages)
+        if not 1 <= max_pages <= 1 << 24:
+            raise W4A16Error(f"max_pages must be in [1, 2^24], got {max_pages}")
+        self._tensors, self._device, self._known = (cu_seqs, pages), cu_seqs.device, None
+        self._max_pages = int(max_pages)
+
+    cu_seqs = property(lambda self: self._tensors[0])
+    pages = property(lambda self: self._tensors[1])
+    max_pages = property(lambda self: self._max_pages)
+
+    def _struct(self, device):
+        """The library's struct, the number of groups and max_pages."""
+        if self._device != device:
+            raise W4A16Error("all tensors must be on the same GPU")
+        c, p = self._tensors
+        if c.numel() != p.numel() + 1 or not (c.is_contiguous() and p.is_contiguous()):
+            self.__init__(c, p, self._max_pages)               # changed in place: checked again
+        at = (c.data_ptr(), p.data_ptr(), p.numel(), self._max_pages)
+        known = self._known
+        if known is None or known[0] != at:
+            known = self._known = at, (byref(_lib.SharedPrefix(*at)), *at[2:])
         return known[1]
 
 
@@ -359,12 +408,14 @@ class PagedKVCache(_Kept):
             self._call("kv_paged_read", gpu, c, ids.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr())
         return k_out, v_out
 
-    def attend(self, q, batch, scale=None, window=0, sinks=0, out=None, workspace=None):
+    def attend(self, q, batch, scale=None, window=0, sinks=0, out=None, workspace=None, prefix=None):
         """softmax(scale * q k^T) v of fp16 q [T, n_q, d] over the cache, into fp16
         [T, n_q, d]; the batch's own tokens have been appended before.  Row i of
         a sequence sees the tokens up to its own, with window > 0 the last
         `window` of them and the sequence's first `sinks`.  scale defaults to
-        d^-1/2.  Rows of no sequence are left as they were."""
+        d^-1/2.  Rows of no sequence are left as they were.  With `prefix` (a
+        SharedPrefix; no window) the pages that a group of sequences share are read and
+        scored once for all of its rows: the same result but for the order of sums."""
         c, dev, gpu = self._checked()
         qs = _heads(q, None, self.d, "q", dev)
         T, n_q = q.shape[:2]
@@ -372,6 +423,8 @@ class PagedKVCache(_Kept):
             raise W4A16Error(f"q must have a multiple of {self.n_kv} heads, at most 1024, got {n_q}")
         if window < 0 or sinks < 0 or (sinks and not window) or max(window, sinks) >= 1 << 31:
             raise W4A16Error("window and sinks must not be negative, and sinks need a window")
+        if window and prefix is not None:
+            raise W4A16Error("a shared prefix takes no window")
         scale = self.d ** -0.5 if scale is None else float(scale)
         if not 0.0 < scale <= 1e6:
             raise W4A16Error(f"scale must be in (0, 1e6], got {scale}")
@@ -382,11 +435,21 @@ class PagedKVCache(_Kept):
         if T == 0:
             return out
         b, B = batch._struct(T, dev)
-        need = _workspace_size(T, B, n_q, self.n_kv, self.d)
+        if prefix is None:
+            need = _workspace_size(T, B, n_q, self.n_kv, self.d)
+        elif not isinstance(prefix, SharedPrefix):
+            raise W4A16Error("prefix must be a SharedPrefix")
+        else:
+            p, groups, max_pages = prefix._struct(dev)
+            need = _shared_workspace_size(T, B, groups, max_pages, self.page, n_q, self.n_kv, self.d)
         if workspace is None:
             workspace = self.k.new_empty(need)
         elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
             raise W4A16Error("workspace must be a contiguous tensor on the cache's GPU")
-        self._call("kv_paged_attention", gpu, c, b, q.data_ptr(), qs, n_q, scale, window, sinks,
-                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr())
+        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if prefix is None:
+            self._call("kv_paged_attention", gpu, c, b, q.data_ptr(), qs, n_q, scale, window, sinks, at, size,
+                       out.data_ptr())
+        else:
+            self._call("kv_paged_attention_shared", gpu, c, b, p, q.data_ptr(), qs, n_q, scale, at, size, out.data_ptr())
         return out
