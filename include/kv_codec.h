@@ -232,16 +232,16 @@ typedef struct kv_shared_prefix {
 } kv_shared_prefix;
 
 /* Workspace bytes of kv_paged_attention_shared; no HIP call is made. */
-int64_t kv_paged_attention_shared_workspace_size(int64_t tokens, int32_t batch, int32_t groups, int32_t max_pages,
-                                                 int32_t page, int32_t n_q, int32_t n_kv, int32_t d);
+int64_t kv_paged_attention_shared_workspace_size(int64_t tokens, int32_t batch, int32_t table_cols, int32_t page,
+                                                 int32_t groups, int32_t max_pages, int32_t n_q, int32_t n_kv, int32_t d);
 
 /*
  * kv_paged_attention without a window, with the shared pages read and scored once for each
  * group, all of its rows at a time: the same result but for the order of sums.  Of a group's
- * shared pages, as many as pages[g], max_pages and every one of its sequences' finished
- * pages (ctx_lens[b] / page, of those that have rows) allow are taken together; they are
- * read from the block table of the group's first sequence that has rows.  max_pages
- * also chooses how the shared pages are worked through, table_cols - max_pages how the rest is.
+ * pages the first min(pages[g], max_pages) are taken together, from the block table of its first
+ * sequence that has rows and has finished them (ctx_lens[b] / page); a sequence that has not
+ * attends to all of its tokens by itself.  How a call is run goes by max_pages for the
+ * shared pages and table_cols - max_pages for the sequences' own tokens.
  */
 int kv_paged_attention_shared(const kv_paged_cache *cache, const kv_paged_batch *batch, const kv_shared_prefix *prefix,
                               const uint16_t *q, int64_t q_stride, int32_t n_q, float scale, void *workspace,

@@ -22,6 +22,45 @@ def lengths(c):
 def sizes(c):
     """(tokens, batch, table_cols, groups, max_pages) of the call."""
     own, new = lengths(c)
-    most = max(p for p, _ in c.groups)
+    most = max(1, *(p for p, _ in c.groups))
     cols = max(p + -(-o // c.page) for p, o in zip([p for p, n in c.groups for _ in range(n)], own)) + 1 + c.wide
     return sum(new), len(new), cols, len(c.groups), most
+
+
+CASES = [
+    Case(128, 128, 8, 8, ((3, 5),), 90, 1, 0),                       # <128, false>, 4 waves
+    Case(128, 64, 8, 8, ((6, 70),), 90, 1, 6),                       # <128, false>, 2 waves
+    Case(128, 64, 8, 8, ((6, 70),), 90, 1, 0),                       # <128, false>, 1 waves
+    Case(128, 64, 2, 16, ((3, 180),), 60, 1, 0),                     # <128, true>, 4 waves
+    Case(128, 64, 8, 8, ((3, 260),), 60, 1, 8),                      # <128, true>, 2 waves
+    Case(128, 64, 8, 8, ((3, 260),), 60, 1, 0),                      # <128, true>, 1 waves
+    Case(64, 64, 8, 8, ((3, 5),), 90, 1, 0),                         # <64, false>, 4 waves
+    Case(64, 64, 16, 16, ((6, 70),), 90, 1, 6),                      # <64, false>, 2 waves
+    Case(64, 64, 16, 16, ((6, 70),), 90, 1, 0),                      # <64, false>, 1 waves
+    Case(64, 64, 2, 16, ((3, 260),), 60, 1, 0),                      # <64, true>, 4 waves
+    Case(64, 64, 8, 8, ((3, 260),), 60, 1, 8),                       # <64, true>, 2 waves
+    Case(64, 64, 8, 8, ((3, 260),), 60, 1, 0),                       # <64, true>, 1 waves
+    Case(96, 64, 8, 8, ((3, 5),), 90, 1, 0),                         # <96, false>, 4 waves
+    Case(96, 64, 8, 8, ((6, 70),), 90, 1, 6),                        # <96, false>, 2 waves
+    Case(96, 64, 8, 8, ((6, 70),), 90, 1, 0),                        # <96, false>, 1 waves
+    Case(96, 64, 2, 16, ((3, 260),), 60, 1, 0),                      # <96, true>, 4 waves
+    Case(96, 64, 8, 8, ((3, 260),), 60, 1, 8),                       # <96, true>, 2 waves
+    Case(96, 64, 8, 8, ((3, 260),), 60, 1, 0),                       # <96, true>, 1 waves
+    Case(256, 64, 8, 8, ((3, 5),), 90, 1, 0),                        # <256, false>, 4 waves
+    Case(256, 64, 16, 16, ((7, 20), (2, 3), (1, 1)), 90, 1, 6),      # <256, false>, 2 waves
+    Case(256, 64, 16, 16, ((7, 20), (2, 3), (1, 1)), 90, 1, 0),      # <256, false>, 1 waves
+    Case(256, 64, 1, 15, ((3, 180),), 60, 1, 0),                  # rows<256>, 4 waves
+    Case(256, 64, 8, 8, ((3, 100),), 60, 3, 8),                      # rows<256>, 2 waves
+    Case(256, 64, 8, 16, ((3, 180),), 60, 1, 0),                     # rows<256>, 1 waves
+    # tables much wider than the sequences, and sequences as long as theirs: chunks of own tokens
+    Case(128, 128, 2, 8, ((3, 5),), 200, 1, 40),
+    Case(64, 64, 1, 8, ((7, 20), (2, 3), (1, 1)), 2500, 1, 0),
+    Case(256, 64, 2, 2, ((5, 4),), 3000, 3, 10),
+    # several rows a sequence, pages of 256, one sequence, single rows, many groups
+    Case(96, 64, 2, 8, ((4, 6), (5, 9)), 90, 5, 0),
+    Case(128, 256, 1, 40, ((2, 9),), 300, 1, 3),
+    Case(64, 64, 2, 2, ((1, 1),), 3, 1, 0),
+    Case(128, 64, 2, 4, tuple((i % 4, 1 + i % 3) for i in range(1, 80)), 70, 1, 0),
+    # more rows than that: as without shared pages
+    Case(128, 128, 2, 16, ((4, 3),), 400, 60, 0),
+]

@@ -62,7 +62,7 @@ SIGNATURES = {
     "kv_paged_attention": (ctypes.c_int, [_cache, _batch, _p, _i64, _i32, ctypes.c_float, _i32, _i32, _p, _i64, _p, _p]),
     "kv_paged_attention_config": (ctypes.c_int, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_char_p,
                                                  _i64]),
-    "kv_paged_attention_shared_workspace_size": (_i64, [_i64] + [_i32] * 7),
+    "kv_paged_attention_shared_workspace_size": (_i64, [_i64] + [_i32] * 8),
     "kv_paged_attention_shared": (ctypes.c_int, [_cache, _batch, _prefix, _p, _i64, _i32, ctypes.c_float, _p, _i64, _p, _p]),
     "kv_paged_attention_shared_config": (ctypes.c_int, [_i64] + [_i32] * 8 + [ctypes.c_char_p, _i64]),
     "sq_absmax_update_f16": (ctypes.c_int, [_p, _i64, _i32, _p, _p]),

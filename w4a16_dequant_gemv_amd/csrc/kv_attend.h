@@ -1,5 +1,5 @@
 // kv_attend.h -- attention over the paged INT8 cache (kv_codec.h): what the kernels of
-// kv_attention.hip and, where sequences share their first pages, of kv_shared.hip do.
+// kv_attention.hip and, for sequences that share their first pages, of kv_shared.hip have in common.
 //
 // Mathematics.  With page scales ks, vs and codes a, c the output row is
 //   o = sum_j p_j vs c_j / sum_j p_j,   p_j = 2^(x_j),  x_j = log2(e) scale ks q . a_j.
@@ -22,7 +22,6 @@
 // V pages are read straight into operand registers in contiguous 16-byte loads.
 #pragma once
 
-#include <limits.h>
 #include <stdio.h>
 
 #include <algorithm>
@@ -121,31 +120,49 @@ struct Args {
     float *part, *stats;         // sums and (m, l) of unfinished row blocks
     int32_t *notes;              // [workers][4]: what the joining kernel has to do
     uint16_t *out;
-    static constexpr bool kShared = false;
-    __device__ int skip(int) const { return 0; }
 };
 
 // Sequences cu_seqs[g] .. cu_seqs[g + 1] - 1 have their first pages in common.  What all their
-// rows get from those pages comes first and apart, as `pre_splits` parts of each row (all rows
-// of a group against one reading of the pages); the other tiles are attended to as above,
-// and each row is joined with its parts where it is finished.
+// rows get from those pages is computed apart, as `splits` parts of each row (all rows of a
+// group against one reading of the pages); a sequence attends to its other tiles by itself, in up to
+// `chunks` parts, and each row is joined from its parts: part and stats are [row of out][splits + chunks].
 struct SharedArgs : Args {
     const int32_t *cu_seqs, *pages;
-    int groups, max_pages, pre_splits;
-    float *pre_part, *pre_stats; // [row of out][pre_splits] sums and (m, l)
-    int32_t *skips;              // [batch]: a sequence's tiles that are in the parts; written by the kernels of the parts
-    static constexpr bool kShared = true;
-    __device__ int skip(int b) const { return skips[b]; }
+    int groups, max_pages;
+    int splits, chunks;          // a row's parts of the shared pages, and of its sequence's own tokens
+    int chunk;                   // tiles of each of these but the last
+
+    __device__ int pages_of(int g) const { return min(min(max(pages[g], 0), max_pages), batch.table_cols); }
+    // What is known of the groups before a sequence is: the sequences that they name, and the first one's pages.
+    struct Named {
+        int lo, hi, pages;
+    };
+    __device__ Named named() const { return {cu_seqs[0], cu_seqs[groups], pages_of(0)}; }
+    __device__ int places() const { return splits + chunks; }
+    // The tiles of sequence b that its parts of the shared pages hold: none where it has not finished the shared pages.
+    __device__ int skip(const KvSeq &s, int b, const Named &all) const
+    {
+        if (s.n <= 0 || b < all.lo || b >= all.hi) return 0;
+        int p = all.pages;
+        if (groups > 1) {
+            int lo = 0, hi = groups;                           // cu_seqs[lo] <= b < cu_seqs[hi]
+            while (lo + 1 < hi) {
+                const int mid = (lo + hi) / 2;
+                if (cu_seqs[mid] <= b) lo = mid; else hi = mid;
+            }
+            p = pages_of(lo);
+        }
+        return s.ctx >> page_shift >= p ? p << (page_shift - 6) : 0;
+    }
 };
 
 // The tiles that some of a sequence's rows at places lo .. hi sees: the first
-// `head` ones and those from `first` on (`count` in all).
+// `head` ones and those from `first` on (`count` in all); with no window those from `skip` on.
 struct Tiles {
     int head, first, count;
     __device__ int at(int i) const { return i < head ? i : i - head + first; }
 };
 
-// (with no window the tiles from `skip` on).
 __device__ __forceinline__ Tiles visible_tiles(const Args &a, int lo, int hi, int skip = 0)
 {
     Tiles t = {0, skip, hi / kTile + 1 - skip};
@@ -162,69 +179,6 @@ __device__ __forceinline__ Tiles visible_tiles(const Args &a, const KvSeq &s, in
 {
     return visible_tiles(a, s.ctx, s.total() - 1, skip);
 }
-
-// The tiles of sequence b that its parts of the shared pages hold.  Whatever the array holds
-// (a sequence that no group names, or two), no more than its finished pages.
-template <typename A>
-__device__ __forceinline__ int skipped(const A &a, const KvSeq &s, int b)
-{
-    if constexpr (!A::kShared) return 0;
-    return s.n > 0 ? min(max(a.skip(b), 0), (s.ctx >> a.page_shift) << (a.page_shift - 6)) : 0;
-}
-
-// Joins a row of out with its parts of the shared pages: their factors first, then any of its channels.
-struct Shared {
-    float keep, top;
-    __device__ Shared(const SharedArgs &a, int64_t row, float m, float &l) : top(m)
-    {
-        const float *stats = a.pre_stats + row * a.pre_splits * 2;
-        for (int p = 0; p < a.pre_splits; ++p) top = fmaxf(top, stats[2 * p]);
-        keep = __builtin_amdgcn_exp2f(m - top);
-        l *= keep;
-        for (int p = 0; p < a.pre_splits; ++p) l += stats[2 * p + 1] * __builtin_amdgcn_exp2f(stats[2 * p] - top);
-    }
-    __device__ f32x4 add(const SharedArgs &a, int64_t row, int d, int ch, f32x4 o) const
-    {
-        o *= keep;
-        for (int p = 0; p < a.pre_splits; ++p) {
-            const int64_t at = row * a.pre_splits + p;
-            o += *reinterpret_cast<const f32x4 *>(a.pre_part + at * d + ch) * __builtin_amdgcn_exp2f(a.pre_stats[at * 2] - top);
-        }
-        return o;
-    }
-};
-
-// The split kernel's work as numbered units: sequence after sequence, its row
-// blocks of RB rows one after the other, each with kStart units for the latency
-// of beginning it and then one for each of the sequence's tiles.  Lane i of a
-// wave holds sequence 64 chunk + i.
-template <int RB>
-struct Roster {
-    int chunk = -1, skip;
-    KvSeq s;
-    int64_t units, end;          // the sequence's units, and their sum up to it within the chunk
-
-    template <typename A>
-    __device__ void load(const A &a, int c)
-    {
-        chunk = c;
-        const int b = c * 64 + (threadIdx.x & 63);
-        units = 0;
-        s = {0, 0, 0, 0};
-        skip = 0;
-        if (b < a.batch.batch) {
-            s = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
-            skip = skipped(a, s, b);
-            if (s.n) units = (int64_t)((s.n * a.group + RB - 1) / RB) * (a.whole ? 1 : visible_tiles(a, s, skip).count + kStart);
-        }
-        end = kv_wave_scan(units);
-    }
-    __device__ KvSeq get(int i) const
-    {
-        return {__builtin_amdgcn_readlane(s.q0, i), __builtin_amdgcn_readlane(s.n, i),
-                __builtin_amdgcn_readlane(s.ctx, i), __builtin_amdgcn_readlane(s.slot, i)};
-    }
-};
 
 // One wave's state for QT blocks of 16 rows.
 template <int D, int QT>
@@ -529,364 +483,57 @@ __device__ __forceinline__ void attend_tiles(Wave<D, QT> &s, const Args &a, cons
     }
 }
 
-// One kv head's work is cut into equal runs of units, one for each worker (a
-// workgroup), whatever the sequences' lengths (or, with few tokens, a worker takes a
-// row block as a whole: then the row blocks are the units); a worker's four waves take its
-// tiles in turn and join at the end of each row block.  A row block that one
-// worker has whole is finished there; the others' parts go to the workspace: the
-// run's first row block to place 0, its last to place 1.  The worker that has a
-// shared row block's first tile leaves a note for the kernel that joins them.
-// Bound by HBM with many tokens (32 x 32k, 64 query heads on 8: 377 us, 5.7 TB/s; 64
-// ragged sequences of 4k on average: 67 us, 4.7 TB/s, where a fixed number of cuts for
-// each sequence took 89), by latency with few (1 x 500 tokens: 9.1 us, uncut).
-// Pages go from memory to operand registers: no wave shares a tile with another, so
-// LDS would add a trip and a barrier.  P is used as two fp16 parts, whose second one
-// costs little here (5 rows of 8 sequences: 21.8 us, 20.0 without it).
-template <int D, int QT, typename A>
-__device__ __forceinline__ void attend_split(const A &a)
-{
-    constexpr int DT = D / 16, RB = 16 * QT;
-    constexpr int PAD = D + 4;                       // floats a row of the joining buffer: four banks on per row
-    __shared__ float joint[kWaves][16 * PAD], stat_m[kWaves][RB], stat_l[kWaves][RB];
-    const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);          // a scalar: its branches are uniform
-    const int h = blockIdx.x % a.cache.n_kv, worker = blockIdx.x / a.cache.n_kv;
-
-    // how many units there are, and what a worker takes: no less than a tile for each wave
-    Roster<RB> roster;
-    int64_t run = 1, units = worker + 1;
-    if (!a.whole) {
-        units = 0;
-        for (int c = 0; c * 64 < a.batch.batch; ++c) {
-            roster.load(a, c);
-            units += kv_lane(roster.end, 63);
-        }
-        run = (int64_t)((double)units * a.inv_workers);
-        while (run * a.workers < units) ++run;
-        run = max(run, (int64_t)kWaves);
-    }
-    int64_t u = run * worker;
-    const int64_t end = min(u + run, units);
-    int note_row = 0, note_rows = 0, note_parts = 0, note_place = 0;   // place: 2 is added for rows with shared pages
-
-    // the sequence with unit u
-    int b = a.batch.batch;
-    int64_t off = u;
-    for (int c = 0; u < end && c * 64 < a.batch.batch; ++c) {
-        if (roster.chunk != c) roster.load(a, c);
-        const uint64_t hit = __ballot(off < roster.end);
-        if (hit) {
-            const int i = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-            b = c * 64 + i;
-            off -= kv_lane(roster.end - roster.units, i);
-            break;
-        }
-        off -= kv_lane(roster.end, 63);
-    }
-
-    for (int place = 0; u < end && b < a.batch.batch;) {
-        if (roster.chunk != b >> 6) roster.load(a, b >> 6);
-        if (off >= kv_lane(roster.units, b & 63)) {          // done with this one, or it has no rows
-            off = 0;
-            ++b;
-            continue;
-        }
-        const KvSeq seq = roster.get(b & 63);
-        const int skip = A::kShared ? __builtin_amdgcn_readlane(roster.skip, b & 63) : 0;
-        const Tiles tiles = visible_tiles(a, seq, skip);
-        const int rows = seq.n * a.group;
-        const int per_block = a.whole ? 1 : tiles.count + kStart, rb = (int)(off / per_block), at = (int)(off - (int64_t)rb * per_block);
-        const int take = (int)min((int64_t)(per_block - at), end - u);
-        const int t0 = max(at - kStart, 0), count = a.whole ? tiles.count : max(at + take - kStart, 0) - t0;
-        const int64_t last = u - at + per_block - 1;         // the row block's last unit
-        u += take;
-        off += take;
-        if (count == 0) continue;                            // only the beginning is this worker's
-
-        Wave<D, QT> s;
-        begin(s, a, seq, h, rb);
-        const int at_min = seq.ctx + rb * RB / a.group;
-        const int at_max = seq.ctx + (min(rb * RB + RB, rows) - 1) / a.group;
-        attend_tiles<kWaves>(s, a, seq, b, h, tiles, t0 + wave, t0 + count, at_min, at_max);
-
-        // join the waves
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            const float l = column_sum(s.l[t]);
-            if (g == 0) {
-                stat_m[wave][t * 16 + m16] = s.m[t];
-                stat_l[wave][t * 16 + m16] = l;
-            }
-        }
-        __syncthreads();
-        const bool whole = t0 == 0 && count == tiles.count;
-        const int64_t slot = ((int64_t)worker * 2 + place) * a.cache.n_kv + h;
-        if (t0 == 0 && !whole) {
-            note_row = seq.q0 * a.group + rb * RB;
-            note_rows = min(RB, rows - rb * RB);
-            note_parts = (int)(last / run) - worker + 1;
-            note_place = place + (skip > 0 ? 2 : 0);
-        }
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            float top = kNone;
-#pragma unroll
-            for (int v = 0; v < kWaves; ++v) top = fmaxf(top, stat_m[v][t * 16 + m16]);
-            const float f = __builtin_amdgcn_exp2f(s.m[t] - top);
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-                *reinterpret_cast<f32x4 *>(&joint[wave][m16 * PAD + d * 16 + g * 4]) = s.o[t][d] * f;
-            __syncthreads();
-            constexpr int PER = D / 4;                   // threads of a row, four channels each
-            for (int i = threadIdx.x; i < 16 * PER; i += kThreads) {
-                const int row = i / PER, ch = i % PER * 4, r = rb * RB + t * 16 + row;
-                if (r >= rows) continue;
-                f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int v = 0; v < kWaves; ++v) o += *reinterpret_cast<const f32x4 *>(&joint[v][row * PAD + ch]);
-                float mm = kNone, l = 0.0f;
-#pragma unroll
-                for (int v = 0; v < kWaves; ++v) mm = fmaxf(mm, stat_m[v][t * 16 + row]);
-#pragma unroll
-                for (int v = 0; v < kWaves; ++v)
-                    l += stat_l[v][t * 16 + row] * __builtin_amdgcn_exp2f(stat_m[v][t * 16 + row] - mm);
-                if (whole) {
-                    const int tok = r / a.group, hq = h * a.group + r - tok * a.group;
-                    const int64_t at_out = (int64_t)(seq.q0 + tok) * a.n_q + hq;
-                    if constexpr (A::kShared) {
-                        if (skip > 0) o = Shared(a, at_out, mm, l).add(a, at_out, D, ch, o);
-                    }
-                    store_out(a.out + at_out * D + ch, o, l);
-                } else {
-                    const int64_t to = slot * RB + t * 16 + row;
-                    *reinterpret_cast<f32x4 *>(a.part + to * D + ch) = o;
-                    if (ch == 0) {
-                        a.stats[to * 2] = mm;
-                        a.stats[to * 2 + 1] = l;
-                    }
-                }
-            }
-            __syncthreads();
-        }
-        place = 1;
-    }
-    if (!a.whole && h == 0 && threadIdx.x == 0) {
-        int32_t *n = a.notes + worker * 4;
-        n[0] = note_row;
-        n[1] = note_rows;
-        n[2] = note_parts;
-        n[3] = note_place;
-    }
-}
-
-// Many row blocks with few tokens each: a wave takes one to itself, so nothing is
-// joined and no wave waits for another.  Row block `item` of a kv head is found without
-// a pass over the sequences: sequence b's numbers begin at rows_before(b) / RB + b, which
-// leaves each of them room enough.
-template <int D, int QT, typename A>
-__device__ __forceinline__ void attend_wave(const A &a)
-{
-    constexpr int DT = D / 16, RB = 16 * QT;
-    const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
-    const int h = blockIdx.x % a.cache.n_kv, item = blockIdx.x / a.cache.n_kv;
-    auto number = [&](int b) {
-        const int before = min(max(a.batch.cu_q[b], 0), (int)a.batch.tokens);
-        return (int64_t)before * a.group / RB + b;
-    };
-    int b = 0;                                               // the last sequence that begins at or before `item`
-    for (int many = a.batch.batch; many > 0;) {
-        const int step = (many + 63) / 64, p = lane * step;
-        const int n = __popcll(__ballot(p < many && number(b + p) <= item));
-        if (n == 0) return;                                  // before the first one: padding
-        b += (n - 1) * step;
-        many = step > 1 ? min(step, many - (n - 1) * step) : 0;
-    }
-    const KvSeq seq = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
-    const int rows = seq.n * a.group, rb = item - (int)number(b);
-    if (rb < 0 || rb * RB >= rows) return;
-    const int skip = skipped(a, seq, b);
-    const Tiles tiles = visible_tiles(a, seq, skip);
-    Wave<D, QT> s;
-    begin(s, a, seq, h, rb);
-    attend_tiles<1>(s, a, seq, b, h, tiles, 0, tiles.count, seq.ctx + rb * RB / a.group,
-                    seq.ctx + (min(rb * RB + RB, rows) - 1) / a.group);
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const int r = rb * RB + t * 16 + m16, tok = r / a.group;
-        float l = column_sum(s.l[t]);
-        if (r >= rows) continue;
-        const int64_t at_out = (int64_t)(seq.q0 + tok) * a.n_q + h * a.group + r - tok * a.group;
-        uint16_t *to = a.out + at_out * D + g * 4;
-        if constexpr (A::kShared) {
-            if (skip > 0) {
-                const Shared shared(a, at_out, s.m[t], l);
-#pragma unroll
-                for (int d = 0; d < DT; ++d) s.o[t][d] = shared.add(a, at_out, D, d * 16 + g * 4, s.o[t][d]);
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < DT; ++d) store_out(to + d * 16, s.o[t][d], l);
-    }
-}
-
-// Joins the parts of a row block that several workers shared: a workgroup per
-// row, D / 4 lanes side by side, the parts dealt out to its NW waves and to as
-// many places in a wave as there is room for.  Bound by latency (a note, then the
-// parts, eight at a time): 3 to 5 us.
-template <int D, int QT, int NW, typename A>
-__device__ __forceinline__ void join_parts(const A &a)
-{
-    constexpr int RB = 16 * QT, PER = D / 4, SIDE = 64 / PER;
-    __shared__ float wave_m[NW], wave_l[NW];
-    __shared__ f32x4 wave_o[NW][PER];
-    const int row = blockIdx.x % RB, h = blockIdx.x / RB % a.cache.n_kv, worker = blockIdx.x / RB / a.cache.n_kv;
-    const int32_t *n = a.notes + worker * 4;
-    const int parts = n[2];
-    if (row >= n[1] || parts == 0) return;
-    const int r = n[0] + row, tok = r / a.group, hq = h * a.group + r - tok * a.group, place = n[3] & 1;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ch = lane % PER * 4;
-    auto slot = [&](int p) {
-        return (((int64_t)(worker + p) * 2 + (p == 0 ? place : 0)) * a.cache.n_kv + h) * RB + row;
-    };
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float m = kNone, l = 0.0f;
-    if (lane < PER * SIDE) {
-        // eight parts on their way at a time, each group against its own maximum
-        for (int p0 = wave * SIDE + lane / PER; p0 < parts; p0 += 8 * NW * SIDE) {
-            f32x4 x[8];
-            float pm[8], pl[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int p = p0 + i * NW * SIDE;
-                pm[i] = kNone;
-                pl[i] = 0.0f;
-                x[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (p < parts) {
-                    const int64_t s = slot(p);
-                    pm[i] = a.stats[s * 2];
-                    pl[i] = a.stats[s * 2 + 1];
-                    x[i] = *reinterpret_cast<const f32x4 *>(a.part + s * D + ch);
-                }
-            }
-            float top = m;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, pm[i]);
-            const float keep = __builtin_amdgcn_exp2f(m - top);
-            o *= keep;
-            l *= keep;
-            m = top;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = __builtin_amdgcn_exp2f(pm[i] - m);
-                o += x[i] * f;
-                l += pl[i] * f;
-            }
-        }
-    }
-    // the places of a wave, then the waves
-    float top = m;
-#pragma unroll
-    for (int i = 1; i < SIDE; ++i) top = fmaxf(top, __shfl(m, (lane % PER) + i * PER));
-    top = fmaxf(top, __shfl(m, lane % PER));
-    const float f = __builtin_amdgcn_exp2f(m - top);
-    o *= f;
-    l *= f;
-    f32x4 sum = o;
-    float sum_l = l;
-#pragma unroll
-    for (int i = 1; i < SIDE; ++i) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] += __shfl(o[e], lane + i * PER);
-        sum_l += __shfl(l, lane + i * PER);
-    }
-    if (lane < PER) {
-        wave_o[wave][lane] = sum;
-        if (lane == 0) {
-            wave_m[wave] = top;
-            wave_l[wave] = sum_l;
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x >= PER) return;
-    top = kNone;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) top = fmaxf(top, wave_m[v]);
-    sum = f32x4{0.f, 0.f, 0.f, 0.f};
-    sum_l = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) {
-        const float w = __builtin_amdgcn_exp2f(wave_m[v] - top);
-        sum += wave_o[v][lane] * w;
-        sum_l += wave_l[v] * w;
-    }
-    const int64_t at_out = (int64_t)tok * a.n_q + hq;
-    if constexpr (A::kShared) {
-        if (n[3] & 2) sum = Shared(a, at_out, top, sum_l).add(a, at_out, D, ch, sum);
-    }
-    store_out(a.out + at_out * D + ch, sum, sum_l);
-}
-
-// The rows of group g's sequences, which lie side by side.
-__device__ __forceinline__ void group_range(const SharedArgs &a, int g, int &lo, int &hi, int &q0, int &n)
-{
-    lo = min(max(a.cu_seqs[g], 0), a.batch.batch);
-    hi = min(max(a.cu_seqs[g + 1], lo), a.batch.batch);
-    const int T = (int)a.batch.tokens;
-    q0 = min(max(a.batch.cu_q[lo], 0), T);
-    n = max(min(a.batch.cu_q[hi], T) - q0, 0);
-}
-
-// The row blocks of RB rows of all groups, numbered: block `item`'s group and its place there.
+// Row block `item` of RB rows, counted through all groups: the rows of its group's sequences, which lie side
+// by side, as one sequence that sees all of the shared pages, the block's place there, and `b`, which
+// has the pages in its block table: the group's first sequence that has finished them.  Every thread of the
+// workgroup calls this.  False if there are not that many blocks, or no such sequence.
 template <int RB>
-__device__ __forceinline__ bool locate_group(const SharedArgs &a, int64_t item, int &g, int64_t &rb)
+__device__ __forceinline__ bool group_rows(const SharedArgs &a, int64_t item, KvSeq &seq, int &b, int64_t &rb)
 {
-    return kv_locate(a.groups, item, [&](int i) {
-        int lo, hi, q0, n;
-        group_range(a, i, lo, hi, q0, n);
-        return ((int64_t)n * a.group + RB - 1) / RB;
-    }, g, rb);
-}
-
-// A group's rows as one sequence that sees all of its shared pages: `b` has their block table.
-// They are as many as the caller says and every sequence with rows has finished; every thread of
-// the workgroup calls this, one workgroup of each group notes the pages for its sequences.
-__device__ __forceinline__ KvSeq group_rows(const SharedArgs &a, int g, bool note, int &b)
-{
-    __shared__ int least, first;
-    int lo, hi, q0, n;
-    group_range(a, g, lo, hi, q0, n);
-    if (threadIdx.x == 0) {
-        least = min(min(max(a.pages[g], 0), a.max_pages), a.batch.table_cols);
-        first = hi;
-    }
-    __syncthreads();
-    int pages = INT_MAX, mine = INT_MAX;
-    for (int i = lo + threadIdx.x; i < hi; i += blockDim.x) {
-        const KvSeq s = kv_seq(a.batch, i, a.cache.slots, a.page_shift);
-        if (s.n > 0) {
-            pages = min(pages, s.ctx >> a.page_shift);
-            mine = min(mine, i);
+    __shared__ int first;
+    const int lane = threadIdx.x & 63, T = (int)a.batch.tokens;
+    int lo = 0, hi = 0, q0 = 0, n = 0, pages = 0;
+    int64_t base = 0;
+    bool found = false;
+    for (int c = 0; c < a.groups && !found; c += 64) {
+        int64_t blocks = 0;
+        const int g = min(c + lane, a.groups - 1);
+        lo = min(max(a.cu_seqs[g], 0), a.batch.batch);
+        hi = min(max(a.cu_seqs[g + 1], lo), a.batch.batch);
+        pages = a.pages_of(g);
+        q0 = min(max(a.batch.cu_q[lo], 0), T);
+        n = max(min(a.batch.cu_q[hi], T) - q0, 0);
+        if (c + lane < a.groups) blocks = ((int64_t)n * a.group + RB - 1) / RB;
+        const int64_t incl = kv_wave_scan(blocks);
+        const uint64_t hit = __ballot(item < base + incl);
+        if (hit) {
+            const int f = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+            rb = item - base - kv_lane(incl - blocks, f);
+            lo = __builtin_amdgcn_readlane(lo, f);
+            hi = __builtin_amdgcn_readlane(hi, f);
+            q0 = __builtin_amdgcn_readlane(q0, f);
+            n = __builtin_amdgcn_readlane(n, f);
+            pages = __builtin_amdgcn_readlane(pages, f);
+            found = true;
         }
+        base += kv_lane(incl, 63);
     }
-    if (mine != INT_MAX) {
-        atomicMin(&least, pages);
-        atomicMin(&first, mine);
-    }
+    if (!found || pages == 0) return false;
+    if (threadIdx.x == 0) first = hi;
     __syncthreads();
-    const int tiles = first < hi ? __builtin_amdgcn_readfirstlane(least) << (a.page_shift - 6) : 0;
+    for (int i0 = lo; i0 < hi; i0 += blockDim.x) {
+        const int i = i0 + threadIdx.x;
+        bool has = false;
+        if (i < hi) {
+            const KvSeq s = kv_seq(a.batch, i, a.cache.slots, a.page_shift);
+            has = s.n > 0 && s.ctx >> a.page_shift >= pages;
+        }
+        if (has) atomicMin(&first, i);
+        if (__syncthreads_or(has)) break;
+    }
     b = __builtin_amdgcn_readfirstlane(first);
-    if (note)
-        for (int i = lo + threadIdx.x; i < hi; i += blockDim.x) a.skips[i] = tiles;
-    return {q0, n, tiles * kTile - n, 0};
-}
-
-// Sequences that no group names share nothing; the first workgroup notes that.
-__device__ __forceinline__ void note_others(const SharedArgs &a)
-{
-    if (blockIdx.x != 0) return;
-    const int B = a.batch.batch, lo = min(max(a.cu_seqs[0], 0), B), hi = min(max(a.cu_seqs[a.groups], lo), B);
-    for (int i = threadIdx.x; i < B; i += blockDim.x)
-        if (i < lo || i >= hi) a.skips[i] = 0;
+    seq = {q0, n, (pages << a.page_shift) - n, 0};
+    return b < hi;
 }
 
 // Many rows of a sequence: a workgroup of NW waves holds 16 QT NW rows (a wave QT
@@ -906,8 +553,10 @@ __device__ __forceinline__ void note_others(const SharedArgs &a)
 // the two that share a SIMD take turns: waves 4 .. 7 run half a tile behind, and
 // each barrier hands the matrix cores to the other wave.  With few row blocks the tiles
 // are cut into `splits` runs and joined by kv_join_rows_kernel.
+// (kv_attend_rows_kernel.  With PARTS the rows are a group's, on its shared pages, and all of them
+// go out as parts: workgroup `block` of `blocks`.)
 template <int D, int NW, int QT, bool PARTS, typename A>
-__device__ __forceinline__ void attend_rows(const A &a, int splits)
+__device__ __forceinline__ void attend_rows(const A &a, int splits, int block, int blocks)
 {
     constexpr int DT = D / 16, KS = (D + 63) / 64, RB = 16 * QT * NW, THREADS = 64 * NW;
     constexpr int UNITS = 4 * D, UN = (UNITS + THREADS - 1) / THREADS;     // 16-byte units of a tile's K (and V)
@@ -917,18 +566,15 @@ __device__ __forceinline__ void attend_rows(const A &a, int splits)
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);                  // a scalar: its branches are uniform
     const int n_kv = a.cache.n_kv, page = 1 << a.page_shift, head = page * D;
-    const int h = blockIdx.x % n_kv, split = blockIdx.x / n_kv % splits;
+    const int h = block % n_kv, split = block / n_kv % splits;
     int b;
     int64_t rb64;
     // the last row blocks, which see the most tokens, first: the short ones fill the gaps
     // at the end (2048 queries on an empty cache: 89 us, 108 in the other order)
-    const int64_t item = (int64_t)(gridDim.x - 1 - blockIdx.x) / n_kv / splits;
+    const int64_t item = (int64_t)(blocks - 1 - block) / n_kv / splits;
     KvSeq seq;
     if constexpr (PARTS) {
-        note_others(a);
-        int group;
-        if (!locate_group<RB>(a, item, group, rb64)) return;
-        seq = group_rows(a, group, h == 0 && split == 0 && rb64 == 0, b);
+        if (!group_rows<RB>(a, item, seq, b, rb64)) return;
     } else {
         if (!kv_locate(a.batch.batch, item, [&](int i) {
                 return (int64_t)((kv_seq(a.batch, i, a.cache.slots, a.page_shift).n * a.group + RB - 1) / RB);
@@ -937,11 +583,9 @@ __device__ __forceinline__ void attend_rows(const A &a, int splits)
         seq = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
     }
     const int rows = seq.n * a.group, row0 = (int)rb64 * RB, full = seq.total() >> a.page_shift << a.page_shift;
-    const int skip = PARTS ? 0 : skipped(a, seq, b);
     Tiles tiles = {0, 0, full / kTile};
     if constexpr (!PARTS)
-        tiles = visible_tiles(a, seq.ctx + row0 / a.group, seq.ctx + (min(row0 + RB, rows) - 1) / a.group, skip);
-    else if (tiles.count == 0) return;
+        tiles = visible_tiles(a, seq.ctx + row0 / a.group, seq.ctx + (min(row0 + RB, rows) - 1) / a.group);
     const int t0 = (int)((int64_t)tiles.count * split / splits), t1 = (int)((int64_t)tiles.count * (split + 1) / splits);
 
     // this wave's rows
@@ -1214,145 +858,24 @@ __device__ __forceinline__ void attend_rows(const A &a, int splits)
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int r = first + t * 16 + m16;
-        float sum = column_sum(l[t]);
+        const float sum = column_sum(l[t]);
         if (r >= rows) continue;
         const int tok = r / a.group;
         const int64_t at_out = (int64_t)(seq.q0 + tok) * a.n_q + h * a.group + r - tok * a.group;
         if (!PARTS && splits == 1) {
-            if constexpr (A::kShared) {
-                if (skip > 0) {
-                    const Shared shared(a, at_out, m[t], sum);
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) o[t][d] = shared.add(a, at_out, D, d * 16 + g * 4, o[t][d]);
-                }
-            }
 #pragma unroll
             for (int d = 0; d < DT; ++d) store_out(a.out + at_out * D + d * 16 + g * 4, o[t][d], sum);
         } else {
-            float *part = a.part, *stats = a.stats;
-            if constexpr (PARTS) {
-                part = a.pre_part;
-                stats = a.pre_stats;
-            }
-            const int64_t slot = at_out * splits + split;
+            int64_t slot = at_out * splits + split;
+            if constexpr (PARTS) slot = at_out * a.places() + split;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(part + slot * D + d * 16 + g * 4) = o[t][d];
+            for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(a.part + slot * D + d * 16 + g * 4) = o[t][d];
             if (g == 0) {
-                stats[slot * 2] = m[t];
-                stats[slot * 2 + 1] = sum;
+                a.stats[slot * 2] = m[t];
+                a.stats[slot * 2 + 1] = sum;
             }
         }
     }
-}
-
-// Joins the `splits` parts of every row of the batch's sequences: D / 4 threads a row,
-// four channels each, bound by the parts' way in (512 queries of 64 heads, two cuts of
-// d = 128: 9.3 us).
-template <int D, typename A>
-__device__ __forceinline__ void join_rows(const A &a, int splits)
-{
-    constexpr int PER = D / 4;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, row = i / PER;
-    const int ch = (int)(i - row * PER) * 4;
-    if (row >= a.batch.tokens * a.n_q) return;
-    const int tok = (int)(row / a.n_q);
-    // a row of no sequence, or of one that was skipped, is left as it was
-    int lo = 0, hi = a.batch.batch;                        // the last sequence that starts at or before the row
-    while (lo + 1 < hi) {
-        const int mid = (lo + hi) / 2;
-        if (a.batch.cu_q[mid] <= tok) lo = mid; else hi = mid;
-    }
-    const KvSeq s = kv_seq(a.batch, lo, a.cache.slots, a.page_shift);
-    if (tok < s.q0 || tok >= s.q0 + s.n) return;
-    float m = kNone;
-    for (int p = 0; p < splits; ++p) m = fmaxf(m, a.stats[(row * splits + p) * 2]);
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.0f;
-    for (int p = 0; p < splits; ++p) {
-        const float f = __builtin_amdgcn_exp2f(a.stats[(row * splits + p) * 2] - m);
-        l += a.stats[(row * splits + p) * 2 + 1] * f;
-        o += *reinterpret_cast<const f32x4 *>(a.part + (row * splits + p) * D + ch) * f;
-    }
-    if constexpr (A::kShared) {
-        if (skipped(a, s, lo) > 0) o = Shared(a, row, m, l).add(a, row, D, ch, o);
-    }
-    store_out(a.out + row * D + ch, o, l);
-}
-
-// Waves per SIMD that the split kernel's registers allow (three would fit for d = 64 and
-// one block of rows, but take longer: 32 ragged sequences of 8000 tokens 34.8 us, 37.2).
-constexpr int split_occupancy(int d, int qt) { return (d <= 64 && qt <= 2) || (d <= 128 && qt == 1) ? 2 : 1; }
-
-// How a call is run.  qt > 0: the split kernel with qt blocks of 16 rows, as many
-// as an average sequence fills.  qt == 0: the rows kernel with `waves` waves and
-// `splits` runs of tiles.
-struct Plan {
-    int qt, waves, splits, workers;
-    int alone;                   // waves that have a row block to themselves, 0: none, workers' runs share them
-    int64_t items, parts;        // row blocks of the rows kernel (an upper bound); rows of workspace, whatever the lengths
-};
-
-// Sequences have about `most` tokens at most, and a row sees at most `span` of them.
-Plan plan_for(int64_t tokens, int batch, int n_q, int n_kv, int d, int64_t most, int64_t span)
-{
-    Plan p = {};
-    const int64_t group = n_q / n_kv, rows = (tokens + batch - 1) / batch * group;
-    // the rows kernel with these would be half idle (8 x 5 rows of 8 query heads on 4000
-    // tokens: 40 us, 42 in the rows kernel; 3 rows 32 and 43; d = 64 with 20 rows on 8000 29 and 42)
-    if (rows <= (d <= 128 ? 48 : 16)) {
-        p.qt = (int)(rows + 15) / 16;
-        const int groups = 256 * split_occupancy(d, p.qt);       // workgroups that the 256 CUs hold at once
-        p.workers = n_kv < groups ? (groups + n_kv - 1) / n_kv : 1;
-        p.parts = (int64_t)p.workers * n_kv * 2 * 16 * p.qt;
-        // Where rows see few tokens, a row block is left whole, which saves the second launch:
-        // a workgroup for each or, with many, a wave.  By what each costs (us; a round is what
-        // the CUs hold): 32 heads and 500 tokens, cut, a workgroup, a wave: 10.4, 9.1, 15.7;
-        // 1000 tokens 10.6, 12.4; 64 x 250 tokens on average, 8 kv heads 21.3, 11.6, 13.6;
-        // 256 x 250 49.6, 47.5, 26.7; 1024 x 250 216, 335, 122; 128 x 1000 46, 42, 48.
-        // Only up to 32 tiles: the host sees no more than what the table holds, and one long
-        // sequence among short ones would keep its wave busy alone.
-        const int rb = 16 * p.qt;
-        const double all = (double)((rows + rb - 1) / rb * batch * n_kv) / groups;           // in rounds
-        const double tiles = (double)std::min(most, span + rb / group + 2 * kTile) / kTile;
-        const double tile = split_occupancy(d, p.qt) == 2 ? 0.45 : 0.8;
-        const double cut = 9.5 + tile * std::max((tiles + kStart) * all, (double)kWaves);
-        const double group4 = std::max(all, 1.0) * (6.0 + tile * tiles);
-        const double one = std::max(all / 4, 1.0) * (6.0 + 4 * tile * tiles);
-        if (tiles <= 32 && std::min(group4, one) < cut) {
-            p.alone = one < group4 ? 1 : kWaves;
-            p.workers = (int)(tokens * group / rb + batch);
-        }
-        return p;
-    }
-    // Waves and cuts by what they cost: a workgroup takes 8 us and 2 a tile, one of four
-    // waves 2.3 where two share a CU and 1.3 alone; cuts cost a second launch and the
-    // parts' way out and back at 4 TB/s.  (64 query heads on 8, four against eight waves:
-    // 512 queries on 8k tokens 157 and 139 us, 2048 on 6144 467 and 410, 512 on none 20.7
-    // and 25.5, 32 x 40 on 2000 124 and 130.  Cuts: 512 on 8k uncut 310, in
-    // two 159; 2 x 1500 in a window of 1024, d = 256, 102 and 120; 32 x 8 on 2k 52 and 62.)
-    // No more than four rounds of cut ones: the parts, at most 2^18 rows, stay small (16
-    // cuts of 100000 rows of 64 heads would be 53 GB), and an uneven end among more
-    // rounds costs little.
-    double best = 0.0;
-    for (int waves = d == 256 ? 8 : 4; waves <= 8; waves += 4) {
-        const int64_t rb = (d == 256 ? 16 : 32) * waves, places = waves == 4 ? 512 : 256;
-        const int64_t groups = (rows + rb - 1) / rb * batch * n_kv;
-        const double tiles = (double)std::min(most, span + rb / group + 2 * kTile) / kTile;
-        for (int cuts = 1; cuts <= 16 && (cuts == 1 || groups * cuts <= 4 * places); ++cuts) {
-            const int64_t full = groups * cuts / places, rest = groups * cuts % places;
-            const double pair = waves == 4 ? 2.3 : 2.0, last = waves == 4 && rest <= 256 ? 1.3 : pair;
-            const double run = tiles / cuts, cost = (double)full * (8.0 + run * pair) + (rest ? 8.0 + run * last : 0.0) +
-                (cuts > 1 ? 5.0 + (double)(tokens * n_q) * cuts * d * 8 / 4e6 : 0.0);
-            if (p.waves == 0 || cost < best) {
-                best = cost;
-                p.waves = waves;
-                p.splits = cuts;
-            }
-            if (cuts > 1) p.parts = std::max(p.parts, tokens * n_q * cuts);
-        }
-    }
-    p.items = tokens * group / ((d == 256 ? 16 : 32) * p.waves) + batch;
-    return p;
 }
 
 // Where a call goes: to a stream, or with `name` nowhere, and the kernels that would have
@@ -1366,17 +889,6 @@ struct Target {
     {
         snprintf(name, (size_t)name_len, format, values...);
         return hipSuccess;
-    }
-    // What is reported next comes behind what has been.
-    void go_on()
-    {
-        if (!name) return;
-        for (const char *c = ", "; *name || *c; ++name, --name_len) {
-            if (*name) continue;
-            if (name_len <= 1) return;
-            *name = *c++;
-            name[1] = 0;
-        }
     }
 };
 

@@ -1,149 +1,276 @@
 // kv_shared.hip -- attention over the paged INT8 cache for sequences that share their first
-// pages (kv_codec.h): the shared pages' parts of every row, then every sequence's own tokens.
+// pages (kv_codec.h).
+//
+// Mathematics.  A row's softmax over two sets of tokens is joined from a part for each: with (O, m, l) as in
+// kv_attend.h, top = max(m_1, m_2), o = (O_1 2^(m_1 - top) + O_2 2^(m_2 - top)) / (l_1 2^(m_1 - top) + l_2 2^(m_2 - top)).
+// All rows of a group of sequences are rows of one matrix product with the shared pages, which are so
+// read once; what each sequence has of its own is read by its own rows.
 #include "kv_attend.h"
 
 namespace {
 
-// The parts of the shared pages where a group has few rows: a workgroup has a block of 16 QT
-// rows of a kv head and one of `pre_splits` runs of the tiles, which its waves take in turn.
-template <int D, int QT, int OCC>
-__global__ __launch_bounds__(kThreads, OCC) void kv_shared_split_kernel(SharedArgs a)
+// Four channels of a row's part.
+template <int D>
+__device__ __forceinline__ void put_part(const SharedArgs &a, int64_t row, int place, int ch, f32x4 o, float m, float l)
 {
-    constexpr int DT = D / 16, RB = 16 * QT, PAD = D + 4, PER = D / 4;
-    __shared__ float joint[kWaves][16 * PAD], stat_m[kWaves][RB], stat_l[kWaves][RB];
-    const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int h = blockIdx.x % a.cache.n_kv, split = blockIdx.x / a.cache.n_kv % a.pre_splits;
-    note_others(a);
-    int group, b;
-    int64_t rb;
-    if (!locate_group<RB>(a, blockIdx.x / a.cache.n_kv / a.pre_splits, group, rb)) return;
-    const KvSeq seq = group_rows(a, group, h == 0 && split == 0 && rb == 0, b);
-    const int rows = seq.n * a.group, row0 = (int)rb * RB;
-    const Tiles tiles = {0, 0, seq.total() / kTile};
-    if (tiles.count == 0) return;
-    const int t0 = (int)((int64_t)tiles.count * split / a.pre_splits), t1 = (int)((int64_t)tiles.count * (split + 1) / a.pre_splits);
-    Wave<D, QT> s;
-    begin(s, a, seq, h, (int)rb);
-    attend_tiles<kWaves>(s, a, seq, b, h, tiles, t0 + wave, t1, 1 << 30, 1 << 30);
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        const float l = column_sum(s.l[t]);
-        if (g == 0) {
-            stat_m[wave][t * 16 + m16] = s.m[t];
-            stat_l[wave][t * 16 + m16] = l;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < QT; ++t) {
-        float top = kNone;
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) top = fmaxf(top, stat_m[v][t * 16 + m16]);
-        const float f = __builtin_amdgcn_exp2f(s.m[t] - top);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-            *reinterpret_cast<f32x4 *>(&joint[wave][m16 * PAD + d * 16 + g * 4]) = s.o[t][d] * f;
-        __syncthreads();
-        for (int i = threadIdx.x; i < 16 * PER; i += kThreads) {
-            const int row = i / PER, ch = i % PER * 4, r = row0 + t * 16 + row;
-            if (r >= rows) continue;
-            f32x4 o = {0.f, 0.f, 0.f, 0.f};
-            float m = kNone, l = 0.0f;
-#pragma unroll
-            for (int v = 0; v < kWaves; ++v) {
-                o += *reinterpret_cast<const f32x4 *>(&joint[v][row * PAD + ch]);
-                m = fmaxf(m, stat_m[v][t * 16 + row]);
-            }
-#pragma unroll
-            for (int v = 0; v < kWaves; ++v)
-                l += stat_l[v][t * 16 + row] * __builtin_amdgcn_exp2f(stat_m[v][t * 16 + row] - m);
-            const int tok = r / a.group;
-            const int64_t to = ((int64_t)(seq.q0 + tok) * a.n_q + h * a.group + r - tok * a.group) * a.pre_splits + split;
-            *reinterpret_cast<f32x4 *>(a.pre_part + to * D + ch) = o;
-            if (ch == 0) {
-                a.pre_stats[to * 2] = m;
-                a.pre_stats[to * 2 + 1] = l;
-            }
-        }
-        __syncthreads();
+    const int64_t to = row * a.places() + place;
+    *reinterpret_cast<f32x4 *>(a.part + to * D + ch) = o;
+    if (ch == 0) {
+        a.stats[to * 2] = m;
+        a.stats[to * 2 + 1] = l;
     }
 }
 
-// The parts of the shared pages where a group has many rows.
+// Bytes of LDS for put_rows.
+constexpr int joint_lds(int d) { return (kWaves * 16 * (d + 4) + 2 * kWaves * 16) * 4; }
+
+// 16 rows, whose tiles `share` waves side by side (1, 2 or 4) took in turn, as one part of each.
+// Every thread of the workgroup calls this; those with nothing are not `live`.
+template <int D, typename F>
+__device__ __forceinline__ void put_rows(const SharedArgs &a, Wave<D, 1> &s, float *smem, int share, bool live, int many,
+                                         int place, F row_of)
+{
+    constexpr int DT = D / 16, PAD = D + 4, PER = D / 4;
+    const int lane = threadIdx.x & 63, g = lane >> 4, m16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), turn = wave % share, lead = wave - turn;
+    float *joint = smem, *stat_m = smem + kWaves * 16 * PAD, *stat_l = stat_m + kWaves * 16;
+    if (live) s.l[0] = column_sum(s.l[0]);
+    if (share == 1) {
+        if (!live || m16 >= many) return;
+        const int64_t row = row_of(m16);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) put_part<D>(a, row, place, d * 16 + g * 4, s.o[0][d], s.m[0], s.l[0]);
+        return;
+    }
+    if (live && g == 0) {
+        stat_m[wave * 16 + m16] = s.m[0];
+        stat_l[wave * 16 + m16] = s.l[0];
+    }
+    __syncthreads();
+    if (live) {
+        float top = kNone;
+        for (int v = 0; v < share; ++v) top = fmaxf(top, stat_m[(lead + v) * 16 + m16]);
+        const float f = __builtin_amdgcn_exp2f(s.m[0] - top);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+            *reinterpret_cast<f32x4 *>(&joint[(wave * 16 + m16) * PAD + d * 16 + g * 4]) = s.o[0][d] * f;
+    }
+    __syncthreads();
+    if (!live) return;
+    for (int i = turn * 64 + lane; i < 16 * PER; i += 64 * share) {
+        const int row = i / PER, ch = i % PER * 4;
+        if (row >= many) continue;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        float m = kNone, l = 0.0f;
+        for (int v = lead; v < lead + share; ++v) {
+            o += *reinterpret_cast<const f32x4 *>(&joint[(v * 16 + row) * PAD + ch]);
+            m = fmaxf(m, stat_m[v * 16 + row]);
+        }
+        for (int v = lead; v < lead + share; ++v) l += stat_l[v * 16 + row] * __builtin_amdgcn_exp2f(stat_m[v * 16 + row] - m);
+        put_part<D>(a, row_of(row), place, ch, o, m, l);
+    }
+}
+
+// The parts of the shared pages, 16 rows of a group and kv head a workgroup, and one of `splits` runs
+// of the tiles, which its waves take in turn from memory (attend_rows: 128 or 256 rows, tiles by way of LDS).
+template <int D>
+__device__ __forceinline__ void shared_rows(const SharedArgs &a, float *smem, int block)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h = block % a.cache.n_kv, split = block / a.cache.n_kv % a.splits;
+    int b;
+    int64_t rb;
+    KvSeq seq;
+    if (!group_rows<16>(a, block / a.cache.n_kv / a.splits, seq, b, rb)) return;
+    const Tiles tiles = {0, 0, seq.total() / kTile};
+    const int t0 = (int)((int64_t)tiles.count * split / a.splits), t1 = (int)((int64_t)tiles.count * (split + 1) / a.splits);
+    Wave<D, 1> s;
+    begin(s, a, seq, h, (int)rb);
+    attend_tiles<kWaves>(s, a, seq, b, h, tiles, t0 + wave, t1, 1 << 30, 1 << 30);
+    const int row0 = (int)rb * 16;
+    put_rows(a, s, smem, kWaves, true, seq.n * a.group - row0, split, [&](int row) {
+        const int tok = (row0 + row) / a.group;
+        return (int64_t)(seq.q0 + tok) * a.n_q + h * a.group + row0 + row - tok * a.group;
+    });
+}
+
+// A sequence's own tokens, 16 of its rows of a kv head and a run of `chunk` tiles (the last run: all that are
+// left) at a time; `share` waves of a workgroup take a run's tiles in turn, so that a workgroup has 4 / share runs.
+// Row block `item` of a kv head is found without a pass over the sequences: sequence b's numbers begin
+// at rows_before(b) / 16 + b, which leaves each of them room enough.
+template <int D>
+__device__ __forceinline__ void own_rows(const SharedArgs &a, float *smem, int block, int per_chunk, int share)
+{
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), turn = wave % share;
+    const int chunk = block / per_chunk, unit = (block - chunk * per_chunk) * (kWaves / share) + wave / share;
+    const int h = unit % a.cache.n_kv, item = unit / a.cache.n_kv;
+    const SharedArgs::Named all = a.named();
+    auto number = [&](int before, int b) { return (int64_t)min(max(before, 0), (int)a.batch.tokens) * a.group / 16 + b; };
+    int b = 0, many = a.batch.batch;                         // the last sequence that begins at or before `item`
+    while (many > 64) {
+        const int step = (many + 63) / 64, p = lane * step;
+        const int n = __popcll(__ballot(p < many && number(a.batch.cu_q[b + p], b + p) <= item));
+        b += max(n - 1, 0) * step;
+        many = min(step, many - max(n - 1, 0) * step);
+    }
+    const int mine = b + min(lane, many - 1), from = a.batch.cu_q[mine];
+    const KvSeq s64 = kv_seq(a.batch, mine, a.cache.slots, a.page_shift);
+    const int before = __popcll(__ballot(lane < many && number(from, mine) <= item)), f = max(before - 1, 0);
+    b += f;
+    const KvSeq seq = {__builtin_amdgcn_readlane(s64.q0, f), __builtin_amdgcn_readlane(s64.n, f),
+                       __builtin_amdgcn_readlane(s64.ctx, f), __builtin_amdgcn_readlane(s64.slot, f)};
+    const int rows = seq.n * a.group, rb = item - (int)number(__builtin_amdgcn_readlane(from, f), b);
+    const Tiles tiles = visible_tiles(a, seq, a.skip(seq, b, all));
+    const int t0 = chunk * a.chunk, t1 = chunk + 1 < a.chunks ? min(t0 + a.chunk, tiles.count) : tiles.count;
+    // of a sequence, not between two; and the run is not empty
+    const bool live = before > 0 && rb >= 0 && rb < (rows + 15) / 16 && t0 < tiles.count;
+    Wave<D, 1> s;
+    if (live) {
+        const int at_min = seq.ctx + rb * 16 / a.group, at_max = seq.ctx + (min(rb * 16 + 16, rows) - 1) / a.group;
+        begin(s, a, seq, h, rb);
+        if (share == 4) attend_tiles<4>(s, a, seq, b, h, tiles, t0 + turn, t1, at_min, at_max);
+        else if (share == 2) attend_tiles<2>(s, a, seq, b, h, tiles, t0 + turn, t1, at_min, at_max);
+        else attend_tiles<1>(s, a, seq, b, h, tiles, t0, t1, at_min, at_max);
+    }
+    put_rows(a, s, smem, share, live, rows - rb * 16, a.splits + chunk, [&](int row) {
+        const int tok = (rb * 16 + row) / a.group;
+        return (int64_t)(seq.q0 + tok) * a.n_q + h * a.group + rb * 16 + row - tok * a.group;
+    });
+}
+
+// Shared pages and own tokens in one launch: the first `first` workgroups compute the shared pages' parts (MANY: 128
+// rows each, otherwise 16), bound by the matrix cores, and the others, bound by memory, run beside them.
+template <int D, bool MANY, int OCC>
+__global__ __launch_bounds__(kThreads, OCC) void kv_shared_kernel(SharedArgs a, int first, int per_chunk, int share)
+{
+    extern __shared__ __attribute__((aligned(16))) float shared_smem[];
+    const int block = blockIdx.x;
+    if (block < first) {
+        if constexpr (MANY) attend_rows<D, 4, 2, true>(a, a.splits, block, first);
+        else shared_rows<D>(a, shared_smem, block);
+    } else {
+        own_rows<D>(a, shared_smem, block - first, per_chunk, share);
+    }
+}
+
+// The shared pages alone, for d = 256: 128 rows take the LDS of a whole CU, and eight waves.
 template <int D, int NW, int QT>
 __global__ __launch_bounds__(64 * NW, 2) void kv_shared_rows_kernel(SharedArgs a)
 {
-    attend_rows<D, NW, QT, true>(a, a.pre_splits);
+    attend_rows<D, NW, QT, true>(a, a.splits, blockIdx.x, gridDim.x);
 }
 
-// The sequences' own tokens.
-template <int D, int QT, int OCC>
-__global__ __launch_bounds__(kThreads, OCC) void kv_own_split_kernel(SharedArgs a) { attend_split<D, QT>(a); }
-
-template <int D, int QT, int OCC>
-__global__ __launch_bounds__(64, OCC) void kv_own_wave_kernel(SharedArgs a) { attend_wave<D, QT>(a); }
-
-template <int D, int QT, int NW>
-__global__ __launch_bounds__(64 * NW) void kv_own_join_kernel(SharedArgs a) { join_parts<D, QT, NW>(a); }
-
-template <int D, int NW, int QT>
-__global__ __launch_bounds__(64 * NW, 2) void kv_own_rows_kernel(SharedArgs a, int splits)
-{
-    attend_rows<D, NW, QT, false>(a, splits);
-}
-
+// Joins each row's parts: D / 4 threads a row, four channels each, eight parts on their way.
+// A workgroup takes rows of one sequence, `per` workgroups a sequence.
 template <int D>
-__global__ __launch_bounds__(kThreads) void kv_own_join_rows_kernel(SharedArgs a, int splits) { join_rows<D>(a, splits); }
+__global__ __launch_bounds__(kThreads) void kv_shared_join_kernel(SharedArgs a, int per)
+{
+    constexpr int PER = D / 4, SIDE = kThreads / PER;
+    const int b = blockIdx.x / per, turn = blockIdx.x % per, ch = threadIdx.x % PER * 4;
+    const KvSeq seq = kv_seq(a.batch, b, a.cache.slots, a.page_shift);
+    if (threadIdx.x >= PER * SIDE || seq.n == 0) return;
+    const int skip = a.skip(seq, b, a.named()), count = visible_tiles(a, seq, skip).count;
+    const int p0 = skip > 0 ? 0 : a.splits, p1 = a.splits + min((count + a.chunk - 1) / a.chunk, a.chunks);
+    const int64_t end = (int64_t)(seq.q0 + seq.n) * a.n_q;
+    for (int64_t row = (int64_t)seq.q0 * a.n_q + turn * SIDE + threadIdx.x / PER; row < end; row += per * SIDE) {
+        const float *stats = a.stats + row * a.places() * 2;
+        const float *part = a.part + row * a.places() * D + ch;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        float m = kNone, l = 0.0f;
+        for (int p = p0; p < p1; p += 8) {
+            f32x4 x[8];
+            float pm[8], pl[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                pm[i] = kNone;
+                pl[i] = 0.0f;
+                x[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (p + i < p1) {
+                    pm[i] = stats[2 * (p + i)];
+                    pl[i] = stats[2 * (p + i) + 1];
+                    x[i] = *reinterpret_cast<const f32x4 *>(part + (int64_t)(p + i) * D);
+                }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, pm[i]);
+            const float keep = __builtin_amdgcn_exp2f(m - top);
+            o *= keep;
+            l *= keep;
+            m = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = __builtin_amdgcn_exp2f(pm[i] - m);
+                o += x[i] * f;
+                l += pl[i] * f;
+            }
+        }
+        store_out(a.out + row * D + ch, o, l);
+    }
+}
 
-// How the shared pages' parts are computed: qt > 0 by kv_shared_split_kernel, otherwise by kv_shared_rows_kernel with
-// `waves` waves; in `splits` runs of tiles.
+// How a call is run.
 struct SharedPlan {
-    int qt, waves, splits;
-    int64_t items;               // row blocks (an upper bound)
+    bool alone;                  // as without shared pages
+    int many;                    // rows of the shared pages' workgroups: 16, or 128 (d = 256: in a launch of their own)
+    int splits, chunks, chunk, share;
+    int64_t items, own;          // row blocks of the shared pages and of the own tokens (upper bounds)
 };
 
-// Groups have `rows` rows a kv head on average and share at most `tiles` tiles.
-SharedPlan shared_plan(int64_t tokens, int groups, int n_q, int n_kv, int d, int64_t tiles)
+// Groups share at most `tiles` tiles; sequences have at most `own` tiles besides.
+SharedPlan shared_plan(int64_t tokens, int batch, int groups, int n_q, int n_kv, int d, int64_t tiles, int64_t own)
 {
     SharedPlan p = {};
-    const int64_t group = n_q / n_kv, rows = (tokens + groups - 1) / groups * group;
+    const int64_t group = n_q / n_kv, rows = (tokens + groups - 1) / groups * group, one = (tokens + batch - 1) / batch * group;
+    // With many rows of its own a sequence is bound by the matrix rate whoever reads the pages (16 x 16 tokens behind 8k,
+    // 64 heads on 8: 101 us shared, 90 not; 32 x 32 behind 2k 106 and 78).
+    p.alone = one > 64;
+    if (p.alone) return p;
+    // Waves of a row block: more of them end a long sequence sooner, fewer need fewer workgroups, of which the CUs hold
+    // 512 (us with 1, 2 and 4: 64 heads on 8, 16 x 500 tokens behind 8k 34.6, 26.7, 22.9; 64 x 1000 behind 4k 55, 41,
+    // 42.6; 256 x 500 behind 8k 129, 125, 133; 128 x 300 behind four times 1k 32.5, 35.8, 40.7; d = 64, 40 x 5 tokens 28.9,
+    // 27.2, 22.7).
+    const int64_t blocks = (one + 15) / 16 * batch * n_kv;
+    p.share = blocks * d <= 50000 ? 4 : own <= 8 ? 1 : 2;
+    p.own = tokens * group / 16 + batch;
+    p.chunks = (int)std::min<int64_t>((own + 31) / 32, 8);
+    p.chunk = (int)((own + p.chunks - 1) / p.chunks);
+    const double beside = (double)(blocks * p.share / 4);
+    // What a choice costs: a start, a run of tiles, which takes longer the more workgroups share the card, a second round of
+    // workgroups, and the parts' way out and back.  (us with 1, 2, 4, 6, 8, 16 and 32 runs: 64 sequences behind 4k, 16
+    // rows a workgroup 50, 54, 63, 73, 82, 118, 199, 128 rows 115, 66, 42, 43, 48, 58, 76; 16 of 32 heads on 8 behind 8k 62, 38, 26,
+    // 23.5, 22.9, 31.5, 43.7 and 203, 110, 61, 47, 39, 29, 29.)
     double best = 0.0;
-    auto offer = [&](int qt, int waves, int64_t rb, int64_t slots, auto cost) {
-        const int64_t blocks = (rows + rb - 1) / rb * groups * n_kv;
-        for (int cuts = 1; cuts <= 64 && cuts <= tiles && (cuts == 1 || blocks * cuts <= 4 * slots); ++cuts) {
-            const double c = cost(blocks * cuts, (double)tiles / cuts) + (double)(tokens * n_q) * cuts * d * 8 / 4e6;
+    auto offer = [&](int rb, int64_t slots, double start, double alone, double full) {
+        const int64_t n_blocks = (rows + rb - 1) / rb * groups * n_kv;
+        for (int cuts = 1; cuts <= 64 && cuts <= tiles && (cuts == 1 || n_blocks * cuts <= 4 * slots); ++cuts) {
+            const double n = (double)(n_blocks * cuts), half = (double)slots / 2, run = (double)tiles / cuts;
+            const double tile = alone + (full - alone) * std::min(1.0, std::max(0.0, n / half - 1.0));
+            const double c = start + tile * (rb == 16 ? std::max(run, (double)kWaves) : run) * std::max(1.0, n / (double)slots) +
+                17.0 * std::max(0.0, (n + beside) / (0.9 * (double)slots) - 1.0) + (double)(tokens * n_q) * cuts * d * 8 / 2e6;
             if (p.splits == 0 || c < best) {
                 best = c;
-                p = {qt, waves, cuts, tokens * group / rb + groups};
+                p.many = rb;
+                p.splits = cuts;
+                p.items = std::max<int64_t>(tokens * group - groups, 0) / rb + groups;
             }
         }
     };
-    for (int qt = 1; qt <= (d <= 128 ? 3 : 1); ++qt) {
-        const int64_t slots = 256 * split_occupancy(d, qt);
-        const double tile = split_occupancy(d, qt) == 2 ? 0.45 : 0.8;
-        offer(qt, 0, 16 * qt, slots, [&](int64_t n, double run) {
-            return std::max(1.0, (double)n / slots) * (6.0 + tile * std::max(run, (double)kWaves));
-        });
-    }
-    for (int waves = d == 256 ? 8 : 4; waves <= 8; waves += 4) {
-        const int64_t places = waves == 4 ? 512 : 256;
-        offer(0, waves, (d == 256 ? 16 : 32) * waves, places, [&](int64_t n, double run) {
-            const int64_t full = n / places, rest = n % places;
-            const double pair = waves == 4 ? 2.3 : 2.0, last = waves == 4 && rest <= 256 ? 1.3 : pair;
-            return (double)full * (8.0 + run * pair) + (rest ? 8.0 + run * last : 0.0);
-        });
-    }
+    const double size = (double)d / 128;
+    offer(16, d <= 128 ? 512 : 256, 8.0, 0.1 + 0.23 * size, 0.1 + 0.75 * size);
+    if (d <= 128) offer(128, 512, 8.0, 1.48, 2.3);
+    else offer(128, 256, 14.0, 2.0, 2.0);                              // in a launch of its own
     return p;
 }
 
-template <int D, int QT>
-hipError_t launch_shared_split(const SharedArgs &a, const SharedPlan &p, const Target &to)
+// The parts of a row.
+int places(const SharedPlan &p) { return p.splits + p.chunks; }
+
+// Tiles that the table has room for behind the shared pages, which stand for the sequences' own tokens.
+int64_t own_tiles(int64_t table_cols, int64_t max_pages, int64_t page)
 {
-    constexpr int OCC = split_occupancy(D, QT);
-    if (to.name) return to.report("kv_shared_split_kernel<%d, %d, %d>, %d cuts", D, QT, OCC, p.splits);
-    kv_shared_split_kernel<D, QT, OCC><<<(unsigned)(p.items * a.cache.n_kv * p.splits), kThreads, 0, to.stream>>>(a);
-    return hipGetLastError();
+    return std::max<int64_t>(table_cols - max_pages, 1) * page / kTile;
 }
 
 constexpr int rows_lds(int d) { return 2 * (8 * ((d + 63) / 64) + d / 8) * 1024; }
@@ -155,120 +282,87 @@ hipError_t allow_lds(K kernel, int bytes)
     return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int D, int NW, int QT>
-hipError_t launch_shared_rows(const SharedArgs &a, const SharedPlan &p, const Target &to)
+template <int D, bool MANY>
+hipError_t launch_kernel(const SharedArgs &a, const SharedPlan &p, int64_t first, const Target &to)
 {
-    if (to.name) return to.report("kv_shared_rows_kernel<%d, %d, %d>, %d cuts", D, NW, QT, p.splits);
-    auto kernel = kv_shared_rows_kernel<D, NW, QT>;
-    if (hipError_t e = allow_lds(kernel, rows_lds(D))) return e;
-    kernel<<<(unsigned)(p.items * a.cache.n_kv * p.splits), 64 * NW, rows_lds(D), to.stream>>>(a);
-    return hipGetLastError();
-}
-
-template <int D, int QT>
-hipError_t launch_own_split(const SharedArgs &a, const Plan &p, const Target &to)
-{
-    const unsigned groups = (unsigned)(a.workers * a.cache.n_kv);
-    constexpr int OCC = split_occupancy(D, QT);
-    const int join = a.workers >= 16 * a.batch.batch ? 4 : 1;
-    if (to.name) {
-        if (p.alone == 1) return to.report("kv_own_wave_kernel<%d, %d, %d>", D, QT, OCC);
-        if (a.whole) return to.report("kv_own_split_kernel<%d, %d, %d>, whole row blocks", D, QT, OCC);
-        return to.report("kv_own_split_kernel<%d, %d, %d>, kv_own_join_kernel<%d, %d, %d>", D, QT, OCC, D, QT, join);
-    }
-    if (p.alone == 1) {
-        kv_own_wave_kernel<D, QT, OCC><<<groups, 64, 0, to.stream>>>(a);
-        return hipGetLastError();
-    }
-    kv_own_split_kernel<D, QT, OCC><<<groups, kThreads, 0, to.stream>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.whole) return e;
-    if (join == 4) kv_own_join_kernel<D, QT, 4><<<groups * 16 * QT, 256, 0, to.stream>>>(a);
-    else kv_own_join_kernel<D, QT, 1><<<groups * 16 * QT, 64, 0, to.stream>>>(a);
-    return hipGetLastError();
-}
-
-template <int D, int NW, int QT>
-hipError_t launch_own_rows(const SharedArgs &a, const Plan &p, const Target &to)
-{
-    if (to.name) {
-        if (p.splits == 1) return to.report("kv_own_rows_kernel<%d, %d, %d>", D, NW, QT);
-        return to.report("kv_own_rows_kernel<%d, %d, %d>, kv_own_join_rows_kernel<%d>, %d cuts", D, NW, QT, D, p.splits);
-    }
-    auto kernel = kv_own_rows_kernel<D, NW, QT>;
-    if (hipError_t e = allow_lds(kernel, rows_lds(D))) return e;
-    kernel<<<(unsigned)(p.items * a.cache.n_kv * p.splits), 64 * NW, rows_lds(D), to.stream>>>(a, p.splits);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t threads = a.batch.tokens * a.n_q * (D / 4);
-    kv_own_join_rows_kernel<D><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, to.stream>>>(a, p.splits);
+    constexpr int OCC = D <= 128 ? 2 : 1, LDS = MANY ? std::max(rows_lds(D), joint_lds(D)) : joint_lds(D);
+    auto kernel = kv_shared_kernel<D, MANY, OCC>;
+    if (hipError_t e = allow_lds(kernel, LDS)) return e;
+    const int64_t each = kWaves / p.share, per_chunk = (p.own * a.cache.n_kv + each - 1) / each;
+    kernel<<<(unsigned)(first + per_chunk * p.chunks), kThreads, LDS, to.stream>>>(a, (int)first, (int)per_chunk, p.share);
     return hipGetLastError();
 }
 
 template <int D>
-hipError_t launch(const SharedArgs &a, const SharedPlan &s, const Plan &p, Target to)
+hipError_t launch(const SharedArgs &a, const SharedPlan &p, const Target &to)
 {
-    hipError_t e;
-    if (s.qt == 1) e = launch_shared_split<D, 1>(a, s, to);
-    else if constexpr (D == 256) e = launch_shared_rows<D, 8, 1>(a, s, to);
-    else if (s.qt == 2) e = launch_shared_split<D, 2>(a, s, to);
-    else if (s.qt == 3) e = launch_shared_split<D, 3>(a, s, to);
-    else e = s.waves == 8 ? launch_shared_rows<D, 8, 2>(a, s, to) : launch_shared_rows<D, 4, 2>(a, s, to);
-    if (e != hipSuccess) return e;
-    to.go_on();
-    if (p.qt == 1) return launch_own_split<D, 1>(a, p, to);
-    if constexpr (D == 256) {
-        return launch_own_rows<D, 8, 1>(a, p, to);
-    } else {
-        if (p.qt == 2) return launch_own_split<D, 2>(a, p, to);
-        if (p.qt == 3) return launch_own_split<D, 3>(a, p, to);
-        return p.waves == 8 ? launch_own_rows<D, 8, 2>(a, p, to) : launch_own_rows<D, 4, 2>(a, p, to);
+    const int64_t first = p.items * a.cache.n_kv * p.splits;
+    if (to.name) {
+        const char *many = p.many == 16 ? "false" : "true";
+        if (D == 256 && p.many == 128)
+            return to.report("kv_shared_rows_kernel<256, 8, 1>, kv_shared_kernel<256, false, 1>, kv_shared_join_kernel<256>, "
+                             "%d cuts, %d waves, %d chunks", p.splits, p.share, p.chunks);
+        return to.report("kv_shared_kernel<%d, %s, %d>, kv_shared_join_kernel<%d>, %d cuts, %d waves, %d chunks", D, many,
+                         D <= 128 ? 2 : 1, D, p.splits, p.share, p.chunks);
     }
+    hipError_t e;
+    if constexpr (D == 256) {
+        if (p.many == 128) {
+            auto kernel = kv_shared_rows_kernel<D, 8, 1>;
+            if (hipError_t f = allow_lds(kernel, rows_lds(D))) return f;
+            kernel<<<(unsigned)first, 512, rows_lds(D), to.stream>>>(a);
+            if (hipError_t f = hipGetLastError()) return f;
+        }
+        e = launch_kernel<D, false>(a, p, p.many == 128 ? 0 : first, to);
+    } else {
+        e = p.many == 128 ? launch_kernel<D, true>(a, p, first, to) : launch_kernel<D, false>(a, p, first, to);
+    }
+    if (e != hipSuccess) return e;
+    constexpr int SIDE = kThreads / (D / 4);
+    const int64_t rows = (a.batch.tokens + a.batch.batch - 1) / a.batch.batch * a.n_q;       // of a sequence on average
+    const int per = (int)((rows + SIDE - 1) / SIDE);
+    kv_shared_join_kernel<D><<<(unsigned)per * (unsigned)a.batch.batch, kThreads, 0, to.stream>>>(a, per);
+    return hipGetLastError();
 }
-
-// Bytes of the parts and of the notes of skipped tiles, each a multiple of 16.
-int64_t parts_bytes(int64_t rows, int d) { return (rows * (d + 2) * 4 + 15) / 16 * 16; }
-int64_t skips_bytes(int batch) { return ((int64_t)batch * 4 + 15) / 16 * 16; }
 
 }  // namespace
 
-int64_t kv_shared_workspace(int64_t tokens, int batch, int groups, int max_pages, int page, int n_q, int n_kv, int d)
+int64_t kv_shared_workspace(int64_t tokens, int batch, int groups, int max_pages, int table_cols, int page, int n_q, int n_kv,
+                            int d)
 {
-    const SharedPlan s = shared_plan(tokens, groups, n_q, n_kv, d, (int64_t)max_pages * page / kTile);
-    return parts_bytes(tokens * n_q * s.splits, d) + skips_bytes(batch) + kv_attention_workspace(tokens, batch, n_q, n_kv, d);
+    const SharedPlan p = shared_plan(tokens, batch, groups, n_q, n_kv, d, (int64_t)max_pages * page / kTile,
+                                     own_tiles(table_cols, max_pages, page));
+    if (p.alone) return kv_attention_workspace(tokens, batch, n_q, n_kv, d);
+    return tokens * n_q * places(p) * (d + 2) * 4;
 }
 
 hipError_t kv_launch_shared(const kv_paged_cache &cache, const kv_paged_batch &batch, const kv_shared_prefix &prefix,
                             const uint16_t *q, int64_t q_stride, int n_q, float scale, void *workspace, uint16_t *out,
                             hipStream_t stream, char *name, int64_t name_len)
 {
-    const SharedPlan s = shared_plan(batch.tokens, prefix.groups, n_q, cache.n_kv, cache.d,
-                                     (int64_t)prefix.max_pages * cache.page / kTile);
-    // what the table has room for behind the shared pages stands for the sequences' own tokens
-    const int64_t most = (int64_t)std::max(batch.table_cols - prefix.max_pages, 1) * cache.page;
-    const Plan p = plan_for(batch.tokens, batch.batch, n_q, cache.n_kv, cache.d, most, most);
-    const int64_t rows = batch.tokens * n_q * s.splits;
-    float *pre_part = (float *)workspace, *pre_stats = pre_part + rows * cache.d;
-    int32_t *skips = reinterpret_cast<int32_t *>((char *)workspace + parts_bytes(rows, cache.d));
-    float *part = reinterpret_cast<float *>((char *)skips + skips_bytes(batch.batch)), *stats = part + p.parts * cache.d;
+    const SharedPlan p = shared_plan(batch.tokens, batch.batch, prefix.groups, n_q, cache.n_kv, cache.d,
+                                     (int64_t)prefix.max_pages * cache.page / kTile,
+                                     own_tiles(batch.table_cols, prefix.max_pages, cache.page));
+    if (p.alone)
+        return kv_launch_attention(cache, batch, q, q_stride, n_q, scale, 0, 0, workspace, out, stream, name, name_len);
+    float *part = (float *)workspace;
     SharedArgs a;
     static_cast<Args &>(a) = {cache, batch, q, q_stride, n_q, n_q / cache.n_kv, scale * 1.44269504f, 0, 0,
-                              __builtin_ctz(cache.page), p.workers, p.alone == kWaves, p.workers ? 1.0 / p.workers : 0.0,
-                              part, stats, reinterpret_cast<int32_t *>(stats + p.parts * 2), out};
+                              __builtin_ctz(cache.page), 0, false, 0.0, part, part + batch.tokens * n_q * places(p) * cache.d,
+                              nullptr, out};
     a.cu_seqs = prefix.cu_seqs;
     a.pages = prefix.pages;
     a.groups = prefix.groups;
     a.max_pages = prefix.max_pages;
-    a.pre_splits = s.splits;
-    a.pre_part = pre_part;
-    a.pre_stats = pre_stats;
-    a.skips = skips;
+    a.splits = p.splits;
+    a.chunks = p.chunks;
+    a.chunk = p.chunk;
     const Target to = {stream, name, name_len};
     switch (cache.d) {
-    case 64: return launch<64>(a, s, p, to);
-    case 96: return launch<96>(a, s, p, to);
-    case 128: return launch<128>(a, s, p, to);
-    case 256: return launch<256>(a, s, p, to);
+    case 64: return launch<64>(a, p, to);
+    case 96: return launch<96>(a, p, to);
+    case 128: return launch<128>(a, p, to);
+    case 256: return launch<256>(a, p, to);
     default: return hipErrorInvalidValue;
     }
 }

@@ -433,12 +433,13 @@ int check_shared(const kv_shared_prefix *p)
 
 }  // namespace
 
-int64_t kv_paged_attention_shared_workspace_size(int64_t tokens, int32_t batch, int32_t groups, int32_t max_pages,
-                                                 int32_t page, int32_t n_q, int32_t n_kv, int32_t d)
+int64_t kv_paged_attention_shared_workspace_size(int64_t tokens, int32_t batch, int32_t table_cols, int32_t page,
+                                                 int32_t groups, int32_t max_pages, int32_t n_q, int32_t n_kv, int32_t d)
 {
     if (check_rows(tokens) || batch < 1 || batch > 65536 || check_heads(n_q, n_kv) || check_paged_d(d)) return 0;
     if (groups < 1 || groups > 65536 || max_pages < 1 || max_pages > (1 << 24) || check_page(page)) return 0;
-    return kv_shared_workspace(tokens, batch, groups, max_pages, page, n_q, n_kv, d);
+    if (table_cols < 1 || table_cols > (1 << 30) / page) return 0;
+    return kv_shared_workspace(tokens, batch, groups, max_pages, table_cols, page, n_q, n_kv, d);
 }
 
 int kv_paged_attention_shared(const kv_paged_cache *cache, const kv_paged_batch *batch, const kv_shared_prefix *prefix,
@@ -453,8 +454,8 @@ int kv_paged_attention_shared(const kv_paged_cache *cache, const kv_paged_batch 
     if (batch->tokens * n_q * cache->d > kMaxElems || (int64_t)prefix->groups * cache->n_kv > int64_t(1) << 21) return Q4_ERR_SHAPE;
     if (int rc = check_paged_rows(q, q_stride, (int64_t)n_q * cache->d, batch->tokens)) return rc;
     if (!aligned(workspace, 16) || !aligned(out, 16)) return Q4_ERR_ALIGN;
-    if (workspace_bytes < kv_shared_workspace(batch->tokens, batch->batch, prefix->groups, prefix->max_pages, cache->page,
-                                              n_q, cache->n_kv, cache->d))
+    if (workspace_bytes < kv_shared_workspace(batch->tokens, batch->batch, prefix->groups, prefix->max_pages, batch->table_cols,
+                                              cache->page, n_q, cache->n_kv, cache->d))
         return Q4_ERR_SHAPE;
     return finish(kv_launch_shared(*cache, *batch, *prefix, q, q_stride, n_q, scale, workspace, out, (hipStream_t)stream));
 }

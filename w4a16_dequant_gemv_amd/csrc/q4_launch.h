@@ -57,7 +57,8 @@ hipError_t kv_launch_attention(const kv_paged_cache &cache, const kv_paged_batch
                                uint16_t *out, hipStream_t stream, char *name = nullptr, int64_t name_len = 0);
 
 // The same for sequences that share their first pages (kv_shared.hip).
-int64_t kv_shared_workspace(int64_t tokens, int batch, int groups, int max_pages, int page, int n_q, int n_kv, int d);
+int64_t kv_shared_workspace(int64_t tokens, int batch, int groups, int max_pages, int table_cols, int page, int n_q, int n_kv,
+                            int d);
 hipError_t kv_launch_shared(const kv_paged_cache &cache, const kv_paged_batch &batch, const kv_shared_prefix &prefix,
                             const uint16_t *q, int64_t q_stride, int n_q, float scale, void *workspace, uint16_t *out,
                             hipStream_t stream, char *name = nullptr, int64_t name_len = 0);

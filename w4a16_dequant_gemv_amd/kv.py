@@ -162,8 +162,8 @@ def _workspace_size(tokens, batch, n_q, n_kv, d):
 
 
 @lru_cache(maxsize=4096)
-def _shared_workspace_size(tokens, batch, groups, max_pages, page, n_q, n_kv, d):
-    return lib().kv_paged_attention_shared_workspace_size(tokens, batch, groups, max_pages, page, n_q, n_kv, d)
+def _shared_workspace_size(*sizes):
+    return lib().kv_paged_attention_shared_workspace_size(*sizes)
 
 
 def attention_config(tokens, batch, table_cols, n_q, n_kv, d, page=128, window=0, sinks=0, groups=0, max_pages=0):
@@ -441,7 +441,7 @@ class PagedKVCache(_Kept):
             raise W4A16Error("prefix must be a SharedPrefix")
         else:
             p, groups, max_pages = prefix._struct(dev)
-            need = _shared_workspace_size(T, B, groups, max_pages, self.page, n_q, self.n_kv, self.d)
+            need = _shared_workspace_size(T, B, batch.block_table.shape[1], self.page, groups, max_pages, n_q, self.n_kv, self.d)
         if workspace is None:
             workspace = self.k.new_empty(need)
         elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
