@@ -28,30 +28,30 @@ def sizes(c):
 
 
 CASES = [
-    Case(128, 128, 8, 8, ((3, 5),), 90, 1, 0),                       # <128, false>, 4 waves
-    Case(128, 64, 8, 8, ((6, 70),), 90, 1, 6),                       # <128, false>, 2 waves
-    Case(128, 64, 8, 8, ((6, 70),), 90, 1, 0),                       # <128, false>, 1 waves
-    Case(128, 64, 2, 16, ((3, 180),), 60, 1, 0),                     # <128, true>, 4 waves
-    Case(128, 64, 8, 8, ((3, 260),), 60, 1, 8),                      # <128, true>, 2 waves
-    Case(128, 64, 8, 8, ((3, 260),), 60, 1, 0),                      # <128, true>, 1 waves
-    Case(64, 64, 8, 8, ((3, 5),), 90, 1, 0),                         # <64, false>, 4 waves
-    Case(64, 64, 16, 16, ((6, 70),), 90, 1, 6),                      # <64, false>, 2 waves
-    Case(64, 64, 16, 16, ((6, 70),), 90, 1, 0),                      # <64, false>, 1 waves
-    Case(64, 64, 2, 16, ((3, 260),), 60, 1, 0),                      # <64, true>, 4 waves
-    Case(64, 64, 8, 8, ((3, 260),), 60, 1, 8),                       # <64, true>, 2 waves
-    Case(64, 64, 8, 8, ((3, 260),), 60, 1, 0),                       # <64, true>, 1 waves
-    Case(96, 64, 8, 8, ((3, 5),), 90, 1, 0),                         # <96, false>, 4 waves
-    Case(96, 64, 8, 8, ((6, 70),), 90, 1, 6),                        # <96, false>, 2 waves
-    Case(96, 64, 8, 8, ((6, 70),), 90, 1, 0),                        # <96, false>, 1 waves
-    Case(96, 64, 2, 16, ((3, 260),), 60, 1, 0),                      # <96, true>, 4 waves
-    Case(96, 64, 8, 8, ((3, 260),), 60, 1, 8),                       # <96, true>, 2 waves
-    Case(96, 64, 8, 8, ((3, 260),), 60, 1, 0),                       # <96, true>, 1 waves
-    Case(256, 64, 8, 8, ((3, 5),), 90, 1, 0),                        # <256, false>, 4 waves
-    Case(256, 64, 16, 16, ((7, 20), (2, 3), (1, 1)), 90, 1, 6),      # <256, false>, 2 waves
-    Case(256, 64, 16, 16, ((7, 20), (2, 3), (1, 1)), 90, 1, 0),      # <256, false>, 1 waves
-    Case(256, 64, 1, 15, ((3, 180),), 60, 1, 0),                  # rows<256>, 4 waves
-    Case(256, 64, 8, 8, ((3, 100),), 60, 3, 8),                      # rows<256>, 2 waves
-    Case(256, 64, 8, 16, ((3, 180),), 60, 1, 0),                     # rows<256>, 1 waves
+    Case(128, 64, 8, 8, ((3, 70),), 60, 1, 0),                        # <128, false, 2>, 1 cuts, 1 waves
+    Case(128, 64, 8, 8, ((3, 70),), 60, 1, 8),                        # <128, false, 2>, 1 cuts, 2 waves
+    Case(128, 64, 1, 8, ((3, 5),), 60, 1, 0),                         # <128, false, 2>, 1 cuts, 4 waves
+    Case(128, 64, 8, 8, ((6, 260),), 60, 3, 0),                       # <128, true, 2>, 1 cuts, 1 waves
+    Case(128, 64, 8, 16, ((12, 180),), 60, 1, 8),                     # <128, true, 2>, 1 cuts, 2 waves
+    Case(128, 64, 1, 32, ((20, 180),), 60, 1, 8),                     # <128, true, 2>, 3 cuts, 4 waves
+    Case(256, 64, 2, 8, ((3, 100),), 60, 1, 0),                       # <256, false, 1>, 1 cuts, 1 waves
+    Case(256, 64, 2, 8, ((3, 100),), 60, 1, 8),                       # <256, false, 1>, 1 cuts, 2 waves
+    Case(256, 64, 1, 8, ((3, 5),), 60, 1, 0),                         # <256, false, 1>, 1 cuts, 4 waves
+    Case(64, 64, 8, 8, ((3, 100),), 60, 1, 0),                        # <64, false, 2>, 1 cuts, 1 waves
+    Case(64, 64, 8, 8, ((3, 100),), 60, 1, 8),                        # <64, false, 2>, 1 cuts, 2 waves
+    Case(64, 64, 1, 8, ((3, 5),), 60, 1, 0),                          # <64, false, 2>, 1 cuts, 4 waves
+    Case(64, 64, 2, 16, ((6, 400),), 60, 3, 0),                       # <64, true, 2>, 1 cuts, 1 waves
+    Case(64, 64, 4, 64, ((6, 260),), 60, 1, 8),                       # <64, true, 2>, 1 cuts, 2 waves
+    Case(64, 64, 2, 32, ((12, 130),), 60, 3, 8),                      # <64, true, 2>, 1 cuts, 4 waves
+    Case(96, 64, 8, 8, ((3, 70),), 60, 1, 0),                         # <96, false, 2>, 1 cuts, 1 waves
+    Case(96, 64, 8, 8, ((3, 70),), 60, 1, 8),                         # <96, false, 2>, 1 cuts, 2 waves
+    Case(96, 64, 1, 8, ((3, 5),), 60, 1, 0),                          # <96, false, 2>, 1 cuts, 4 waves
+    Case(96, 64, 8, 8, ((6, 400),), 60, 3, 0),                        # <96, true, 2>, 1 cuts, 1 waves
+    Case(96, 64, 2, 16, ((6, 180),), 60, 3, 8),                       # <96, true, 2>, 1 cuts, 2 waves
+    Case(96, 64, 1, 32, ((6, 260),), 60, 1, 8),                       # <96, true, 2>, 1 cuts, 4 waves
+    Case(256, 64, 4, 64, ((3, 260),), 60, 1, 0),                      # rows_kernel<256, 8, 1>, 1 cuts, 1 waves
+    Case(256, 64, 4, 64, ((3, 260),), 60, 1, 8),                      # rows_kernel<256, 8, 1>, 1 cuts, 2 waves
+    Case(256, 64, 2, 8, ((60, 70),), 60, 3, 0),                       # rows_kernel<256, 8, 1>, 8 cuts, 4 waves
     # tables much wider than the sequences, and sequences as long as theirs: chunks of own tokens
     Case(128, 128, 2, 8, ((3, 5),), 200, 1, 40),
     Case(64, 64, 1, 8, ((7, 20), (2, 3), (1, 1)), 2500, 1, 0),

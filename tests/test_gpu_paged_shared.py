@@ -52,10 +52,13 @@ class Shared(World):
         y = out.cpu().numpy().astype(np.float64)
         at = front
         assert (y[:front] == 7).all()
+        # of many sequences the first ones, those at the groups' borders, the last one and some
+        some = {*range(6), *self.cu.tolist(), *(self.cu - 1).tolist(), *np.random.default_rng(1).integers(0, len(self.seqs), 16).tolist()}
         for b, (s, m) in enumerate(zip(self.seqs, self.new if n is None else n)):
+            assert np.isfinite(y[at:at + m]).all(), b
             if b in skip:
                 assert (y[at:at + m] == 7).all(), b
-            elif m:
+            elif m and b in some:
                 o, size, most = ref.attend(s, x[at:at + m], self.d ** -0.5 if scale is None else scale, hidden=hidden[b] if hidden else ())
                 err, tol = np.abs(y[at:at + m] - o), ref.tolerance(o, size, most, len(s), self.d, weights=weights)
                 assert bool((err <= tol).all()), (b, float((err / tol).max()), np.argwhere(~(err <= tol))[:3].tolist())
@@ -92,8 +95,8 @@ def test_against_the_definition(c):
 
 
 # one kernel of each kind, with three groups of which the last has one sequence
-KINDS = [Case(128, 64, 2, 8, ((5, 6), (3, 4), (2, 1)), 150, 1, 0), Case(64, 64, 8, 8, ((6, 130), (3, 120), (2, 1)), 90, 1, 0),
-         Case(256, 64, 8, 16, ((4, 90), (3, 89), (2, 1)), 60, 1, 0)]
+KINDS = [Case(128, 64, 2, 8, ((5, 6), (3, 4), (2, 1)), 150, 1, 0), Case(64, 64, 4, 64, ((6, 150), (5, 109), (2, 1)), 60, 1, 8),
+         Case(256, 64, 4, 64, ((6, 100), (5, 100), (4, 1)), 60, 1, 0)]
 
 
 @pytest.mark.parametrize("c", KINDS)

@@ -236,31 +236,36 @@ SharedPlan shared_plan(int64_t tokens, int batch, int groups, int n_q, int n_kv,
     p.own = tokens * group / 16 + batch;
     p.chunks = (int)std::min<int64_t>((own + 31) / 32, 8);
     p.chunk = (int)((own + p.chunks - 1) / p.chunks);
-    const double beside = (double)(blocks * p.share / 4);
-    // What a choice costs: a start, a run of tiles, which takes longer the more workgroups share the card, a second round of
-    // workgroups, and the parts' way out and back.  (us with 1, 2, 4, 6, 8, 16 and 32 runs: 64 sequences behind 4k, 16
-    // rows a workgroup 50, 54, 63, 73, 82, 118, 199, 128 rows 115, 66, 42, 43, 48, 58, 76; 16 of 32 heads on 8 behind 8k 62, 38, 26,
-    // 23.5, 22.9, 31.5, 43.7 and 203, 110, 61, 47, 39, 29, 29.)
+    // What a choice costs, in us: a start, then the longest run of tiles or, where that is more, all the work shared out to the
+    // workgroups that the CUs hold at once, and the parts' way out and back.  A tile of the shared pages takes a workgroup
+    // `alone` us with a CU to itself, `full` with two on each.  (With 1, 2, 4, 6, 8, 16 and 32 runs: 64 sequences behind 4k, 16
+    // rows a workgroup 50, 53, 61, 69, 74, 106, 168, 128 rows 110, 64, 43, 41, 47, 62, 80; 16 of 32 heads on 8 behind 8k 59, 36, 24,
+    // 22, 22, 30, 39 and 198, 105, 60, 45, 38, 30, 29.)
+    const double size = (double)d / 128;
+    const double slots = d <= 128 ? 512 : 256;
+    const double own_work = (double)(blocks * p.share) / 4 * (6.0 + 1.1 * size * (double)std::min<int64_t>(own, p.chunk) / p.share);
     double best = 0.0;
-    auto offer = [&](int rb, int64_t slots, double start, double alone, double full) {
+    auto offer = [&](int rb, double start, double alone, double full) {
         const int64_t n_blocks = (rows + rb - 1) / rb * groups * n_kv;
-        for (int cuts = 1; cuts <= 64 && cuts <= tiles && (cuts == 1 || n_blocks * cuts <= 4 * slots); ++cuts) {
-            const double n = (double)(n_blocks * cuts), half = (double)slots / 2, run = (double)tiles / cuts;
-            const double tile = alone + (full - alone) * std::min(1.0, std::max(0.0, n / half - 1.0));
-            const double c = start + tile * (rb == 16 ? std::max(run, (double)kWaves) : run) * std::max(1.0, n / (double)slots) +
-                17.0 * std::max(0.0, (n + beside) / (0.9 * (double)slots) - 1.0) + (double)(tokens * n_q) * cuts * d * 8 / 2e6;
-            if (p.splits == 0 || c < best) {
-                best = c;
+        for (const int cuts : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            if (cuts > 1 && (cuts > tiles || (double)(n_blocks * cuts) > 4 * slots)) break;
+            const double n = (double)(n_blocks * cuts), run = (double)tiles / cuts;
+            const double tile = alone + (full - alone) * std::min(1.0, std::max(0.0, 2 * n / slots - 1.0));
+            const double chain = tile * (rb == 16 ? std::max(run, (double)kWaves) : run) * std::max(1.0, n / slots);
+            const double parts = (double)(tokens * n_q) * cuts * d * 8 / 2e6;
+            const bool apart = d == 256 && rb == 128;                            // in a launch of its own
+            const double work = apart ? chain + own_work / slots : std::max(chain, (n * run * full + own_work) / slots);
+            if (p.splits == 0 || start + work + parts < best) {
+                best = start + work + parts;
                 p.many = rb;
                 p.splits = cuts;
                 p.items = std::max<int64_t>(tokens * group - groups, 0) / rb + groups;
             }
         }
     };
-    const double size = (double)d / 128;
-    offer(16, d <= 128 ? 512 : 256, 8.0, 0.1 + 0.23 * size, 0.1 + 0.75 * size);
-    if (d <= 128) offer(128, 512, 8.0, 1.48, 2.3);
-    else offer(128, 256, 14.0, 2.0, 2.0);                              // in a launch of its own
+    offer(16, 8.0, 0.1 + 0.29 * size, 0.1 + 0.75 * size);
+    if (d <= 128) offer(128, 10.0, 1.48, 2.3);
+    else offer(128, 16.0, 2.6, 2.6);
     return p;
 }
 
