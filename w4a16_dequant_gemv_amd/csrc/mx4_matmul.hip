@@ -137,7 +137,9 @@ __device__ __forceinline__ u32x4 buffer_of(const void *p, uint32_t bytes)
 // 256 elements of every row, 128 bytes, and their scales; two stages in LDS.  A wave reads
 // the operands of the next 64 elements between the matrix instructions of these ones.  In
 // the middle of a stage's last ones every wave has all it needs of the stage and the next one
-// has come in: one barrier, and the stage after that is sent for, a whole stage ahead.
+// has come in: one barrier, and the stage after that is sent for, a whole stage ahead.  Where k ends inside a stage,
+// the codes behind it are the next row's or zeros; their scales are made 2^-127 on both sides, and such products vanish
+// in any sum.
 template <int TYPE, int TM, int TN, int NB>
 __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restrict__ xc, const uint8_t *__restrict__ xs,
                                                           const uint8_t *__restrict__ wc, const uint8_t *__restrict__ ws,
@@ -154,7 +156,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
     const int m0 = tile_m * BM, n0 = tile_n * BN;
     const int rows_m = min(BM, m - m0), rows_n = min(BN, n_out - n0);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int pitch = k / 2, steps = k / 256, rest = k % 256 / 32;       // whole stages, blocks behind them
+    const int pitch = k / 2, steps = (k + 255) / 256;
 
     // Loading: lane i of a load puts 16 bytes at row i / 8, place i % 8, where swz puts another chunk of the row.
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
@@ -210,6 +212,8 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
         if (i < TM) f.x[i] = *reinterpret_cast<const u32x4 *>(smem + buf * STAGE + X + (xrow + 32 * i) * 128 + c);
         else f.w[i - TM] = *reinterpret_cast<const u32x4 *>(smem + buf * STAGE + W + (wrow + 32 * (i - TM)) * 128 + c);
     };
+    const int left = k / 32 - (steps - 1) * 8 - 4 * g;                   // blocks of the last stage for this lane
+    const uint32_t tail = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1;
     auto read_scale = [&](Scale &f, int buf, int i) {
         if (i < TM) f.x[i] = *reinterpret_cast<const uint32_t *>(smem + buf * STAGE + XS + (xrow + 32 * i) * 8 + 4 * g);
         else f.w[i - TM] = *reinterpret_cast<const uint32_t *>(smem + buf * STAGE + WS + (wrow + 32 * (i - TM)) * 8 + 4 * g);
@@ -249,7 +253,13 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
     Frag f0, f1;
     Scale s0, s1;
     // stage s in buffer `buf`, `last` and `after` being the buffers around it
-    auto stage = [&](int s, int last, int buf, int after, const Scale &now, Scale &next) {
+    auto stage = [&](int s, int last, int buf, int after, Scale &now, Scale &next) {
+        if (s + 1 == steps) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) now.x[i] &= tail;
+#pragma unroll
+            for (int i = 0; i < TN; ++i) now.w[i] &= tail;
+        }
         quarter(Q0{}, f0, now, f1, buf, s + NB - 1, last, FIRST, PIECES);
         quarter(Q1{}, f1, now, f0, buf, 0, 0, 0, 0);
         quarter(Q2{}, f0, now, f1, buf, 0, 0, 0, 0);
@@ -276,7 +286,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if (steps > 0) {
+    {
 #pragma unroll
         for (int s = 0; s < NB - 1; ++s)
 #pragma unroll
@@ -305,45 +315,6 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
         if (s < steps) stage(s, last, buf, after, s0, s1);
         wait_vmem<0>();
     }
-    if (rest) {
-        // the blocks behind the last whole stage, through registers: what lies behind them is zero
-        __syncthreads();
-        for (int i = tid; i < (BM + BN) * 8; i += 256) {
-            const bool of_x = i < BM * 8;
-            const int row = (of_x ? i : i - BM * 8) >> 3, c = i & 7;
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (c < rest)
-                v = *reinterpret_cast<const u32x4 *>((of_x ? xc + (int64_t)(m0 + min(row, rows_m - 1)) * pitch
-                                                           : wc + (int64_t)(n0 + min(row, rows_n - 1)) * pitch) +
-                                                     steps * 128 + c * 16);
-            *reinterpret_cast<u32x4 *>(smem + (of_x ? X : W) + row * 128 + ((c ^ swz(row)) * 16)) = v;
-        }
-        const uint64_t mask = ~0ull >> (64 - 8 * rest);
-        for (int i = tid; i < BM + BN; i += 256) {
-            const bool of_x = i < BM;
-            const int row = of_x ? i : i - BM;
-            const uint64_t v = *reinterpret_cast<const uint64_t *>(
-                of_x ? xs + ((int64_t)steps * m + m0 + min(row, rows_m - 1)) * 8
-                     : ws + ((int64_t)steps * n_out + n0 + min(row, rows_n - 1)) * 8);
-            *reinterpret_cast<uint64_t *>(smem + (of_x ? XS : WS) + row * 8) = v & mask;
-        }
-        __syncthreads();
-        auto one = [&](auto J) {
-            constexpr int j = decltype(J)::value;
-            if (j >= rest) return;
-#pragma unroll
-            for (int i = 0; i < PART; ++i) read(f0, 0, j, i);
-#pragma unroll
-            for (int t = 0; t < ALL; ++t) mma(J, f0, s0, t);
-        };
-#pragma unroll
-        for (int i = 0; i < PART; ++i) read_scale(s0, 0, i);
-        one(Q0{});
-        one(Q1{});
-        one(Q2{});
-        one(Q3{});
-    }
-
     // y goes through LDS (rows padded to YS bytes) and leaves as 16-byte pieces of whole rows.
     constexpr int YS = BN * 2 + 16;
     static_assert(BM * YS <= NB * STAGE, "output tile exceeds LDS");
@@ -361,19 +332,22 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
                     u32x2{lo, hi};
             }
     __syncthreads();
-    constexpr int CPR = BN / 8;
-    const bool vec16 = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && (n_out & 7) == 0;
+    const int cols = min(BN, n_out - n0);
+    uint16_t *out = y + (int64_t)m0 * n_out + n0;
+    if ((reinterpret_cast<uintptr_t>(y) & 15) == 0 && (n_out & 7) == 0) {
+        constexpr int CPR = BN / 8;
 #pragma unroll 4
-    for (int i = tid; i < rows_m * CPR; i += 256) {
-        const int row = i / CPR, pc = i % CPR, col = n0 + pc * 8;
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(smem + row * YS + pc * 16);
-        uint16_t *to = y + (int64_t)(m0 + row) * n_out + col;
-        if (vec16 && col + 8 <= n_out) {
-            *reinterpret_cast<u32x4 *>(to) = v;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (col + e < n_out) to[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        for (int i = tid; i < rows_m * CPR; i += 256) {
+            const int row = i / CPR, c = i % CPR * 8;
+            if (c < cols)
+                *reinterpret_cast<u32x4 *>(out + (int64_t)row * n_out + c) = *reinterpret_cast<const u32x4 *>(smem + row * YS + c * 2);
+        }
+    } else {
+        // rows that begin anywhere: a wave's stores are still side by side
+#pragma unroll 8
+        for (int i = tid; i < rows_m * BN; i += 256) {
+            const int row = i / BN, c = i % BN;
+            if (c < cols) out[(int64_t)row * n_out + c] = *reinterpret_cast<const uint16_t *>(smem + row * YS + c * 2);
         }
     }
 }
