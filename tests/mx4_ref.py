@@ -29,7 +29,7 @@ def values(codes, scales):
     rows, k = codes.shape
     v = VALUES[codes & 7] * np.where(codes & 8, -1.0, 1.0)
     s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(np.int64) - 127))
-    return (v.reshape(rows, -1, 32) * s[..., None]).reshape(rows, k)
+    return (v.reshape(rows, k // 32, 32) * s[..., None]).reshape(rows, k)
 
 
 def pack(codes):
@@ -37,7 +37,7 @@ def pack(codes):
 
 
 def unpack(b):
-    return np.stack((b & 15, b >> 4), -1).reshape(b.shape[0], -1)
+    return np.stack((b & 15, b >> 4), -1).reshape(b.shape[0], 2 * b.shape[1])
 
 
 def laid(scales):
@@ -45,7 +45,7 @@ def laid(scales):
     rows, blocks = scales.shape
     s = np.zeros((rows, -(-blocks // 8) * 8), np.uint8)
     s[:, :blocks] = scales
-    return np.ascontiguousarray(s.reshape(rows, -1, 8).transpose(1, 0, 2))
+    return np.ascontiguousarray(s.reshape(rows, -(-blocks // 8), 8).transpose(1, 0, 2))
 
 
 def product(x, w, half_step):

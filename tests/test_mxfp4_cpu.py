@@ -115,13 +115,14 @@ def test_python_refuses():
     for f in (lambda: mxfp4.quantize(torch.zeros(4, 64)), lambda: mxfp4.dequantize(q), lambda: mxfp4.matmul(q, q),
               lambda: mxfp4.linear(torch.zeros((4, 64), dtype=torch.float16), q), lambda: mxfp4.dequantize(c),
               lambda: mxfp4.MXTensor.from_blocks(c, torch.zeros((4, 3), dtype=torch.uint8)),
+              lambda: mxfp4.MXTensor.from_blocks(c[:, :0], torch.zeros((4, 0), dtype=torch.uint8)),
               lambda: mxfp4.MXTensor.from_blocks(c.int(), torch.zeros((4, 2), dtype=torch.uint8)),
               lambda: mxfp4.MXTensor.from_blocks(c[:, :24], torch.zeros((4, 1), dtype=torch.uint8))):
         with pytest.raises(W4A16Error):
             f()
 
 
-@pytest.mark.parametrize("rows,k", [(1, 32), (3, 256), (5, 288), (7, 11008)])
+@pytest.mark.parametrize("rows,k", [(0, 32), (0, 512), (1, 32), (3, 256), (5, 288), (7, 11008)])
 def test_order_of_scales(rows, k):
     rng = np.random.default_rng(k)
     s = rng.integers(0, 256, (rows, k // 32), dtype=np.uint8)

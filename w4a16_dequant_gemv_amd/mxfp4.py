@@ -47,7 +47,7 @@ class MXTensor:
 
     def block_scales(self):
         """The scales in the order of a checkpoint, uint8 [rows, k // 32]."""
-        return self.scales.permute(1, 0, 2).reshape(self.rows, -1)[:, :self.k // BLOCK].contiguous()
+        return self.scales.permute(1, 0, 2).flatten(1)[:, :self.k // BLOCK].contiguous()
 
     @classmethod
     def from_blocks(cls, codes, block_scales):
@@ -56,10 +56,10 @@ class MXTensor:
             raise W4A16Error("codes must be uint8 [rows, k // 2]")
         rows, blocks = codes.shape[0], codes.shape[1] // (BLOCK // 2)
         if not isinstance(block_scales, torch.Tensor) or block_scales.dtype != torch.uint8 or \
-                codes.shape[1] % (BLOCK // 2) or block_scales.shape != (rows, blocks):
+                not blocks or codes.shape[1] % (BLOCK // 2) or block_scales.shape != (rows, blocks):
             raise W4A16Error("block_scales must be uint8 [rows, k // 32], k a multiple of 32")
         s = torch.nn.functional.pad(block_scales, (0, -blocks % 8))
-        return cls(codes.contiguous(), s.view(rows, -1, 8).transpose(0, 1).contiguous())
+        return cls(codes.contiguous(), s.view(rows, -(-blocks // 8), 8).transpose(0, 1).contiguous())
 
 
 def _parts(q, name):
