@@ -57,12 +57,16 @@ int mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, in
  * of two values whose scales multiply to less than 2^-126 may count as zero.  A block
  * with s = 255 makes the sums that it is part of NaN.  Results do not
  * depend on anything but the operands and sizes.
+ * `workspace`: device memory of at least mx4_matmul_workspace_size bytes (may be NULL where that
+ * is 0), overwritten; calls sharing one must not overlap.
  */
 int mx4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes, const uint8_t *w_scales,
-               int64_t m, int64_t n_out, int64_t k, int32_t type, void *y, void *stream);
+               int64_t m, int64_t n_out, int64_t k, int32_t type, void *workspace, int64_t workspace_bytes, void *y,
+               void *stream);
 
-/* Workspace bytes of mx4_linear, 0 where few rows of x are quantized without one; no HIP
- * call is made. */
+/* Workspace bytes of mx4_matmul, for the sums of parts of a long k, and of mx4_linear, which also has the
+ * quantized x there; 0 where a call needs none.  No HIP call is made. */
+int64_t mx4_matmul_workspace_size(int64_t m, int64_t n_out, int64_t k);
 int64_t mx4_linear_workspace_size(int64_t m, int64_t n_out, int64_t k);
 
 /*

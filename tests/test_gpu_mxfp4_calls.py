@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 # (m, n_out, k): every kernel of the product, rows that end inside a stage and rows that do not
 SIZES = [(1, 40, 288), (5, 100, 4096), (20, 130, 512), (70, 500, 800), (700, 3000, 544), (1000, 4001, 2080), (2000, 6001, 544),
-         (2050, 8000, 1056)]
+         (2050, 8000, 1056), (2000, 8101, 800), (40, 302, 8000), (100, 71, 28640)]
 
 
 def random(m, k, seed, dtype=torch.float16):
@@ -77,7 +77,7 @@ def test_extreme_scales(m, n, k):
 def test_captured_steps():
     """Layers in one captured graph, of which those of a stream share a workspace, replayed with new inputs and the
     program's own work between the replays."""
-    sizes = [(1, 4096, 1024), (8, 1000, 4096), (100, 700, 1024), (900, 3000, 544)]
+    sizes = [(1, 4096, 1024), (8, 1000, 4096), (100, 700, 1024), (900, 3000, 544), (40, 300, 11008)]
     w = [operand(n, k, n)[0] for _, n, k in sizes]
     x = [random(m, k, m) for m, _, k in sizes]
     ws = torch.empty(max(mxfp4.workspace_size(*s) for s in sizes) + 16, dtype=torch.uint8, device="cuda")
@@ -107,8 +107,8 @@ def test_captured_steps():
 
 def test_streams():
     """Calls on two streams at once, without workspaces of the caller's."""
-    qw, _ = operand(3000, 1056, 1)
-    xs = [random(m, 1056, m) for m in (3, 40, 700, 2050)]
+    qw, _ = operand(300, 11008, 1)
+    xs = [random(m, 11008, m) for m in (3, 40, 700, 2050)]
     want = [mxfp4.linear(x, qw) for x in xs]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
@@ -132,6 +132,7 @@ def test_empty_and_refused():
     wide = torch.zeros((40, 4096), dtype=torch.float16, device="cuda")
     big, _ = operand(100, 4096, 1)
     ws = torch.empty(mxfp4.workspace_size(40, 100, 4096), dtype=torch.uint8, device="cuda")
+    long, _ = operand(64, 28672, 1)
     wrong = mxfp4.MXTensor(qw.codes, qw.scales[:, :9].contiguous())
     for f in (lambda: mxfp4.linear(x.float(), qw), lambda: mxfp4.linear(x.cpu(), qw), lambda: mxfp4.linear(x[:, :32], qw),
               lambda: mxfp4.linear(x.T, qw), lambda: mxfp4.linear(x[0], qw), lambda: mxfp4.linear(x[:1].expand(4, 64), qw),
@@ -140,13 +141,15 @@ def test_empty_and_refused():
               lambda: mxfp4.linear(x, qw, out=torch.empty((4, 10), dtype=torch.float16)),
               lambda: mxfp4.linear(x, qw, out=torch.empty((10, 4), dtype=torch.float16, device="cuda").T),
               lambda: mxfp4.linear(wide, big, workspace=ws[:-16]), lambda: mxfp4.linear(wide, big, workspace=ws.cpu()),
-              lambda: mxfp4.linear(wide, big, workspace=ws[8:]), lambda: mxfp4.matmul(qw, big), lambda: mxfp4.matmul(qw, qw, torch.float32),
+              lambda: mxfp4.linear(wide, big, workspace=ws[8:]), lambda: mxfp4.matmul(long, long, workspace=ws[:64]), lambda: mxfp4.matmul(qw, big), lambda: mxfp4.matmul(qw, qw, torch.float32),
               lambda: mxfp4.quantize(x[:, 1:33]), lambda: mxfp4.quantize(x.int()), lambda: mxfp4.quantize(x[:, :48]),
               lambda: mxfp4.quantize(x, out=big), lambda: mxfp4.dequantize(qw, torch.float64), lambda: mxfp4.dequantize(wrong),
               lambda: mxfp4.quantize(torch.zeros((4, 100), dtype=torch.float16, device="cuda")[:, :64])):
         with pytest.raises(W4A16Error):
             f()
     mxfp4.linear(wide, big, workspace=ws)
+    own = torch.empty(mxfp4.workspace_size(64, 64, 28672, linear=False), dtype=torch.uint8, device="cuda")
+    assert torch.equal(mxfp4.matmul(long, long, workspace=own), mxfp4.matmul(long, long))
     mxfp4.linear(one, big, workspace=ws[:0])                  # quantized on the way
 
 

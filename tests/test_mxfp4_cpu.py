@@ -42,9 +42,10 @@ def dequantize(L, **kw):
 
 
 def matmul(L, **kw):
-    a = dict(xc=P, xs=P, wc=P, ws=P, m=3, n=5, k=64, type=0, y=P)
+    a = dict(xc=P, xs=P, wc=P, ws=P, m=3, n=5, k=64, type=0, space=None, size=0, y=P)
     a.update(kw)
-    return L.mx4_matmul(a["xc"], a["xs"], a["wc"], a["ws"], a["m"], a["n"], a["k"], a["type"], a["y"], None)
+    return L.mx4_matmul(a["xc"], a["xs"], a["wc"], a["ws"], a["m"], a["n"], a["k"], a["type"], a["space"],
+                        a["size"], a["y"], None)
 
 
 def linear(L, **kw):
@@ -71,7 +72,8 @@ def linear(L, **kw):
     (matmul, dict(m=0), Q4_ERR_SHAPE), (matmul, dict(n=0), Q4_ERR_SHAPE), (matmul, dict(n=1 << 25), Q4_ERR_SHAPE),
     (matmul, dict(k=40), Q4_ERR_SHAPE), (matmul, dict(m=1 << 20, n=1 << 20), Q4_ERR_SHAPE), (matmul, dict(xc=P + 8), Q4_ERR_ALIGN),
     (matmul, dict(xs=P + 4), Q4_ERR_ALIGN), (matmul, dict(wc=P + 8), Q4_ERR_ALIGN), (matmul, dict(ws=P + 4), Q4_ERR_ALIGN),
-    (matmul, dict(y=P + 1), Q4_ERR_ALIGN),
+    (matmul, dict(y=P + 1), Q4_ERR_ALIGN), (matmul, dict(m=64, k=28672), Q4_ERR_NULL),
+    (matmul, dict(m=64, k=28672, space=P, size=16384), Q4_ERR_SHAPE), (matmul, dict(m=64, k=28672, space=P + 8, size=1 << 24), Q4_ERR_ALIGN),
     (linear, dict(x=None), Q4_ERR_NULL), (linear, dict(wc=None), Q4_ERR_NULL), (linear, dict(ws=None), Q4_ERR_NULL),
     (linear, dict(space=None), Q4_ERR_NULL), (linear, dict(y=None), Q4_ERR_NULL), (linear, dict(type=2), Q4_ERR_SHAPE),
     (linear, dict(m=0), Q4_ERR_SHAPE), (linear, dict(k=16, stride=16), Q4_ERR_SHAPE), (linear, dict(stride=4064), Q4_ERR_SHAPE),
@@ -84,21 +86,25 @@ def test_refusals(L, call, bad, code):
 
 def test_workspace_size(L):
     for bad in ((0, 5, 64), (3, 0, 64), (3, 5, 0), (3, 5, 48), (-1, 5, 64), (1 << 25, 5, 64)):
-        assert L.mx4_linear_workspace_size(*bad) == 0
+        assert L.mx4_linear_workspace_size(*bad) == 0 and L.mx4_matmul_workspace_size(*bad) == 0
     for m, n, k in ((17, 100, 4096), (33, 5, 288), (2048, 11008, 4096)):
         size = mxfp4.workspace_size(m, n, k)
         assert size >= m * k // 2 + -(-k // 256) * 8 * m
         assert linear(L, m=m, n=n, k=k, stride=k, size=size - 1) == Q4_ERR_SHAPE
         assert linear(L, m=m, n=n, k=k, stride=k, space=None) == Q4_ERR_NULL
     assert mxfp4.workspace_size(1, 4096, 4096) == 0          # quantized on the way
+    assert mxfp4.workspace_size(2048, 11008, 4096, linear=False) == 0
+    parts = mxfp4.workspace_size(64, 300, 28672, linear=False)
+    assert parts >= 2 * 64 * 300 * 4 and mxfp4.workspace_size(64, 300, 28672) >= parts + 64 * 28672 * 17 // 32
 
 
 def test_config_reports_every_kernel(L):
     """Each kernel that the rules can choose, at sizes that the GPU tests run."""
     names = {mxfp4.kernel_config(m, n, k, linear=linear) for m, n, k in KERNELS for linear in (True, False)}
     for want in ("mx4_rows_kernel<0, 1, 0>", "mx4_quantize_kernel<0>, mx4_rows_kernel<0, 1, -1>", "mx4_rows_kernel<0, 2, -1>",
-                 "mx4_rows_kernel<0, 2, 0>", "mx4_tile_kernel<0, 1, 1, 4>", "mx4_tile_kernel<0, 2, 1, 3>", "mx4_tile_kernel<0, 2, 2, 3>",
-                 "mx4_tile_kernel<0, 2, 2, 2>", "mx4_tile_kernel<0, 3, 4, 2>", "mx4_tile_kernel<0, 4, 4, 2>"):
+                 "mx4_rows_kernel<0, 2, 0>", "mx4_tile_kernel<0, 1, 1, 4, false>", "mx4_tile_kernel<0, 2, 1, 3, false>",
+                 "mx4_tile_kernel<0, 2, 2, 3, false>", "mx4_tile_kernel<0, 2, 2, 2, false>", "mx4_tile_kernel<0, 3, 4, 2, false>",
+                 "mx4_tile_kernel<0, 4, 4, 2, false>", "mx4_tile_kernel<0, 1, 1, 4, true>, mx4_join_kernel<0>"):
         assert want in names, want
     assert mxfp4.kernel_config(1, 64, 64, torch.bfloat16) == "mx4_rows_kernel<1, 1, 1>"
     buf = __import__("ctypes").create_string_buffer(8)

@@ -86,7 +86,8 @@ SIGNATURES = {
 MX4_SIGNATURES = {
     "mx4_quantize": (ctypes.c_int, [_p, _i32, _i64, _i64, _i64, _p, _p, _p]),
     "mx4_dequantize": (ctypes.c_int, [_p, _p, _i64, _i64, _i32, _p, _p]),
-    "mx4_matmul": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _p]),
+    "mx4_matmul": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p, _p]),
+    "mx4_matmul_workspace_size": (_i64, [_i64, _i64, _i64]),
     "mx4_linear_workspace_size": (_i64, [_i64, _i64, _i64]),
     "mx4_linear": (ctypes.c_int, [_p, _i32, _i64, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _p]),
     "mx4_linear_config": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, ctypes.c_char_p, _i64]),

@@ -118,10 +118,13 @@ __global__ __launch_bounds__(64 * kRowWaves, 4) void mx4_rows_kernel(const void 
 
 // 64 lanes x 16 bytes from memory to LDS at `lds` (lane after lane), without a stop in
 // registers.  In assembly, since the compiler makes every LDS read of a wave wait for all
-// such loads that the wave has on their way; the barrier that ends a stage waits for them.
+// such loads that the wave has on their way; the barrier that ends a stage waits for them.  A load may not take a
+// scalar register that a vector instruction (readfirstlane) wrote less than five instructions before, which the compiler does
+// not see to here: PAUSE of them for a buffer that was just made, none for one that is `fixed`.
+template <int PAUSE>
 __device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff)
 {
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" : : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff) : "memory");
+    asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" : : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff), "n"(PAUSE) : "memory");
 }
 
 __device__ __forceinline__ u32x4 buffer_of(const void *p, uint32_t bytes)
@@ -132,71 +135,143 @@ __device__ __forceinline__ u32x4 buffer_of(const void *p, uint32_t bytes)
                  (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)kBufferFlags};
 }
 
+// The same value, in scalar registers from here on.
+__device__ __forceinline__ u32x4 fixed(u32x4 rsrc)
+{
+    asm volatile("s_nop 4" : "+s"(rsrc));
+    return rsrc;
+}
+
+// What the kernels of many rows have in LDS: a tile of BM rows of x and BN of W, of which a stage is 256
+// elements of every row, 128 bytes, and their scales.  Four waves load it in PIECES instructions each.
+template <int BM, int BN>
+struct Stages {
+    static constexpr int XSL = (BM + 127) / 128, WSL = (BN + 127) / 128;                        // loads of scales: 128 rows each
+    static constexpr int X = 0, W = BM * 128, XS = W + BN * 128, WS = XS + XSL * 1024, SIZE = WS + WSL * 1024;
+    static constexpr int XL = BM / 32, WL = BN / 32, PIECES = XL + WL + 1;                      // loads of a wave: 8 rows each
+    int m0, n0, rows_m, rows_n, steps, lane, wave;
+    uint32_t lds0;
+    u32x4 xr, wr;
+    uint32_t xoff[XL], woff[WL];
+    const uint8_t *scales;               // of this wave's load of scales: its rows', a step's distance, how many there are
+    int64_t scale_step;
+    uint32_t scale_bytes, scale_part, scale_at;
+
+    // Lane i of a load puts 16 bytes at row i / 8, place i % 8, where swz puts another chunk of the row.
+    __device__ __forceinline__ Stages(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int m, int n_out,
+                                      int k, int tile_m, int tile_n, char *smem)
+        : m0(tile_m * BM), n0(tile_n * BN)
+    {
+        rows_m = min(BM, m - m0);
+        rows_n = min(BN, n_out - n0);
+        steps = (k + 255) / 256;
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
+        const int pitch = k / 2;
+        xr = fixed(buffer_of(xc + (int64_t)m0 * pitch, (uint32_t)rows_m * pitch));
+        wr = fixed(buffer_of(wc + (int64_t)n0 * pitch, (uint32_t)rows_n * pitch));
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            const int r = (wave * XL + i) * 8 + (lane >> 3);
+            xoff[i] = (uint32_t)min(r, rows_m - 1) * pitch + ((lane & 7) ^ swz(r)) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < WL; ++i) {
+            const int r = (wave * WL + i) * 8 + (lane >> 3);
+            woff[i] = (uint32_t)min(r, rows_n - 1) * pitch + ((lane & 7) ^ swz(r)) * 16;
+        }
+        // a wave with no part of its own repeats one, so that all have as many loads on their way
+        const int turn = wave % (XSL + WSL);
+        const bool of_x = turn < XSL;
+        scale_part = (of_x ? turn : turn - XSL) * 1024;
+        scale_at = (of_x ? XS : WS) + scale_part;
+        scales = of_x ? xs + (int64_t)m0 * 8 : ws + (int64_t)n0 * 8;
+        scale_step = (int64_t)(of_x ? m : n_out) * 8;
+        scale_bytes = (of_x ? rows_m : rows_n) * 8;
+    }
+
+    // Piece p of stage s; from stage `end` on the buffers are empty and nothing is read.
+    __device__ __forceinline__ void load(int s, int end, int buf, int p) const
+    {
+        const uint32_t at = lds0 + buf * SIZE;
+        const bool there = s < end;
+        if (p < XL) {
+            u32x4 b = xr;
+            b[2] = there ? b[2] : 0u;
+            load_to_lds<0>(b, at + X + (wave * XL + p) * 1024, xoff[p], s * 128);
+        } else if (p < XL + WL) {
+            u32x4 b = wr;
+            b[2] = there ? b[2] : 0u;
+            load_to_lds<0>(b, at + W + (wave * WL + p - XL) * 1024, woff[p - XL], s * 128);
+        } else {
+            // what lies behind the tile's rows comes as zeros
+            load_to_lds<4>(buffer_of(scales + s * scale_step, there ? scale_bytes : 0), at + scale_at, scale_part + lane * 16, 0);
+        }
+    }
+};
+
+// Rows of a tile of y go through LDS (padded, so that a wave's rows lie in different banks) and leave as 16-byte pieces.
+template <int BN>
+constexpr int kRowOfY = BN * 2 + 16;
+
+// Four sums, channels c .. c + 3 of row `row` of the tile.
+template <int TYPE, int BN>
+__device__ __forceinline__ void put_y(char *tile, int row, int c, float a, float b, float d, float e)
+{
+    const uint32_t lo = Mx4Type<TYPE>::store(a) | (uint32_t)Mx4Type<TYPE>::store(b) << 16;
+    const uint32_t hi = Mx4Type<TYPE>::store(d) | (uint32_t)Mx4Type<TYPE>::store(e) << 16;
+    *reinterpret_cast<u32x2 *>(tile + row * kRowOfY<BN> + c * 2) = u32x2{lo, hi};
+}
+
+template <int BN>
+__device__ __forceinline__ void write_y(const char *tile, uint16_t *y, int m0, int n0, int rows_m, int n_out)
+{
+    const int cols = min(BN, n_out - n0);
+    uint16_t *out = y + (int64_t)m0 * n_out + n0;
+    if ((reinterpret_cast<uintptr_t>(y) & 15) == 0 && (n_out & 7) == 0) {
+        constexpr int CPR = BN / 8;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < rows_m * CPR; i += 256) {
+            const int row = i / CPR, c = i % CPR * 8;
+            if (c < cols)
+                *reinterpret_cast<u32x4 *>(out + (int64_t)row * n_out + c) =
+                    *reinterpret_cast<const u32x4 *>(tile + row * kRowOfY<BN> + c * 2);
+        }
+    } else {
+        // rows that begin anywhere: a wave's stores are still side by side
+#pragma unroll 8
+        for (int i = threadIdx.x; i < rows_m * BN; i += 256) {
+            const int row = i / BN, c = i % BN;
+            if (c < cols) out[(int64_t)row * n_out + c] = *reinterpret_cast<const uint16_t *>(tile + row * kRowOfY<BN> + c * 2);
+        }
+    }
+}
+
 // Many rows of x: a workgroup has BM = 64 TM rows of x and BN = 64 TN of W, each of its four
-// waves (one a SIMD, two by two) a quarter of them as TM x TN blocks of 32 x 32.  A stage is
-// 256 elements of every row, 128 bytes, and their scales; two stages in LDS.  A wave reads
+// waves (one a SIMD, two by two) a quarter of them as TM x TN blocks of 32 x 32; NB stages in LDS.  A wave reads
 // the operands of the next 64 elements between the matrix instructions of these ones.  In
 // the middle of a stage's last ones every wave has all it needs of the stage and the next one
 // has come in: one barrier, and the stage after that is sent for, a whole stage ahead.  Where k ends inside a stage,
 // the codes behind it are the next row's or zeros; their scales are made 2^-127 on both sides, and such products vanish
 // in any sum.
-template <int TYPE, int TM, int TN, int NB>
+template <int TYPE, int TM, int TN, int NB, bool PARTS>
 __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restrict__ xc, const uint8_t *__restrict__ xs,
                                                           const uint8_t *__restrict__ wc, const uint8_t *__restrict__ ws,
-                                                          int m, int n_out, int k, uint16_t *__restrict__ y, int tiles_m,
-                                                          int tiles_n)
+                                                          int m, int n_out, int k, void *__restrict__ to, int tiles_m,
+                                                          int tiles_n, int splits)
 {
-    constexpr int BM = 64 * TM, BN = 64 * TN;
-    constexpr int XSL = (BM + 127) / 128, WSL = (BN + 127) / 128;        // loads of scales: 128 rows each
-    constexpr int X = 0, W = BM * 128, XS = W + BN * 128, WS = XS + XSL * 1024, STAGE = WS + WSL * 1024;
-    constexpr int XL = BM / 32, WL = BN / 32;                            // loads of a wave: 8 rows each
+    typedef Stages<64 * TM, 64 * TN> S;
+    constexpr int STAGE = S::SIZE, X = S::X, W = S::W, XS = S::XS, WS = S::WS, PIECES = S::PIECES;
     extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tiles = tiles_m * tiles_n, tile = PARTS ? (int)blockIdx.x % tiles : (int)blockIdx.x;
     int tile_m, tile_n;
-    xcd_tile<4>(blockIdx.x, tiles_m, tiles_n, tile_m, tile_n);
-    const int m0 = tile_m * BM, n0 = tile_n * BN;
-    const int rows_m = min(BM, m - m0), rows_n = min(BN, n_out - n0);
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int pitch = k / 2, steps = (k + 255) / 256;
-
-    // Loading: lane i of a load puts 16 bytes at row i / 8, place i % 8, where swz puts another chunk of the row.
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem;
-    const u32x4 xr = buffer_of(xc + (int64_t)m0 * pitch, (uint32_t)rows_m * pitch);
-    const u32x4 wr = buffer_of(wc + (int64_t)n0 * pitch, (uint32_t)rows_n * pitch);
-    uint32_t xoff[XL], woff[WL];
-#pragma unroll
-    for (int i = 0; i < XL; ++i) {
-        const int r = (wave * XL + i) * 8 + (lane >> 3);
-        xoff[i] = (uint32_t)min(r, rows_m - 1) * pitch + ((lane & 7) ^ swz(r)) * 16;
-    }
-#pragma unroll
-    for (int i = 0; i < WL; ++i) {
-        const int r = (wave * WL + i) * 8 + (lane >> 3);
-        woff[i] = (uint32_t)min(r, rows_n - 1) * pitch + ((lane & 7) ^ swz(r)) * 16;
-    }
-    // Piece p of stage s; behind the last stage the buffers are empty and nothing is read.
-    constexpr int PIECES = XL + WL + 1;
-    auto load = [&](int s, int buf, int p) {
-        const uint32_t at = lds0 + buf * STAGE;
-        const bool there = s < steps;
-        if (p < XL) {
-            u32x4 b = xr;
-            b[2] = there ? b[2] : 0u;
-            load_to_lds(b, at + X + (wave * XL + p) * 1024, xoff[p], s * 128);
-        } else if (p < XL + WL) {
-            u32x4 b = wr;
-            b[2] = there ? b[2] : 0u;
-            load_to_lds(b, at + W + (wave * WL + p - XL) * 1024, woff[p - XL], s * 128);
-        } else {
-            // what lies behind the tile's rows comes as zeros; a wave with no part of its own repeats one, so
-            // that all have as many loads on their way
-            const int turn = wave % (XSL + WSL);
-            const bool of_x = turn < XSL;
-            const int part = of_x ? turn : turn - XSL;
-            const uint8_t *from = of_x ? xs + ((int64_t)s * m + m0) * 8 : ws + ((int64_t)s * n_out + n0) * 8;
-            load_to_lds(buffer_of(from, there ? (of_x ? rows_m : rows_n) * 8 : 0), at + (of_x ? XS : WS) + part * 1024,
-                        part * 1024 + lane * 16, 0);
-        }
-    };
+    xcd_tile<4>(tile, tiles_m, tiles_n, tile_m, tile_n);
+    const S st(xc, xs, wc, ws, m, n_out, k, tile_m, tile_n, smem);
+    const int lane = st.lane, wave = st.wave, steps = st.steps;
+    const int split = PARTS ? (int)blockIdx.x / tiles : 0;               // stages first .. end - 1 are this workgroup's
+    const int first = PARTS ? split * steps / splits : 0, end = PARTS ? (split + 1) * steps / splits : steps;
+    auto load = [&](int s, int buf, int p) { st.load(s, end, buf, p); };
 
     // Operands: lane (r, g) has blocks 4 g + j of its row for the j-th quarter of a stage, their scales in a word.
     const int r = lane & 31, g = lane >> 5, wm = wave >> 1, wn = wave & 1;
@@ -290,34 +365,41 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
 #pragma unroll
         for (int s = 0; s < NB - 1; ++s)
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i) load(s, s, i);
+            for (int i = 0; i < PIECES; ++i) load(first + s, s, i);
         wait_vmem<(NB - 2) * PIECES>();
         barrier_keep_vmem();
 #pragma unroll
-        for (int i = 0; i < FIRST; ++i) load(NB - 1, NB - 1, i);
+        for (int i = 0; i < FIRST; ++i) load(first + NB - 1, NB - 1, i);
 #pragma unroll
         for (int i = 0; i < PART; ++i) {
             read(f0, 0, 0, i);
             read_scale(s0, 0, i);
         }
-        int s = 0, last = NB - 1, buf = 0, after = 1;
+        int s = first, last = NB - 1, buf = 0, after = 1;
         auto on = [&] {
             last = buf;
             buf = after;
             after = after + 1 == NB ? 0 : after + 1;
         };
-        for (; s + 2 <= steps; s += 2) {
+        for (; s + 2 <= end; s += 2) {
             stage(s, last, buf, after, s0, s1);
             on();
             stage(s + 1, last, buf, after, s1, s0);
             on();
         }
-        if (s < steps) stage(s, last, buf, after, s0, s1);
+        if (s < end) stage(s, last, buf, after, s0, s1);
         wait_vmem<0>();
     }
-    // y goes through LDS (rows padded to YS bytes) and leaves as 16-byte pieces of whole rows.
-    constexpr int YS = BN * 2 + 16;
-    static_assert(BM * YS <= NB * STAGE, "output tile exceeds LDS");
+    if constexpr (PARTS) {
+        // the sums as the lanes have them, block after block of 32 x 32
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            static_cast<f32x4 *>(to)[(((int64_t)blockIdx.x * 4 + wave) * 4 + q) * 64 + lane] =
+                f32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+        return;
+    }
+    static_assert(!PARTS || ALL == 1, "the joining kernel takes tiles of 64 x 64");
+    static_assert(64 * TM * kRowOfY<64 * TN> <= NB * STAGE, "output tile exceeds LDS");
     __syncthreads();
 #pragma unroll
     for (int a = 0; a < TM; ++a)
@@ -326,29 +408,42 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const f32x16 &v = acc[a][b];
-                const uint32_t lo = Mx4Type<TYPE>::store(v[4 * q]) | (uint32_t)Mx4Type<TYPE>::store(v[4 * q + 1]) << 16;
-                const uint32_t hi = Mx4Type<TYPE>::store(v[4 * q + 2]) | (uint32_t)Mx4Type<TYPE>::store(v[4 * q + 3]) << 16;
-                *reinterpret_cast<u32x2 *>(smem + (xrow + 32 * a) * YS + (wn * 32 * TN + 32 * b + 8 * q + 4 * g) * 2) =
-                    u32x2{lo, hi};
+                put_y<TYPE, 64 * TN>(smem, xrow + 32 * a, wn * 32 * TN + 32 * b + 8 * q + 4 * g, v[4 * q], v[4 * q + 1], v[4 * q + 2],
+                                     v[4 * q + 3]);
             }
     __syncthreads();
-    const int cols = min(BN, n_out - n0);
-    uint16_t *out = y + (int64_t)m0 * n_out + n0;
-    if ((reinterpret_cast<uintptr_t>(y) & 15) == 0 && (n_out & 7) == 0) {
-        constexpr int CPR = BN / 8;
-#pragma unroll 4
-        for (int i = tid; i < rows_m * CPR; i += 256) {
-            const int row = i / CPR, c = i % CPR * 8;
-            if (c < cols)
-                *reinterpret_cast<u32x4 *>(out + (int64_t)row * n_out + c) = *reinterpret_cast<const u32x4 *>(smem + row * YS + c * 2);
-        }
-    } else {
-        // rows that begin anywhere: a wave's stores are still side by side
+    write_y<64 * TN>(smem, static_cast<uint16_t *>(to), st.m0, st.n0, st.rows_m, n_out);
+}
+
+// y from the sums of mx4_tile_kernel<TYPE, 1, 1, NB, true>, always added up in this order: a workgroup has a block of 32 x 32.
+template <int TYPE>
+__global__ __launch_bounds__(256) void mx4_join_kernel(const f32x4 *__restrict__ parts, int splits, int m, int n_out,
+                                                       uint16_t *__restrict__ y, int tiles_m, int tiles_n)
+{
+    const int64_t next = (int64_t)tiles_m * tiles_n * 1024;
+    const f32x4 *p = parts + (int64_t)blockIdx.x * 256 + threadIdx.x;
+    f32x4 sum = p[0];
 #pragma unroll 8
-        for (int i = tid; i < rows_m * BN; i += 256) {
-            const int row = i / BN, c = i % BN;
-            if (c < cols) out[(int64_t)row * n_out + c] = *reinterpret_cast<const uint16_t *>(smem + row * YS + c * 2);
-        }
+    for (int i = 1; i < splits; ++i) {
+        const f32x4 v = p[i * next];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] += v[e];
+    }
+    int tile_m, tile_n;
+    xcd_tile<4>(blockIdx.x / 4, tiles_m, tiles_n, tile_m, tile_n);
+    const int wave = blockIdx.x & 3, lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int row = tile_m * 64 + (wave >> 1) * 32 + (lane & 31), c = tile_n * 64 + (wave & 1) * 32 + q * 8 + (lane >> 5) * 4;
+    if (row >= m || c >= n_out) return;
+    uint16_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = Mx4Type<TYPE>::store(sum[e]);
+    uint16_t *to = y + (int64_t)row * n_out + c;
+    if ((reinterpret_cast<uintptr_t>(y) & 7) == 0 && (n_out & 3) == 0) {
+        *reinterpret_cast<u32x2 *>(to) = u32x2{(uint32_t)v[0] | (uint32_t)v[1] << 16, (uint32_t)v[2] | (uint32_t)v[3] << 16};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < n_out) to[e] = v[e];
     }
 }
 
@@ -356,13 +451,28 @@ template <int TYPE, int TM, int TN, int NB>
 hipError_t launch_tiles(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int m, int n_out,
                         int k, uint16_t *y, hipStream_t stream)
 {
-    constexpr int LDS = NB * (64 * (TM + TN) * 128 + ((TM + 1) / 2 + (TN + 1) / 2) * 1024);
-    auto kernel = mx4_tile_kernel<TYPE, TM, TN, NB>;
+    constexpr int LDS = NB * Stages<64 * TM, 64 * TN>::SIZE;
+    auto kernel = mx4_tile_kernel<TYPE, TM, TN, NB, false>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     if (e != hipSuccess) return e;
     const int tiles_m = (m + 64 * TM - 1) / (64 * TM), tiles_n = (n_out + 64 * TN - 1) / (64 * TN);
-    kernel<<<(unsigned)(tiles_m * tiles_n), 256, LDS, stream>>>(xc, xs, wc, ws, m, n_out, k, y, tiles_m, tiles_n);
+    kernel<<<(unsigned)(tiles_m * tiles_n), 256, LDS, stream>>>(xc, xs, wc, ws, m, n_out, k, y, tiles_m, tiles_n, 1);
+    return hipGetLastError();
+}
+
+template <int TYPE>
+hipError_t launch_parts(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int m, int n_out,
+                        int k, int splits, f32x4 *parts, uint16_t *y, hipStream_t stream)
+{
+    constexpr int LDS = 4 * Stages<64, 64>::SIZE;
+    auto kernel = mx4_tile_kernel<TYPE, 1, 1, 4, true>;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+    if (e != hipSuccess) return e;
+    const int tiles_m = (m + 63) / 64, tiles_n = (n_out + 63) / 64, tiles = tiles_m * tiles_n;
+    kernel<<<(unsigned)(tiles * splits), 256, LDS, stream>>>(xc, xs, wc, ws, m, n_out, k, parts, tiles_m, tiles_n, splits);
+    mx4_join_kernel<TYPE><<<(unsigned)(tiles * 4), 256, 0, stream>>>(parts, splits, m, n_out, y, tiles_m, tiles_n);
     return hipGetLastError();
 }
 
@@ -385,9 +495,9 @@ hipError_t launch_rows(const void *x, const uint8_t *xs, int64_t stride, const u
 }
 
 // How a product is run: by mx4_rows_kernel (tm == 0; at most 32 rows of x), or by tiles of 64 tm x 64 tn
-// with nb stages in LDS.
+// with nb stages in LDS, in `splits` parts of k that mx4_join_kernel adds up.
 struct Plan {
-    int tm, tn, nb;
+    int tm, tn, nb, splits;
 };
 
 struct TileCost {
@@ -396,30 +506,47 @@ struct TileCost {
     double start, alone, full;       // us: a tile's beginning and end; a stage with few and with all CUs busy
 };
 
-// Measured with 64 to 4096 rows of x, n_out from 1024 to 28672, k from 1024 to 8192; off by 10 % at most where it
-// matters.  (us, the kernels below in order: 64 x 8192 x 8192 12.5, 15.3, 18.2, 26.9, 37.3, 42.3; 512 x 11008 x 4096
-// 30.9, 21.7, 22.7, 18.3, 22.2, 25.8; 2048 x 11008 x 4096 94.8, 70.8, 67.0, 57.6, 53.0, 58.4; 8192^3 497, 398, 358, 306,
-// 271, 244.)
+// Measured at 750 sizes: 17 to 4096 rows of x, n_out from 300 to 28672, k from 512 to 28672.  What these costs choose takes
+// 0.7 % longer than the fastest of all, 26 % at most.  (us, the tiles below in order: 64 x 8192 x 8192 12.5, 15.3,
+// 18.2, 26.9, 37.3, 42.3; 512 x 11008 x 4096 28.6, 22.6, 23.0, 19.7, 22.2, 25.8; 2048 x 11008 x 4096 94.8, 70.8, 67.0, 57.6, 53.0, 58.4;
+// 8192^3 497, 398, 358, 306, 271, 244.)
 constexpr TileCost kTiles[] = {
-    {{1, 1, 4}, 512, 3.0, 0.20, 0.47}, {{2, 1, 3}, 512, 3.3, 0.25, 0.74}, {{2, 2, 3}, 256, 3.7, 0.38, 0.60},
-    {{2, 2, 2}, 512, 4.0, 0.50, 1.10}, {{3, 4, 2}, 256, 5.0, 0.80, 1.38}, {{4, 4, 2}, 256, 6.0, 1.00, 1.78},
+    {{1, 1, 4, 1}, 512, 3.3, 0.26, 0.53}, {{2, 1, 3, 1}, 512, 3.3, 0.31, 0.79}, {{2, 2, 3, 1}, 256, 3.3, 0.38, 0.66},
+    {{2, 2, 2, 1}, 512, 2.9, 0.59, 1.30}, {{3, 4, 2, 1}, 256, 5.4, 1.00, 1.60}, {{4, 4, 2, 1}, 256, 7.0, 1.20, 2.00},
 };
 
 Plan plan_for(int64_t m, int64_t n_out, int64_t k)
 {
-    const double steps = (double)((k + 255) / 256);
+    const int64_t stages = (k + 255) / 256;
+    const double steps = (double)stages;
     const double memory = (double)(n_out * k) * 17 / 32 / 4.6e6;         // us, W at what a stream of it reaches
     Plan best = {};
     double least = 1e30;
     for (const TileCost &t : kTiles) {
         const int64_t bm = 64 * t.plan.tm, bn = 64 * t.plan.tn;
         const int64_t tiles = ((m + bm - 1) / bm) * ((n_out + bn - 1) / bn), full = tiles / t.slots, rest = tiles % t.slots;
+        // CUs that share an L2 get into each other's way the more the more of them are busy
+        const double part = (double)rest / t.slots;
         double cost = (double)full * (t.start + steps * t.full);
-        if (rest) cost += t.start + steps * (t.alone + (t.full - t.alone) * (double)rest / t.slots);
+        if (rest) cost += t.start + steps * (t.alone + (t.full - t.alone) * part * part);
         cost = std::max(cost, memory);
         if (cost < least) {
             least = cost;
             best = t.plan;
+        }
+    }
+    // Few tiles and a long k: one CU's loads bound a tile (64 x 64 x 256 elements in 0.26 us, whether two or seven stages are
+    // on their way), so more of them take parts of k, at the cost of a second launch and of their sums' way through memory
+    // (64 x 256 x 28672 32.0 us, in 12 parts 9.2; 64 x 8192 x 28672 41.7, in 2 parts 30.4; 64 x 4096 x 4096 7.6, in 2 parts 8.7).
+    const int64_t tiles = ((m + 63) / 64) * ((n_out + 63) / 64);
+    for (const int splits : {2, 3, 4, 6, 8, 12, 16}) {
+        if (tiles * splits > 512 || splits > stages) break;
+        const double part = (double)(tiles * splits) / 512;
+        const double one = 3.3 + (double)((stages + splits - 1) / splits) * (0.26 + 0.27 * part * part);
+        const double cost = std::max(one, memory) + 1.8 + 0.1 * splits + 5.3 * part;
+        if (cost < least) {
+            least = cost;
+            best = {1, 1, 4, splits};
         }
     }
     // 16 rows of W a workgroup: most workgroups where there are few rows of x, but x comes once for each (1 x 4096 x
@@ -428,7 +555,7 @@ Plan plan_for(int64_t m, int64_t n_out, int64_t k)
         const double groups = (double)((n_out + 15) / 16), rounds = std::max(1.0, groups / 512);
         const double slope = (0.065 + 0.0043 * (double)m) * (1.0 + 1.3 * std::min(1.0, groups / 512));
         const double cost = 2.5 + steps * slope * rounds + 0.8 * (rounds - 1.0);
-        if (std::max(cost, memory) < least) best = {0, 0, 0};
+        if (std::max(cost, memory) < least) best = {0, 0, 0, 1};
     }
     return best;
 }
@@ -437,10 +564,17 @@ Plan plan_for(int64_t m, int64_t n_out, int64_t k)
 // itself (1 x 8192 x 8192 10.9 us, 12.4 in two launches; 4 x 4096 x 4096 6.0 and 6.4; 8 x 4096 x 4096 8.0 and 6.8).
 bool quantizes_itself(const Plan &p, int64_t m, int64_t k) { return p.tm == 0 && m * k <= 16384; }
 
+// Bytes of the parts' sums.
+int64_t part_bytes(const Plan &p, int64_t m, int64_t n_out)
+{
+    return p.splits > 1 ? p.splits * ((m + 63) / 64) * ((n_out + 63) / 64) * 16384 : 0;
+}
+
 template <int TYPE>
 hipError_t launch(const Plan &p, const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int m,
-                  int n_out, int k, uint16_t *y, hipStream_t stream)
+                  int n_out, int k, void *parts, uint16_t *y, hipStream_t stream)
 {
+    if (p.splits > 1) return launch_parts<TYPE>(xc, xs, wc, ws, m, n_out, k, p.splits, (f32x4 *)parts, y, stream);
     if (p.tm == 0)
         return m <= 16 ? launch_rows<TYPE, 1, -1>(xc, xs, 0, wc, ws, m, n_out, k, y, stream)
                        : launch_rows<TYPE, 2, -1>(xc, xs, 0, wc, ws, m, n_out, k, y, stream);
@@ -457,33 +591,37 @@ hipError_t launch(const Plan &p, const uint8_t *xc, const uint8_t *xs, const uin
 
 template <int TYPE>
 hipError_t launch_linear(const void *x, int64_t stride, const uint8_t *wc, const uint8_t *ws, int m, int n_out, int k,
-                         uint8_t *codes, uint8_t *scales, uint16_t *y, hipStream_t stream)
+                         uint8_t *codes, uint8_t *scales, void *parts, uint16_t *y, hipStream_t stream)
 {
     const Plan p = plan_for(m, n_out, k);
     if (quantizes_itself(p, m, k))
         return m <= 16 ? launch_rows<TYPE, 1, TYPE>(x, nullptr, stride, wc, ws, m, n_out, k, y, stream)
                        : launch_rows<TYPE, 2, TYPE>(x, nullptr, stride, wc, ws, m, n_out, k, y, stream);
     const hipError_t e = mx4_launch_quantize(x, TYPE, m, k, stride, codes, scales, stream);
-    return e != hipSuccess ? e : launch<TYPE>(p, codes, scales, wc, ws, m, n_out, k, y, stream);
+    return e != hipSuccess ? e : launch<TYPE>(p, codes, scales, wc, ws, m, n_out, k, parts, y, stream);
 }
 
 }  // namespace
 
 hipError_t mx4_launch_matmul(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int64_t m,
-                             int64_t n_out, int64_t k, int type, void *y, hipStream_t stream)
+                             int64_t n_out, int64_t k, int type, void *parts, void *y, hipStream_t stream)
 {
     auto f = type == MX4_F16 ? launch<MX4_F16> : launch<MX4_BF16>;
-    return f(plan_for(m, n_out, k), xc, xs, wc, ws, (int)m, (int)n_out, (int)k, (uint16_t *)y, stream);
+    return f(plan_for(m, n_out, k), xc, xs, wc, ws, (int)m, (int)n_out, (int)k, parts, (uint16_t *)y, stream);
 }
 
 hipError_t mx4_launch_linear(const void *x, int type, int64_t stride, const uint8_t *wc, const uint8_t *ws, int64_t m,
-                             int64_t n_out, int64_t k, uint8_t *codes, uint8_t *scales, void *y, hipStream_t stream)
+                             int64_t n_out, int64_t k, uint8_t *codes, uint8_t *scales, void *parts, void *y, hipStream_t stream)
 {
     auto f = type == MX4_F16 ? launch_linear<MX4_F16> : launch_linear<MX4_BF16>;
-    return f(x, stride, wc, ws, (int)m, (int)n_out, (int)k, codes, scales, (uint16_t *)y, stream);
+    return f(x, stride, wc, ws, (int)m, (int)n_out, (int)k, codes, scales, parts, (uint16_t *)y, stream);
 }
 
-bool mx4_linear_needs_room(int64_t m, int64_t n_out, int64_t k) { return !quantizes_itself(plan_for(m, n_out, k), m, k); }
+Mx4Room mx4_room(int64_t m, int64_t n_out, int64_t k)
+{
+    const Plan p = plan_for(m, n_out, k);
+    return {!quantizes_itself(p, m, k), part_bytes(p, m, n_out)};
+}
 
 void mx4_linear_name(int64_t m, int64_t n_out, int64_t k, int type, bool linear, char *name, int64_t name_len)
 {
@@ -492,5 +630,6 @@ void mx4_linear_name(int64_t m, int64_t n_out, int64_t k, int type, bool linear,
     const char *first = "";
     if (linear && !self) first = type == MX4_F16 ? "mx4_quantize_kernel<0>, " : "mx4_quantize_kernel<1>, ";
     if (p.tm == 0) snprintf(name, (size_t)name_len, "%smx4_rows_kernel<%d, %d, %d>", first, type, m <= 16 ? 1 : 2, self ? type : -1);
-    else snprintf(name, (size_t)name_len, "%smx4_tile_kernel<%d, %d, %d, %d>", first, type, p.tm, p.tn, p.nb);
+    else if (p.splits > 1) snprintf(name, (size_t)name_len, "%smx4_tile_kernel<%d, 1, 1, 4, true>, mx4_join_kernel<%d>", first, type, type);
+    else snprintf(name, (size_t)name_len, "%smx4_tile_kernel<%d, %d, %d, %d, false>", first, type, p.tm, p.tn, p.nb);
 }

@@ -578,21 +578,33 @@ int mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, in
     return finish(mx4_launch_dequantize(codes, scales, rows, k, type, out, (hipStream_t)stream));
 }
 
+int64_t mx4_matmul_workspace_size(int64_t m, int64_t n_out, int64_t k)
+{
+    if (check_mx4_shape(m, k) || check_mx4_shape(n_out, k) || m * n_out > kMaxElems) return 0;
+    return mx4_room(m, n_out, k).parts;
+}
+
 int mx4_matmul(const uint8_t *x_codes, const uint8_t *x_scales, const uint8_t *w_codes, const uint8_t *w_scales,
-               int64_t m, int64_t n_out, int64_t k, int32_t type, void *y, void *stream)
+               int64_t m, int64_t n_out, int64_t k, int32_t type, void *workspace, int64_t workspace_bytes, void *y,
+               void *stream)
 {
     if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return Q4_ERR_NULL;
     if (check_mx4_shape(m, k) || check_mx4_shape(n_out, k) || m * n_out > kMaxElems || type < MX4_F16 || type > MX4_BF16)
         return Q4_ERR_SHAPE;
-    if (!aligned(x_codes, 16) || !aligned(x_scales, 8) || !aligned(w_codes, 16) || !aligned(w_scales, 8) || !aligned(y, 2))
+    const int64_t need = mx4_room(m, n_out, k).parts;
+    if (need && !workspace) return Q4_ERR_NULL;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 8) || !aligned(w_codes, 16) || !aligned(w_scales, 8) ||
+        !aligned(workspace, 16) || !aligned(y, 2))
         return Q4_ERR_ALIGN;
-    return finish(mx4_launch_matmul(x_codes, x_scales, w_codes, w_scales, m, n_out, k, type, y, (hipStream_t)stream));
+    if (workspace_bytes < need) return Q4_ERR_SHAPE;
+    return finish(mx4_launch_matmul(x_codes, x_scales, w_codes, w_scales, m, n_out, k, type, workspace, y, (hipStream_t)stream));
 }
 
 int64_t mx4_linear_workspace_size(int64_t m, int64_t n_out, int64_t k)
 {
     if (check_mx4_shape(m, k) || check_mx4_shape(n_out, k) || m * n_out > kMaxElems) return 0;
-    return mx4_linear_needs_room(m, n_out, k) ? mx4_code_bytes(m, k) + mx4_scale_bytes(m, k) : 0;
+    const Mx4Room room = mx4_room(m, n_out, k);
+    return (room.x ? mx4_code_bytes(m, k) + mx4_scale_bytes(m, k) : 0) + room.parts;
 }
 
 int mx4_linear(const void *x, int32_t type, int64_t stride, const uint8_t *w_codes, const uint8_t *w_scales, int64_t m,
@@ -602,12 +614,14 @@ int mx4_linear(const void *x, int32_t type, int64_t stride, const uint8_t *w_cod
     if (check_mx4_shape(m, k) || check_mx4_shape(n_out, k) || m * n_out > kMaxElems || type < MX4_F16 || type > MX4_BF16)
         return Q4_ERR_SHAPE;
     if (int rc = check_mx4_rows(x, type, m, k, stride)) return rc;
-    const int64_t need = mx4_linear_workspace_size(m, n_out, k);
+    const Mx4Room room = mx4_room(m, n_out, k);
+    const int64_t of_x = room.x ? mx4_code_bytes(m, k) + mx4_scale_bytes(m, k) : 0, need = of_x + room.parts;
     if (need && !workspace) return Q4_ERR_NULL;
     if (!aligned(w_codes, 16) || !aligned(w_scales, 8) || !aligned(workspace, 16) || !aligned(y, 2)) return Q4_ERR_ALIGN;
     if (workspace_bytes < need) return Q4_ERR_SHAPE;
-    uint8_t *codes = need ? (uint8_t *)workspace : nullptr, *scales = need ? codes + mx4_code_bytes(m, k) : nullptr;
-    return finish(mx4_launch_linear(x, type, stride, w_codes, w_scales, m, n_out, k, codes, scales, y, (hipStream_t)stream));
+    uint8_t *codes = room.x ? (uint8_t *)workspace : nullptr, *scales = room.x ? codes + mx4_code_bytes(m, k) : nullptr;
+    void *parts = room.parts ? (uint8_t *)workspace + of_x : nullptr;
+    return finish(mx4_launch_linear(x, type, stride, w_codes, w_scales, m, n_out, k, codes, scales, parts, y, (hipStream_t)stream));
 }
 
 int mx4_linear_config(int64_t m, int64_t n_out, int64_t k, int32_t type, int32_t linear, char *name, int64_t name_len)

@@ -81,11 +81,16 @@ hipError_t mx4_launch_quantize(const void *x, int type, int64_t rows, int64_t k,
 hipError_t mx4_launch_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t k, int type,
                                  void *out, hipStream_t stream);
 hipError_t mx4_launch_matmul(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc, const uint8_t *ws, int64_t m,
-                             int64_t n_out, int64_t k, int type, void *y, hipStream_t stream);
-// Whether mx4_launch_linear needs room for the quantized x: `codes` and `scales`.
-bool mx4_linear_needs_room(int64_t m, int64_t n_out, int64_t k);
+                             int64_t n_out, int64_t k, int type, void *parts, void *y, hipStream_t stream);
+// What a product needs: whether mx4_launch_linear has room for the quantized x (`codes`, `scales`), and bytes of `parts`.
+struct Mx4Room {
+    bool x;
+    int64_t parts;
+};
+Mx4Room mx4_room(int64_t m, int64_t n_out, int64_t k);
 hipError_t mx4_launch_linear(const void *x, int type, int64_t stride, const uint8_t *wc, const uint8_t *ws, int64_t m,
-                             int64_t n_out, int64_t k, uint8_t *codes, uint8_t *scales, void *y, hipStream_t stream);
+                             int64_t n_out, int64_t k, uint8_t *codes, uint8_t *scales, void *parts, void *y,
+                             hipStream_t stream);
 // The kernels of mx4_launch_matmul or, if `linear`, mx4_launch_linear.
 void mx4_linear_name(int64_t m, int64_t n_out, int64_t k, int type, bool linear, char *name, int64_t name_len);
 

@@ -152,8 +152,21 @@ def dequantize(q, dtype=torch.float32, out=None):
     return out
 
 
-def matmul(x, w, dtype=torch.float16, out=None):
-    """y = x W^T of MXTensors x [m, k] and w [n_out, k], fp16 or bf16 [m, n_out]."""
+def _room(need, workspace, like):
+    """(bytes, address) of the caller's workspace, or of a new one where one is needed."""
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != like.device or not workspace.is_contiguous():
+            raise W4A16Error("workspace must be a contiguous tensor on x's GPU")
+        return workspace.numel() * workspace.element_size(), workspace.data_ptr(), workspace
+    if not need:
+        return 0, None, None
+    workspace = like.new_empty(need, dtype=torch.uint8)
+    return need, workspace.data_ptr(), workspace
+
+
+def matmul(x, w, dtype=torch.float16, out=None, workspace=None):
+    """y = x W^T of MXTensors x [m, k] and w [n_out, k], fp16 or bf16 [m, n_out].
+    workspace: at least workspace_size(m, n_out, k, linear=False) bytes, as for `linear`."""
     xc, xs, m, k = _parts(x, "x")
     wc, ws, n, wk = _parts(w, "w")
     if k != wk:
@@ -164,8 +177,9 @@ def matmul(x, w, dtype=torch.float16, out=None):
         raise W4A16Error(f"dtype must be float16 or bfloat16, got {dtype}")
     out = _output(out, xc, (m, n), dtype)
     if m and n:
+        size, at, _keep = _room(workspace_size(m, n, k, False), workspace, xc)
         _call("mx4_matmul", xc.get_device(), xc.data_ptr(), xs.data_ptr(), wc.data_ptr(), ws.data_ptr(), m, n, k,
-              _HALVES[dtype], out.data_ptr())
+              _HALVES[dtype], at, size, out.data_ptr())
     return out
 
 
@@ -183,15 +197,8 @@ def linear(x, w, out=None, workspace=None):
     out = _output(out, x, (m, n), x.dtype)
     if m == 0 or n == 0:
         return out
-    need, at = workspace_size(m, n, k), None
-    if workspace is not None:
-        if not isinstance(workspace, torch.Tensor) or workspace.device != x.device or not workspace.is_contiguous():
-            raise W4A16Error("workspace must be a contiguous tensor on x's GPU")
-        need, at = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-    elif need:
-        workspace = wc.new_empty(need)
-        at = workspace.data_ptr()
-    _call("mx4_linear", x.get_device(), x.data_ptr(), kind, stride, wc.data_ptr(), ws.data_ptr(), m, n, k, at, need,
+    size, at, _keep = _room(workspace_size(m, n, k), workspace, wc)
+    _call("mx4_linear", x.get_device(), x.data_ptr(), kind, stride, wc.data_ptr(), ws.data_ptr(), m, n, k, at, size,
           out.data_ptr())
     return out
 
@@ -207,7 +214,7 @@ def kernel_config(m, n_out, k, dtype=torch.float16, linear=True):
 
 
 @lru_cache(maxsize=4096)
-def workspace_size(m, n_out, k):
-    """Bytes of `linear`'s workspace for x [m, k] and w [n_out, k]: room for the quantized
-    x, none where the product quantizes it itself."""
-    return lib().mx4_linear_workspace_size(m, n_out, k)
+def workspace_size(m, n_out, k, linear=True):
+    """Bytes of `linear`'s (or `matmul`'s) workspace for x [m, k] and w [n_out, k]: room for the
+    quantized x and for the sums of a long k's parts; 0 where a call needs neither."""
+    return (lib().mx4_linear_workspace_size if linear else lib().mx4_matmul_workspace_size)(m, n_out, k)
