@@ -20,11 +20,11 @@ def i32(v):
 class Shared(World):
     """Groups of sequences over the same first pages, each with tokens of its own behind them."""
 
-    def __init__(self, c, seed=0, own=None):
+    def __init__(self, c, seed=0, own=None, pool=None):
         owns, self.new = lengths(c)
         owns = owns if own is None else own
         T, B, cols, G, most = sizes(c)
-        super().__init__(B, c.n_kv, c.d, c.page, most=(cols + 2) * c.page, seed=seed)
+        super().__init__(B, c.n_kv, c.d, c.page, pool=pool, most=(cols + 2) * c.page, seed=seed)
         self.cols = cols
         self.table = self.table[:, :cols].copy()
         self.c, self.cu = c, np.concatenate([[0], np.cumsum([n for _, n in c.groups])])
@@ -243,6 +243,15 @@ def test_captured_steps_and_changed_groups():
         for o in outs:
             assert torch.equal(o.view(torch.int16), want.view(torch.int16)), step
         w.check(x, want)
+
+
+@pytest.mark.parametrize("c", [Case(128, 64, 8, 64, ((5, 20),), 150, 1, 0), Case(128, 64, 8, 8, ((5, 3), (3, 2)), 150, 1, 0)])
+def test_pages_beyond_4_gib(c):
+    """Pools of 4.6 GB for K and for V, pages all over them."""
+    w = Shared(c, pool=70001)
+    assert int(w.table.max()) * 64 * 8 * 128 > 1 << 32
+    x, out, _ = run(w, w.prefix())
+    w.check(x, out, weights=weights(c))
 
 
 @pytest.mark.parametrize("seed", range(24))
