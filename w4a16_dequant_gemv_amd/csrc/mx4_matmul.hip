@@ -319,14 +319,14 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
         acc[a][b] = mx4_mfma32<j, j>(f.w[b], f.x[a], acc[a][b], s.w[b], s.x[a]);
     };
     // the products of quarter J, between them the reads of the next quarter and pieces LO .. HI - 1 of stage `to`
-    constexpr int FIRST = PIECES / 3;
+    constexpr int FIRST = PIECES / 3, EARLY = ALL > 1 ? ALL / 2 : 1, MEET = ALL / 4;
     auto quarter = [&](auto J, const Frag &f, const Scale &s, Frag &next, int buf, int to, int into, int lo, int hi) {
         constexpr int j = decltype(J)::value;
 #pragma unroll
         for (int t = 0; t < ALL; ++t) {
-            mma(J, f, s, t);
 #pragma unroll
-            for (int i = t * PART / ALL; i < (t + 1) * PART / ALL; ++i) read(next, buf, j + 1, i);
+            for (int i = t * PART / EARLY; i < min((t + 1) * PART / EARLY, PART); ++i) read(next, buf, j + 1, i);
+            mma(J, f, s, t);
 #pragma unroll
             for (int i = lo + t * (hi - lo) / ALL; i < lo + (t + 1) * (hi - lo) / ALL; ++i) load(to, into, i);
             __builtin_amdgcn_sched_barrier(0);
@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
         quarter(Q1{}, f1, now, f0, buf, 0, 0, 0, 0);
         quarter(Q2{}, f0, now, f1, buf, 0, 0, 0, 0);
 #pragma unroll
-        for (int t = 0; t < ALL / 2; ++t) {
+        for (int t = 0; t < MEET; ++t) {
             mma(Q3{}, f1, now, t);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -359,11 +359,11 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(const uint8_t *__restr
         barrier_keep_vmem();
         // behind the last stage old values are read and not used
 #pragma unroll
-        for (int t = ALL / 2; t < ALL; ++t) {
-            constexpr int HALF = ALL - ALL / 2;
-            const int u = t - ALL / 2;
+        for (int t = MEET; t < ALL; ++t) {
+            constexpr int HALF = ALL - MEET;
+            const int u = t - MEET;
 #pragma unroll
-            for (int i = u * PART / HALF; i < (u + 1) * PART / HALF; ++i) {
+            for (int i = u * PART / EARLY; i < min((u + 1) * PART / EARLY, PART); ++i) {
                 read(f0, after, 0, i);
                 read_scale(next, after, i);
             }
