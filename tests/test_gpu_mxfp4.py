@@ -156,3 +156,26 @@ def test_every_kernel(m, n, k):
         y = mxfp4.linear(x, qw)
         check_product(y, ref.values(*ref.quantize(exact(x))), w, mxfp4.kernel_config(m, n, k, dtype))
         assert torch.equal(y, mxfp4.matmul(mxfp4.quantize(x), qw, dtype))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_products(seed):
+    """Sizes from one row, channel or block to some thousands, x in rows apart, y anywhere, a workspace of the caller's."""
+    rng = np.random.default_rng(400 + seed)
+    size = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    m, n, k = size(1, 3000), size(1, 9000), 32 * size(1, 900)
+    while m * n * k > 2e9:
+        m, n = max(1, m // 2), max(1, n * 2 // 3)
+    dtype = (torch.float16, torch.bfloat16)[int(rng.integers(2))]
+    apart, off = 8 * int(rng.integers(0, 5)), int(rng.integers(0, 3))
+    print(m, n, k, dtype, mxfp4.kernel_config(m, n, k, dtype), flush=True)
+    qw, w = operand(n, k, seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((m, k + apart), generator=g, device="cuda").to(dtype)[:, :k]
+    room = torch.full((m * n + 8,), 7.0, dtype=dtype, device="cuda")
+    y = room[off:off + m * n].view(m, n)
+    ws = torch.full((mxfp4.workspace_size(m, n, k) + 16,), 255, dtype=torch.uint8, device="cuda")
+    mxfp4.linear(x, qw, out=y, workspace=ws)
+    check_product(y, ref.values(*ref.quantize(exact(x))), w)
+    assert bool((room[:off] == 7).all()) and bool((room[off + m * n:] == 7).all()) and bool((ws[-16:] == 255).all())
+    assert torch.equal(y, mxfp4.matmul(mxfp4.quantize(x), qw, dtype))

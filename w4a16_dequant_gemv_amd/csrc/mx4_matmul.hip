@@ -519,13 +519,13 @@ struct TileCost {
     double start, alone, full;       // us: a tile's beginning and end; a stage with few and with all CUs busy
 };
 
-// Measured at 750 sizes: 17 to 4096 rows of x, n_out from 300 to 28672, k from 512 to 28672.  What these costs choose takes
+// Measured at 790 sizes: 17 to 4096 rows of x, n_out from 39 to 28672, k from 32 to 28672.  What these costs choose takes
 // 0.7 % longer than the fastest of all, 26 % at most.  (us, the tiles below in order: 64 x 8192 x 8192 12.5, 15.3,
 // 18.2, 26.9, 37.3, 42.3; 512 x 11008 x 4096 28.6, 22.6, 23.0, 19.7, 22.2, 25.8; 2048 x 11008 x 4096 94.8, 70.8, 67.0, 57.6, 53.0, 58.4;
 // 8192^3 497, 398, 358, 306, 271, 244.)
 constexpr TileCost kTiles[] = {
-    {{1, 1, 4, 1}, 512, 3.3, 0.26, 0.53}, {{2, 1, 3, 1}, 512, 3.3, 0.31, 0.79}, {{2, 2, 3, 1}, 256, 3.3, 0.38, 0.66},
-    {{2, 2, 2, 1}, 512, 2.9, 0.59, 1.30}, {{3, 4, 2, 1}, 256, 5.4, 1.00, 1.60}, {{4, 4, 2, 1}, 256, 7.0, 1.20, 2.00},
+    {{1, 1, 4, 1}, 512, 3.3, 0.25, 0.55}, {{2, 1, 3, 1}, 512, 3.3, 0.28, 1.10}, {{2, 2, 3, 1}, 256, 3.3, 0.46, 0.69},
+    {{2, 2, 2, 1}, 512, 3.0, 0.66, 1.30}, {{3, 4, 2, 1}, 256, 5.1, 1.30, 1.70}, {{4, 4, 2, 1}, 256, 7.1, 1.40, 2.00},
 };
 
 Plan plan_for(int64_t m, int64_t n_out, int64_t k)
@@ -555,8 +555,8 @@ Plan plan_for(int64_t m, int64_t n_out, int64_t k)
     for (const int splits : {2, 3, 4, 6, 8, 12, 16}) {
         if (tiles * splits > 512 || splits > stages) break;
         const double part = (double)(tiles * splits) / 512;
-        const double one = 3.3 + (double)((stages + splits - 1) / splits) * (0.26 + 0.27 * part * part);
-        const double cost = std::max(one, memory) + 1.8 + 0.1 * splits + 5.3 * part;
+        const double one = 3.3 + (double)((stages + splits - 1) / splits) * (0.25 + 0.30 * part * part);
+        const double cost = std::max(one, memory) + 1.7 + 0.13 * splits + 4.3 * part;
         if (cost < least) {
             least = cost;
             best = {1, 1, 4, splits};
