@@ -3,7 +3,7 @@ values that they stand for, and products with the error that a kernel may have."
 import numpy as np
 
 # Sizes (m, n_out, k) that between them are run by every kernel of the product.
-KERNELS = [(1, 40, 288), (5, 100, 4096), (16, 256, 8192), (20, 130, 512), (20, 100, 2048), (70, 500, 800), (700, 3000, 544),
+KERNELS = [(1, 40, 288), (1, 100, 8160), (5, 100, 4096), (3, 40, 10016), (16, 256, 8192), (20, 130, 512), (20, 100, 2048), (70, 500, 800), (700, 3000, 544),
            (1000, 4001, 2080), (1111, 6000, 544), (2000, 6001, 544), (2050, 5003, 1056), (2000, 8101, 800), (40, 302, 8000), (100, 70, 28640),
            (64, 4096, 11008)]
 

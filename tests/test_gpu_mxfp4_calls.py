@@ -11,7 +11,7 @@ from w4a16_dequant_gemv_amd import W4A16Error, mxfp4
 pytestmark = pytest.mark.gpu
 
 # (m, n_out, k): every kernel of the product, rows that end inside a stage and rows that do not
-SIZES = [(1, 40, 288), (5, 100, 4096), (20, 130, 512), (70, 500, 800), (700, 3000, 544), (1000, 4001, 2080), (2000, 6001, 544),
+SIZES = [(1, 40, 288), (5, 100, 4096), (1, 100, 8160), (7, 90, 10016), (20, 130, 512), (70, 500, 800), (700, 3000, 544), (1000, 4001, 2080), (2000, 6001, 544),
          (2050, 5003, 1056), (2000, 8101, 800), (40, 302, 8000), (100, 71, 28640)]
 
 

@@ -101,12 +101,12 @@ def test_workspace_size(L):
 def test_config_reports_every_kernel(L):
     """Each kernel that the rules can choose, at sizes that the GPU tests run."""
     names = {mxfp4.kernel_config(m, n, k, linear=linear) for m, n, k in KERNELS for linear in (True, False)}
-    for want in ("mx4_rows_kernel<0, 1, 0>", "mx4_quantize_kernel<0>, mx4_rows_kernel<0, 1, -1>", "mx4_rows_kernel<0, 2, -1>",
-                 "mx4_rows_kernel<0, 2, 0>", "mx4_tile_kernel<0, 1, 1, 4, false>", "mx4_tile_kernel<0, 2, 1, 3, false>",
+    for want in ("mx4_rows_kernel<0, 1, 0, 2>", "mx4_rows_kernel<0, 1, 0, 4>", "mx4_quantize_kernel<0>, mx4_rows_kernel<0, 1, -1, 2>",
+                 "mx4_quantize_kernel<0>, mx4_rows_kernel<0, 1, -1, 4>", "mx4_rows_kernel<0, 2, -1, 2>", "mx4_rows_kernel<0, 2, 0, 2>", "mx4_tile_kernel<0, 1, 1, 4, false>", "mx4_tile_kernel<0, 2, 1, 3, false>",
                  "mx4_tile_kernel<0, 2, 2, 3, false>", "mx4_tile_kernel<0, 2, 2, 2, false>", "mx4_tile_kernel<0, 3, 4, 2, false>",
                  "mx4_tile_kernel<0, 4, 4, 2, false>", "mx4_tile_kernel<0, 1, 1, 4, true>, mx4_join_kernel<0>"):
         assert want in names, want
-    assert mxfp4.kernel_config(1, 64, 64, torch.bfloat16) == "mx4_rows_kernel<1, 1, 1>"
+    assert mxfp4.kernel_config(1, 64, 64, torch.bfloat16) == "mx4_rows_kernel<1, 1, 1, 2>"
     buf = __import__("ctypes").create_string_buffer(8)
     assert L.mx4_linear_config(1, 64, 64, 0, 1, None, 8) == Q4_ERR_NULL
     for bad in ((0, 64, 64, 0), (1, 64, 48, 0), (1, 64, 64, 2), (1, 1 << 25, 64, 0)):

@@ -16,13 +16,13 @@ namespace {
 constexpr int kRowWaves = 8;
 
 // Few rows of x: a workgroup has 16 rows of W and all of x, its waves take steps of 256
-// elements in turn and are summed at the end.  W goes from memory to operand registers, two
+// elements in turn and are summed at the end.  W goes from memory to operand registers, U
 // steps ahead; x lies in LDS, `chunk` steps of it at a time, and comes there as codes or, with
 // X the type of its elements, is quantized on the way.  What lies behind a row's last block
 // is zero in x and so does not matter in W.  The 16 x 16 x 128 form: half as much padding with few rows of x
 // as the 32 x 32 one.  Replayed with W from the Infinity Cache or HBM, 1 x 4096 x 4096 takes 4.2 us, of which a launch and
-// the first loads are 2.9, 1 x 8192 x 8192 9.7 (3.7 TB/s), 8 x 8192 x 28672 28.5 (4.4 TB/s).
-template <int TYPE, int MT, int X>
+// the first loads are 2.9, 1 x 8192 x 8192 8.2 (4.3 TB/s), 1 x 28672 x 8192 23.7 (5.3 TB/s), 8 x 8192 x 28672 28.0 (4.5 TB/s).
+template <int TYPE, int MT, int X, int U>
 __global__ __launch_bounds__(64 * kRowWaves, 4) void mx4_rows_kernel(const void *__restrict__ x, const uint8_t *__restrict__ xs,
                                                            int64_t stride, const uint8_t *__restrict__ wc,
                                                            const uint8_t *__restrict__ ws, int m, int n_out, int k,
@@ -37,7 +37,6 @@ __global__ __launch_bounds__(64 * kRowWaves, 4) void mx4_rows_kernel(const void 
     const uint8_t *wrow = wc + (int64_t)wr * pitch, *wscale = ws + (int64_t)wr * 8 + 2 * g;
     char *xscale = smem + chunk * m * 128;
 
-    constexpr int U = 2;
     u32x4 a[U][2];
     uint32_t sa[U];
     auto load = [&](int s, int u) {
@@ -489,15 +488,15 @@ hipError_t launch_parts(const uint8_t *xc, const uint8_t *xs, const uint8_t *wc,
     return hipGetLastError();
 }
 
-template <int TYPE, int MT, int X>
-hipError_t launch_rows(const void *x, const uint8_t *xs, int64_t stride, const uint8_t *wc, const uint8_t *ws, int m,
+template <int TYPE, int MT, int X, int U>
+hipError_t launch_rows_ahead(const void *x, const uint8_t *xs, int64_t stride, const uint8_t *wc, const uint8_t *ws, int m,
                        int n_out, int k, uint16_t *y, hipStream_t stream)
 {
-    constexpr int NW = kRowWaves, ROUND = 2 * NW;                                        // steps of one round of the waves
+    constexpr int NW = kRowWaves, ROUND = U * NW;                                        // steps of one round of the waves
     const int steps = (k + 255) / 256, most = std::max(1, 80 * 1024 / (m * 136) / ROUND) * ROUND;
     const int chunk = std::min(most, steps);
     const int lds = std::max(chunk * m * 136, NW * MT * 1024);
-    auto kernel = mx4_rows_kernel<TYPE, MT, X>;
+    auto kernel = mx4_rows_kernel<TYPE, MT, X, U>;
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, lds);
@@ -505,6 +504,20 @@ hipError_t launch_rows(const void *x, const uint8_t *xs, int64_t stride, const u
     }
     kernel<<<(unsigned)((n_out + 15) / 16), 64 * NW, lds, stream>>>(x, xs, stride, wc, ws, m, n_out, k, chunk, y);
     return hipGetLastError();
+}
+
+// Steps of W that a wave has on their way: four where it has that many (us with two and with four: 1 x 8192 x 8192 9.7 and 8.2,
+// 16 x 8192 x 8192 12.7 and 11.3, 1 x 28672 x 8192 27.6 and 23.7; but 1 x 28672 x 4096 14.7 and 16.9), and at most 16 rows, with
+// which x is in LDS in one piece or two.
+int rows_ahead(int64_t m, int64_t k) { return m <= 16 && (k + 255) / 256 >= 4 * kRowWaves ? 4 : 2; }
+
+template <int TYPE, int X>
+hipError_t launch_rows(const void *x, const uint8_t *xs, int64_t stride, const uint8_t *wc, const uint8_t *ws, int m,
+                       int n_out, int k, uint16_t *y, hipStream_t stream)
+{
+    if (m > 16) return launch_rows_ahead<TYPE, 2, X, 2>(x, xs, stride, wc, ws, m, n_out, k, y, stream);
+    return rows_ahead(m, k) == 4 ? launch_rows_ahead<TYPE, 1, X, 4>(x, xs, stride, wc, ws, m, n_out, k, y, stream)
+                                 : launch_rows_ahead<TYPE, 1, X, 2>(x, xs, stride, wc, ws, m, n_out, k, y, stream);
 }
 
 // How a product is run: by mx4_rows_kernel (tm == 0; at most 32 rows of x), or by tiles of 64 tm x 64 tn
@@ -568,14 +581,19 @@ Plan plan_for(int64_t m, int64_t n_out, int64_t k)
         const double groups = (double)((n_out + 15) / 16), rounds = std::max(1.0, groups / 512);
         const double slope = (0.065 + 0.0043 * (double)m) * (1.0 + 1.3 * std::min(1.0, groups / 512));
         const double cost = 2.5 + steps * slope * rounds + 0.8 * (rounds - 1.0);
-        if (std::max(cost, memory) < least) best = {0, 0, 0, 1};
+        const double stream = rows_ahead(m, k) == 4 ? 0.87 * memory : memory;
+        if (std::max(cost, stream) < least) best = {0, 0, 0, 1};
     }
     return best;
 }
 
 // x is quantized by the product's own workgroups where that costs less than a launch of its own (2 us): each does it for
-// itself (1 x 8192 x 8192 10.9 us, 12.4 in two launches; 4 x 4096 x 4096 6.0 and 6.4; 8 x 4096 x 4096 8.0 and 6.8).
-bool quantizes_itself(const Plan &p, int64_t m, int64_t k) { return p.tm == 0 && m * k <= 16384; }
+// itself, 2.2 us for 16384 elements, and 512 at a time (1 x 8192 x 8192 9.2 us, 10.1 in two launches; 4 x 4096 x 4096 6.0 and
+// 6.4; 8 x 4096 x 4096 8.0 and 6.8; 1 x 28672 x 8192 28.0 and 25.5).
+bool quantizes_itself(const Plan &p, int64_t m, int64_t n_out, int64_t k)
+{
+    return p.tm == 0 && (double)(m * k) * std::max(1.0, (double)((n_out + 15) / 16) / 512) <= 16384;
+}
 
 // Bytes of the parts' sums.
 int64_t part_bytes(const Plan &p, int64_t m, int64_t n_out)
@@ -588,9 +606,7 @@ hipError_t launch(const Plan &p, const uint8_t *xc, const uint8_t *xs, const uin
                   int n_out, int k, void *parts, uint16_t *y, hipStream_t stream)
 {
     if (p.splits > 1) return launch_parts<TYPE>(xc, xs, wc, ws, m, n_out, k, p.splits, (f32x4 *)parts, y, stream);
-    if (p.tm == 0)
-        return m <= 16 ? launch_rows<TYPE, 1, -1>(xc, xs, 0, wc, ws, m, n_out, k, y, stream)
-                       : launch_rows<TYPE, 2, -1>(xc, xs, 0, wc, ws, m, n_out, k, y, stream);
+    if (p.tm == 0) return launch_rows<TYPE, -1>(xc, xs, 0, wc, ws, m, n_out, k, y, stream);
     switch (p.tm * 100 + p.tn * 10 + p.nb) {
     case 114: return launch_tiles<TYPE, 1, 1, 4>(xc, xs, wc, ws, m, n_out, k, y, stream);
     case 213: return launch_tiles<TYPE, 2, 1, 3>(xc, xs, wc, ws, m, n_out, k, y, stream);
@@ -607,9 +623,8 @@ hipError_t launch_linear(const void *x, int64_t stride, const uint8_t *wc, const
                          uint8_t *codes, uint8_t *scales, void *parts, uint16_t *y, hipStream_t stream)
 {
     const Plan p = plan_for(m, n_out, k);
-    if (quantizes_itself(p, m, k))
-        return m <= 16 ? launch_rows<TYPE, 1, TYPE>(x, nullptr, stride, wc, ws, m, n_out, k, y, stream)
-                       : launch_rows<TYPE, 2, TYPE>(x, nullptr, stride, wc, ws, m, n_out, k, y, stream);
+    if (quantizes_itself(p, m, n_out, k))
+        return launch_rows<TYPE, TYPE>(x, nullptr, stride, wc, ws, m, n_out, k, y, stream);
     const hipError_t e = mx4_launch_quantize(x, TYPE, m, k, stride, codes, scales, stream);
     return e != hipSuccess ? e : launch<TYPE>(p, codes, scales, wc, ws, m, n_out, k, parts, y, stream);
 }
@@ -633,16 +648,16 @@ hipError_t mx4_launch_linear(const void *x, int type, int64_t stride, const uint
 Mx4Room mx4_room(int64_t m, int64_t n_out, int64_t k)
 {
     const Plan p = plan_for(m, n_out, k);
-    return {!quantizes_itself(p, m, k), part_bytes(p, m, n_out)};
+    return {!quantizes_itself(p, m, n_out, k), part_bytes(p, m, n_out)};
 }
 
 void mx4_linear_name(int64_t m, int64_t n_out, int64_t k, int type, bool linear, char *name, int64_t name_len)
 {
     const Plan p = plan_for(m, n_out, k);
-    const bool self = linear && quantizes_itself(p, m, k);
+    const bool self = linear && quantizes_itself(p, m, n_out, k);
     const char *first = "";
     if (linear && !self) first = type == MX4_F16 ? "mx4_quantize_kernel<0>, " : "mx4_quantize_kernel<1>, ";
-    if (p.tm == 0) snprintf(name, (size_t)name_len, "%smx4_rows_kernel<%d, %d, %d>", first, type, m <= 16 ? 1 : 2, self ? type : -1);
+    if (p.tm == 0) snprintf(name, (size_t)name_len, "%smx4_rows_kernel<%d, %d, %d, %d>", first, type, m <= 16 ? 1 : 2, self ? type : -1, rows_ahead(m, k));
     else if (p.splits > 1) snprintf(name, (size_t)name_len, "%smx4_tile_kernel<%d, 1, 1, 4, true>, mx4_join_kernel<%d>", first, type, type);
     else snprintf(name, (size_t)name_len, "%smx4_tile_kernel<%d, %d, %d, %d, false>", first, type, p.tm, p.tn, p.nb);
 }
