@@ -237,10 +237,13 @@ int64_t kv_paged_attention_shared_workspace_size(int64_t tokens, int32_t batch, 
 
 /*
  * kv_paged_attention without a window, with the shared pages read and scored once for each
- * group, all of its rows at a time: the same result but for the order of sums.  Of a group's
- * pages the first min(pages[g], max_pages) are taken together, from the block table of its first
+ * group, all of its rows at a time: the same result but for the order of sums, each weight of the
+ * second product in two fp16 parts (2^-22).  Of a group's pages the first
+ * min(pages[g], max_pages) are taken together, from the block table of its first
  * sequence that has rows and has finished them (ctx_lens[b] / page); a sequence that has not
- * attends to all of its tokens by itself.  How a call is run goes by max_pages for the
+ * attends to all of its tokens by itself.  A call of more than 64 rows a kv head for each
+ * sequence on average (tokens / batch, rounded up, times n_q / n_kv) is run as
+ * kv_paged_attention in all of its sequences.  How others are run goes by max_pages for the
  * shared pages and table_cols - max_pages for the sequences' own tokens.
  */
 int kv_paged_attention_shared(const kv_paged_cache *cache, const kv_paged_batch *batch, const kv_shared_prefix *prefix,

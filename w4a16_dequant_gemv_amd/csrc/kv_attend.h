@@ -547,6 +547,9 @@ __device__ __forceinline__ bool group_rows(const SharedArgs &a, int64_t item, Kv
 // A second part here would be half as much matrix work again: 576 us for 420 above, 120
 // for 103 at d = 256 (2 x 1500 in a window of 1024).  The outputs' error against 64 bits
 // is 2.9e-4 of their size this way and 2.07e-4 that way, their own rounding to fp16.
+// With PARTS, where a sequence may have a single row, the second part is there: a row's weights are then as exact as
+// without shared pages, whichever kernel takes these (a tile 1.9 us for 1.5 with a CU to itself, 3.0 for 2.3 with two
+// workgroups on each, d = 128).
 // A wave's matrix work (a tile's scores, the last one's second product) and its
 // vector work (weights, conversion of tiles) do not overlap by themselves, and
 // waves that meet at barriers do the same at the same time; so with eight waves
@@ -641,7 +644,7 @@ __device__ __forceinline__ void attend_rows(const A &a, int splits, int block, i
         return v_tile + (i & 1) * VF * 64 + ch / 16 * 128 + unit / D * 16 + (ch & 15);
     };
     f32x4 x[QT][4];
-    f16x8 p[QT][2];
+    f16x8 p[QT][2], rest[QT][2];                           // P, and with PARTS what is left of it
     // O += P V of tile i - 1, and the scores of tile i.  Operands are read ahead, and
     // an accumulator comes up again after one or three others.  `between` is run twice, after two
     // pieces of the scores.
@@ -662,12 +665,15 @@ __device__ __forceinline__ void attend_rows(const A &a, int splits, int block, i
             fetch(n + AHEAD);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int one = e & 1, half = e >> 1;                  // operand 2 one + half
+            for (int e = 0; e < (PARTS && n < VP ? 8 : 4); ++e) {
+                const int one = e & 1, half = e >> 1 & 1;              // operand 2 one + half
                 const f16x8 v = f[n % (AHEAD + 1)][2 * one + half];
                 if (n < VP) {
 #pragma unroll
-                    for (int t = 0; t < QT; ++t) o[t][2 * n + one] = mfma(v, p[t][half], o[t][2 * n + one]);
+                    for (int t = 0; t < QT; ++t) {
+                        const f16x8 w = PARTS && e >= 4 ? rest[t][half] : p[t][half];
+                        o[t][2 * n + one] = mfma(v, w, o[t][2 * n + one]);
+                    }
                 } else {
                     const int j = (n - VP) / KS * 2 + one, c = (n - VP) % KS * 2 + half;
                     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -720,8 +726,8 @@ __device__ __forceinline__ void attend_rows(const A &a, int splits, int block, i
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             float sum = 0.0f;
-            weigh_exp(x[t], 0, c1, w - m[t], p[t], sum);
-            weigh_exp(x[t], 1, c1, w - m[t], p[t], sum);
+            weigh_exp(x[t], 0, c1, w - m[t], p[t], sum, PARTS ? rest[t] : nullptr);
+            weigh_exp(x[t], 1, c1, w - m[t], p[t], sum, PARTS ? rest[t] : nullptr);
             l[t] += sum * inv;
         }
     };

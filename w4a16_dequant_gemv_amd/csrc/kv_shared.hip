@@ -8,8 +8,8 @@
 // Both go out as parts in binary32 and are joined by a second launch.  (Joining within the first one would take a wait between
 // workgroups; one workgroup for a row block's shared and own tokens takes them one after the other, and was slower on
 // every size tried for d <= 128.)  Measured, replayed, 64 heads on 8, d = 128, with and without shared pages: 64 sequences
-// with up to 1000 tokens of their own behind 4096 42 and 71 us, 32 with 500 behind 131072 175 and 678 (0.79 PFLOP/s),
-// 64 with 1000 behind 32768 107 and 343; 4 of 32 heads on 32 with 100 behind 512 10.8 and 13.6.
+// with up to 1000 tokens of their own behind 4096 47 and 69 us, 32 with 500 behind 131072 225 and 681,
+// 64 with 1000 behind 32768 131 and 344; 4 of 32 heads on 32 with 100 behind 512 11.0 and 13.7.
 #include "kv_attend.h"
 
 namespace {
@@ -78,9 +78,9 @@ __device__ __forceinline__ void put_rows(const SharedArgs &a, Wave<D, 1> &s, flo
 
 // The parts of the shared pages, 16 rows of a group and kv head a workgroup, and one of `splits` runs
 // of the tiles, which its waves take in turn from memory.  Bound by the chain of a wave's tiles, 0.39 us each at d = 128 and
-// 0.85 with two workgroups on a CU; with many rows attend_rows has 128 of them share a tile by way of LDS, 1.5 and 2.3 us a
-// tile (64 rows: 1.1, no faster in all; 256 rows of eight waves, in a launch of their own: 32 sequences behind 131072 tokens 166 us
-// against 175, all others slower).
+// 0.85 with two workgroups on a CU; with many rows attend_rows has 128 of them share a tile by way of LDS, 1.9 and 3.0 us a
+// tile.  (Tried while weights were one fp16 part there, 1.5 and 2.3 us a tile: 64 rows, 1.1, no faster in all; 256 rows of eight
+// waves, in a launch of their own, 32 sequences behind 131072 tokens 166 us against 175, all others slower.)
 template <int D>
 __device__ __forceinline__ void shared_rows(const SharedArgs &a, float *smem, int block)
 {
@@ -237,9 +237,9 @@ SharedPlan shared_plan(int64_t tokens, int batch, int groups, int n_q, int n_kv,
     p.alone = one > 64;
     if (p.alone) return p;
     // Waves of a row block: more of them end a long sequence sooner, fewer need fewer workgroups, of which the CUs hold
-    // 512 (us with 1, 2 and 4: 64 heads on 8, 16 x 500 tokens behind 8k 34.6, 26.7, 22.9; 64 x 1000 behind 4k 55, 41,
-    // 42.6; 256 x 500 behind 8k 129, 125, 133; 128 x 300 behind four times 1k 32.5, 35.8, 40.7; d = 64, 40 x 5 tokens 28.9,
-    // 27.2, 22.7).
+    // 512 (us with 1, 2 and 4: 64 heads on 8, 16 x 500 tokens behind 8k 37, 27.6, 24.9; 64 x 1000 behind 4k 61.5, 46.4,
+    // 47.3; 256 x 500 behind 8k 159, 153, 162; 128 x 300 behind four times 1k 35.2, 37.3, 42.7; d = 64, 40 x 5 tokens 28.9,
+    // 27.3, 22.1).
     const int64_t blocks = (one + 15) / 16 * batch * n_kv;
     p.share = blocks * d <= 50000 ? 4 : own <= 8 ? 1 : 2;
     p.own = tokens * group / 16 + batch;
@@ -247,9 +247,11 @@ SharedPlan shared_plan(int64_t tokens, int batch, int groups, int n_q, int n_kv,
     p.chunk = (int)((own + p.chunks - 1) / p.chunks);
     // What a choice costs, in us: a start, then the longest run of tiles or, where that is more, all the work shared out to the
     // workgroups that the CUs hold at once, and the parts' way out and back.  A tile of the shared pages takes a workgroup
-    // `alone` us with a CU to itself, `full` with two on each.  (With 1, 2, 4, 6, 8, 16 and 32 runs: 64 sequences behind 4k, 16
-    // rows a workgroup 50, 53, 61, 69, 74, 106, 168, 128 rows 110, 64, 43, 41, 47, 62, 80; 16 of 32 heads on 8 behind 8k 59, 36, 24,
-    // 22, 22, 30, 39 and 198, 105, 60, 45, 38, 30, 29.)
+    // `alone` us with a CU to itself, `full` with two on each.  (With 1, 2, 4, 6, 8, 12 runs: 64 sequences behind 4k, 16
+    // rows a workgroup 51, 53, 60, 68, 75, 95, 128 rows 134, 76, 49, 45, 49, 56; 16 of 32 heads on 8 behind 8k 58, 36, 24,
+    // 22, 22, 23 and 250, 130, 72, 54, 45, 37.)  The 128 rows' constants are below what their tiles take, 1.9 and 3.0 us: what
+    // they choose takes 2.3 % longer than the best choice on average at 38 sizes, 27 % at most, with 1.9 and 3.0 3.1 %, since the
+    // 16 rows' are low too.
     const double size = (double)d / 128;
     const double slots = d <= 128 ? 512 : 256;
     const double own_work = (double)(blocks * p.share) / 4 * (6.0 + 1.1 * size * (double)std::min<int64_t>(own, p.chunk) / p.share);
