@@ -17,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a16.so")
+TEST_LIB = os.path.join(ROOT, "tests", "_build", "libbuffer_range.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -70,6 +71,16 @@ def build(verbose=True):
     if verbose:
         print(f"built {LIB}")
     return LIB
+
+
+def build_test_kernels():
+    """Kernels that only tests launch (tests/*.hip)."""
+    os.makedirs(os.path.dirname(TEST_LIB), exist_ok=True)
+    r = subprocess.run([HIPCC, *COMMON, "-shared", os.path.join(ROOT, "tests", "buffer_range.hip"), "-o", TEST_LIB],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"hipcc failed for buffer_range.hip:\n{r.stderr}")
+    return TEST_LIB
 
 
 def build_host_sanitized(out, build_dir):
