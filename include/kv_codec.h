@@ -228,7 +228,8 @@ int kv_paged_attention_config(int64_t tokens, int32_t batch, int32_t table_cols,
 typedef struct kv_shared_prefix {
     const int32_t *cu_seqs;      /* [groups + 1] */
     const int32_t *pages;        /* [groups] */
-    int32_t groups, max_pages;   /* 1 .. 65536 groups; no group shares more than max_pages (at least 1) */
+    int32_t groups, max_pages;   /* 1 .. 65536 groups, groups * n_kv at most 2^21; no group shares more than max_pages,
+                                    which is in [1, 2^24] */
 } kv_shared_prefix;
 
 /* Workspace bytes of kv_paged_attention_shared; no HIP call is made. */

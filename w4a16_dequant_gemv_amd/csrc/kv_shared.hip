@@ -227,6 +227,15 @@ struct SharedPlan {
     int64_t items, own;          // row blocks of the shared pages and of the own tokens (upper bounds)
 };
 
+constexpr int64_t kMaxBlocks = (int64_t(1) << 32) / kThreads - 1;
+
+// Workgroups of a chunk of the own tokens.
+int64_t own_blocks(const SharedPlan &p, int n_kv)
+{
+    const int64_t each = kWaves / p.share;
+    return (p.own * n_kv + each - 1) / each;
+}
+
 // Groups share at most `tiles` tiles; sequences have at most `own` tiles besides.
 SharedPlan shared_plan(int64_t tokens, int batch, int groups, int n_q, int n_kv, int d, int64_t tiles, int64_t own)
 {
@@ -277,6 +286,13 @@ SharedPlan shared_plan(int64_t tokens, int batch, int groups, int n_q, int n_kv,
     offer(16, 8.0, 0.1 + 0.29 * size, 0.1 + 0.75 * size);
     if (d <= 128) offer(128, 10.0, 1.48, 2.3);
     else offer(128, 16.0, 2.6, 2.6);
+    // A launch has less than 2^32 threads: so many row blocks take their own tokens in fewer chunks.  (One always has room:
+    // batch n_kv is at most 2^21 and rows n_kv 64 times that.)
+    const int64_t most = (kMaxBlocks - p.items * n_kv * p.splits) / own_blocks(p, n_kv);
+    if (p.chunks > most) {
+        p.chunks = (int)std::max<int64_t>(most, 1);
+        p.chunk = (int)((own + p.chunks - 1) / p.chunks);
+    }
     return p;
 }
 
@@ -304,7 +320,7 @@ hipError_t launch_kernel(const SharedArgs &a, const SharedPlan &p, int64_t first
     constexpr int OCC = D <= 128 ? 2 : 1, LDS = MANY ? std::max(rows_lds(D), joint_lds(D)) : joint_lds(D);
     auto kernel = kv_shared_kernel<D, MANY, OCC>;
     if (hipError_t e = allow_lds(kernel, LDS)) return e;
-    const int64_t each = kWaves / p.share, per_chunk = (p.own * a.cache.n_kv + each - 1) / each;
+    const int64_t per_chunk = own_blocks(p, a.cache.n_kv);
     kernel<<<(unsigned)(first + per_chunk * p.chunks), kThreads, LDS, to.stream>>>(a, (int)first, (int)per_chunk, p.share);
     return hipGetLastError();
 }
@@ -336,7 +352,7 @@ hipError_t launch(const SharedArgs &a, const SharedPlan &p, const Target &to)
     if (e != hipSuccess) return e;
     constexpr int SIDE = kThreads / (D / 4);
     const int64_t rows = (a.batch.tokens + a.batch.batch - 1) / a.batch.batch * a.n_q;       // of a sequence on average
-    const int per = (int)((rows + SIDE - 1) / SIDE);
+    const int per = (int)std::min((rows + SIDE - 1) / SIDE, kMaxBlocks / a.batch.batch);
     kv_shared_join_kernel<D><<<(unsigned)per * (unsigned)a.batch.batch, kThreads, 0, to.stream>>>(a, per);
     return hipGetLastError();
 }

@@ -415,7 +415,9 @@ class PagedKVCache(_Kept):
         `window` of them and the sequence's first `sinks`.  scale defaults to
         d^-1/2.  Rows of no sequence are left as they were.  With `prefix` (a
         SharedPrefix; no window) the pages that a group of sequences share are read and
-        scored once for all of its rows: the same result but for the order of sums."""
+        scored once for all of its rows: the same result but for the order of sums.  Calls of
+        more than 64 rows a kv head for each sequence on average are run as without one, so
+        a long chunk of a prompt is better called apart from the others' single tokens."""
         c, dev, gpu = self._checked()
         qs = _heads(q, None, self.d, "q", dev)
         T, n_q = q.shape[:2]
